@@ -38,6 +38,15 @@ SIGNATURES = {
     "hadamard_rotate_quant_fp8_qkv": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "rope_cos_sin_table": (_I, [_P, _I, _I, _D, _P]),
     "rope_hadamard_rotate_quant_fp8": (_I, [_P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "rope_scaled_table": (_I, [_P, _I, _I, _D, _I, _D, _D, _P]),
+    "rope_apply": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _LL, _LL, _I, _I, _I, _I, _P]),
+    "kv_cache_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _LL, _LL, _I, _I, _I, _I, _P]),
+    "rope_kv_cache_append": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _LL, _LL, _LL, _I, _I,
+                                  _I, _I, _I, _I, _I, _P]),
+    "kv_cache_gather": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "attn_decode_paged_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "attn_decode_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _I, _I, _I, _I,
+                               _I, _I, _F, _P]),
     "attn_get_last_error": (ctypes.c_char_p, []),
     "attn_check": (_I, [_P]),
     "attn_set_spin_limit": (None, [_LL]),

@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "attn46.h"
+#include "cache.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -956,8 +957,15 @@ int attn_check(void* stream) {
     e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "error word reset: %s", cudaGetErrorString(e));
     if (host[0] == ATTN_ERR_INVALID_ARG)
-      return fail(host[0], "a kernel rejected its device-side input (site %d: cu_seqlens must run from 0 to "
-                  "total, non-decreasing, no sequence longer than max_seqlen)", host[1]);
+      return fail(host[0], "a kernel rejected its device-side input (site %d: %s)", host[1],
+                  host[1] == 41   ? "a rotary position lies outside the table; its token was not written"
+                  : host[1] == 42 ? "a slot lies past the cache; its token was not written"
+                  : host[1] == 43 ? "a token lies in no sequence or page of the cache; it was not written"
+                  : host[1] == 53 ? "a context or query length is negative or longer than the page table; nothing "
+                                    "was written"
+                  : host[1] == 54 ? "a page number lies outside the cache; its sequence's outputs are undefined"
+                                  : "cu_seqlens must run from 0 to total, non-decreasing, no sequence longer than "
+                                    "max_seqlen");
     return fail(host[0], "a kernel's bounded wait ran out (code %d, site %d)", host[0], host[1]);
   }
   return ok();
@@ -1018,3 +1026,42 @@ int attn_fwd_split(const void* q, const void* k, const void* v, const float* q_s
 }
 
 }  // extern "C"
+
+// What the paged cache's entry points (api_cache.cu) share with the ones above.
+namespace ea46 {
+
+int api_fail(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+int api_ok() { return ok(); }
+int api_err_words(int** out) { return err_words(out); }
+long long api_spin_limit() { return spin_limit(); }
+bool api_aligned16(const void* p) { return aligned16(p); }
+bool api_overlap(const void* a, size_t na, const void* b, size_t nb) { return overlap(a, na, b, nb); }
+
+// The cache as (D, offset, head, page) with a box of one swizzle panel x min(page_size, 128) rows.
+int api_make_cache_map(CUtensorMap* m, const CacheView& c, const void* ptr, int D, bool fp8) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const int esz = fp8 ? 1 : 2, row_bytes = D * esz, panel_row = row_bytes >= 128 ? 128 : row_bytes;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(c.n_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.tok_stride) * esz, static_cast<cuuint64_t>(c.head_stride) * esz,
+                                 static_cast<cuuint64_t>(c.page_stride) * esz};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(panel_row / esz),
+                             static_cast<cuuint32_t>(c.page_size < 128 ? c.page_size : 128), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                         const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         panel_row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         l2_promotion(row_bytes), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache (%d)", int(r));
+  return ATTN_OK;
+}
+
+}  // namespace ea46

@@ -10,6 +10,7 @@
 // per-step path.
 #include <cuda_runtime.h>
 
+#include "cache.h"
 #include "internal.h"
 
 namespace ea46 {
@@ -27,7 +28,42 @@ __global__ void rope_table_kernel(float2* cs, long long n, int D, double base) {
   cs[idx] = make_float2(__double2float_rn(c), __double2float_rn(s));
 }
 
+// The table for a context stretched by `factor`, theta_i in fp64:
+//   linear  position interpolation: theta_i / factor;
+//   ntk     base * factor^(rot / (rot - 2)) in place of base;
+//   yarn    by parts (Peng et al. 2023, "YaRN", section 3.2-3.3): a pair that makes more than 32
+//           turns within the original length keeps theta_i, one that makes fewer than 1 takes
+//           theta_i / factor, in between linear in the number of turns; cos and sin times
+//           0.1 ln(factor) + 1.
+__global__ void rope_scaled_table_kernel(float2* cs, long long n, int rot, double base, int scaling, double factor,
+                                         double original_length) {
+  const long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (idx >= n) return;
+  const long long p = idx / (rot / 2);
+  const int i = static_cast<int>(idx % (rot / 2));
+  if (scaling == ROPE_NTK) base *= pow(factor, static_cast<double>(rot) / (rot - 2));
+  double theta = pow(base, -2.0 * i / rot), gain = 1.0;
+  if (scaling == ROPE_LINEAR) theta /= factor;
+  if (scaling == ROPE_YARN) {
+    const double turns = original_length * theta / 6.283185307179586476925;
+    const double keep = fmin(1.0, fmax(0.0, (turns - 1.0) / 31.0));
+    theta = (1.0 - keep) * theta / factor + keep * theta;
+    gain = 0.1 * log(factor) + 1.0;
+  }
+  double s, c;
+  sincos(static_cast<double>(p) * theta, &s, &c);
+  cs[idx] = make_float2(__double2float_rn(c * gain), __double2float_rn(s * gain));
+}
+
 }  // namespace
+
+cudaError_t launch_rope_scaled_table(float* cs, int n_pos, int rot, double base, int scaling, double factor,
+                                     double original_length, cudaStream_t stream) {
+  const long long n = static_cast<long long>(n_pos) * (rot / 2);
+  rope_scaled_table_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, stream>>>(
+      reinterpret_cast<float2*>(cs), n, rot, base, scaling, factor, original_length);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_rope_table(float* cs, int n_pos, int D, double base, cudaStream_t stream) {
   const long long n = static_cast<long long>(n_pos) * (D / 2);

@@ -17,7 +17,9 @@ __all__ = ["attn_fwd", "attn_fwd_fp8", "attn_fwd_varlen", "attn_fwd_varlen_fp8",
            "hadamard_rotate_quant_fp8_varlen", "rope_cos_sin_table", "rope_hadamard_rotate_quant_fp8",
            "rope_hadamard_rotate_quant_fp8_varlen", "varlen_scale_blocks", "block_count", "check",
            "set_spin_limit", "set_key_split", "key_split_plan", "attn_fwd_split", "split_workspace_bytes",
-           "selftest_bounded_wait", "ATTN_BF16", "ATTN_FP8_E4M3"]
+           "selftest_bounded_wait", "ATTN_BF16", "ATTN_FP8_E4M3", "rope_scaled_table", "rope_apply",
+           "kv_cache_append", "rope_kv_cache_append", "kv_cache_gather", "attn_decode_paged",
+           "decode_paged_workspace_bytes"]
 
 ATTN_BF16 = 0
 ATTN_FP8_E4M3 = 1
@@ -27,6 +29,8 @@ _BF16 = (torch.bfloat16,)
 _CODES = (torch.uint8,) + ((torch.float8_e4m3fn,) if hasattr(torch, "float8_e4m3fn") else ())
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
+_I64 = (torch.int64,)
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 def block_count(S):
@@ -507,3 +511,215 @@ def attn_fwd_split(q, k, v, q_scale=None, k_scale=None, v_scale=None, causal=Fal
 
 def selftest_bounded_wait(cycles, stream=None):
     _lib.call("attn_selftest_bounded_wait", int(cycles), _stream(stream))
+
+
+# ---- rotary positions and the paged key/value cache ----
+# The calls below run on their tensors' device, whichever is current; what they allocate for a
+# given stream is allocated for that stream.
+
+def _run(dev, stream, name, *args):
+    """Call `name` with the stream appended, with `dev` current."""
+    if dev.index == torch.cuda.current_device():
+        return _lib.call(name, *args, _stream(stream))
+    with torch.cuda.device(dev):
+        return _lib.call(name, *args, _stream(stream))
+
+
+def _new(shape, dtype, dev, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _rows(t, name, heads=None, D=None, device=None):
+    """Check rows of heads ([tokens, heads, D], or [B, S, heads, D]): bf16 on a CUDA device, heads and
+    D contiguous, tokens evenly spaced (a view of a fused projection).  Returns (tokens, stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in _BF16:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {_BF16[0]}")
+    sh, st = t.shape, t.stride()
+    n = len(sh)
+    if n not in (3, 4):
+        raise ValueError(f"{name}: expected 3 or 4 dimensions, got shape {tuple(sh)}")
+    if (heads is not None and sh[-2] != heads) or (D is not None and sh[-1] != D):
+        raise ValueError(f"{name}: expected {heads} heads of {D}, got shape {tuple(sh)}")
+    if (st[-1] != 1 and sh[-1] > 1) or (st[-2] != sh[-1] and sh[-2] > 1):
+        raise ValueError(f"{name}: heads must be contiguous within a token")
+    if n == 4 and sh[0] > 1 and sh[1] > 1 and st[0] != sh[1] * st[1]:
+        raise ValueError(f"{name}: tokens must be evenly spaced")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
+    tokens = sh[0] if n == 3 else sh[0] * sh[1]
+    if tokens <= 1:
+        return tokens, sh[-2] * sh[-1]
+    return tokens, (st[-3] if sh[-3] > 1 else st[0])
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev):
+    """Check a paged cache; returns (n_pages, page_size, Hkv, D, layout, dtype)."""
+    _arg(k_cache, "k_cache", _BF16 + _CODES, dim=4, device=dev)
+    _arg(v_cache, "v_cache", (k_cache.dtype,), shape=k_cache.shape, device=dev)
+    n_pages, a, b, D = k_cache.shape
+    page, Hkv = (a, b) if token_major else (b, a)
+    if k_cache.element_size() == 1:
+        _arg(k_scale, "k_scale", _F32, shape=(n_pages, Hkv, page), device=dev)
+        _arg(v_scale, "v_scale", _F32, shape=(n_pages, Hkv, page), device=dev)
+        return n_pages, page, Hkv, D, int(bool(token_major)), ATTN_FP8_E4M3
+    if k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale go with an E4M3 cache")
+    return n_pages, page, Hkv, D, int(bool(token_major)), ATTN_BF16
+
+
+def _table_rot(rope_cs, dev):
+    _arg(rope_cs, "rope_cs", _F32, dim=3, device=dev)
+    if rope_cs.shape[2] != 2:
+        raise ValueError(f"rope_cs: expected shape (n_pos, rot_dim / 2, 2), got {tuple(rope_cs.shape)}")
+    return int(rope_cs.shape[0]), 2 * int(rope_cs.shape[1])
+
+
+def rope_scaled_table(n_pos, rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=0, device="cuda",
+                      out=None, stream=None):
+    """Rotary table fp32 [n_pos, rot_dim/2, 2] for a context stretched by ``factor``: ``scaling`` "none",
+    "linear" (position interpolation), "ntk" (larger base) or "yarn" (by parts around
+    ``original_length``, with its multiplier on cos and sin).  Built on the GPU in fp64."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALING)}, got {scaling!r}")
+    _opt(out, "out", _F32, shape=(n_pos, rot_dim // 2, 2))
+    if out is None:
+        out = _new((n_pos, rot_dim // 2, 2), torch.float32, torch.device(device), stream)
+    _run(out.device, stream, "rope_scaled_table", _ptr(out), int(n_pos), int(rot_dim), float(base),
+         ROPE_SCALING[scaling], float(factor), float(original_length))
+    return out
+
+
+def rope_apply(x, rope_cs, positions=None, half=False, transpose=False, out=None, stream=None):
+    """Rotary positions of x, bf16 [tokens, H, D] or [B, S, H, D] (evenly spaced tokens), by the table
+    ``rope_cs`` [n_pos, rot_dim/2, 2]; elements past rot_dim are copied.  ``positions``: int32 of x's
+    token shape (None: 0, 1, .. along the token axis).  ``half``: pairs (i, i + rot_dim/2) instead of
+    (2i, 2i+1).  ``transpose``: the gradient with respect to x of an output gradient x.  ``out``: may
+    be x itself."""
+    tokens, stride = _rows(x, "x")
+    dev = x.device
+    H, D = x.shape[-2:]
+    n_pos, rot = _table_rot(rope_cs, dev)
+    _opt(positions, "positions", _I32, shape=x.shape[:-2], device=dev)
+    if out is None:
+        out = _new(x.shape, torch.bfloat16, dev, stream)
+        out_stride = H * D
+    else:
+        if tuple(out.shape) != tuple(x.shape):
+            raise ValueError(f"out: expected shape {tuple(x.shape)}, got {tuple(out.shape)}")
+        _, out_stride = _rows(out, "out", device=dev)
+    _run(dev, stream, "rope_apply", _ptr(x), _ptr(out), _ptr(rope_cs), _ptr(positions), tokens, x.shape[-3], H, D,
+         stride, out_stride, n_pos, rot, int(bool(half)), int(bool(transpose)))
+    return out
+
+
+def kv_cache_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, token_major=False, stream=None):
+    """Write k, v (bf16 [tokens, Hkv, D], evenly spaced tokens) to rows ``slots`` (int64 [tokens],
+    page * page_size + offset; negative: padded, not written; otherwise distinct) of a paged cache
+    [n_pages, Hkv, page_size, D] (``token_major``: [n_pages, page_size, Hkv, D]), bf16 or E4M3 with one
+    scale per row (fp32 [n_pages, Hkv, page_size])."""
+    tokens, ks = _rows(k, "k")
+    dev = k.device
+    n_pages, page, Hkv, D, layout, dtype = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    _rows(k, "k", Hkv, D)
+    tv, vs = _rows(v, "v", Hkv, D, dev)
+    if tv != tokens:
+        raise ValueError(f"k holds {tokens} tokens, v {tv}")
+    _arg(slots, "slots", _I64, shape=(tokens,), device=dev)
+    _run(dev, stream, "kv_cache_append", _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+         _ptr(slots), tokens, Hkv, D, ks, vs, n_pages, page, layout, dtype)
+
+
+def rope_kv_cache_append(q, k, v, rope_cs, positions, k_cache, v_cache, slots, k_scale=None, v_scale=None, half=False,
+                         token_major=False, q_out=None, stream=None):
+    """``rope_apply`` on q [tokens, Hq, D] and k, then ``kv_cache_append`` of k and v, in one launch.
+    ``positions``: int32 [tokens].  Returns the rotated q."""
+    tokens, qs = _rows(q, "q")
+    dev = q.device
+    n_pages, page, Hkv, D, layout, dtype = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    Hq = q.shape[-2]
+    _rows(q, "q", Hq, D)
+    tk, ks = _rows(k, "k", Hkv, D, dev)
+    tv, vs = _rows(v, "v", Hkv, D, dev)
+    if not tokens == tk == tv:
+        raise ValueError(f"q, k and v hold {tokens}, {tk} and {tv} tokens")
+    n_pos, rot = _table_rot(rope_cs, dev)
+    _arg(positions, "positions", _I32, shape=(tokens,), device=dev)
+    _arg(slots, "slots", _I64, shape=(tokens,), device=dev)
+    _opt(q_out, "q_out", _BF16, shape=q.shape, device=dev)
+    if q_out is None:
+        q_out = _new(q.shape, torch.bfloat16, dev, stream)
+    _run(dev, stream, "rope_kv_cache_append", _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(rope_cs), _ptr(positions),
+         _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(slots), tokens, Hq, Hkv, D, qs, ks, vs,
+         n_pages, page, layout, dtype, n_pos, rot, int(bool(half)))
+    return q_out
+
+
+def kv_cache_gather(k_cache, v_cache, page_table, cu_seqlens, total, k_scale=None, v_scale=None, token_major=False,
+                    k_out=None, v_out=None, stream=None):
+    """Packed bf16 keys and values [total, Hkv, D] of sequences in a paged cache: ``page_table`` int32
+    [n_seq, max_pages], ``cu_seqlens`` int32 [n_seq + 1] (0 .. total)."""
+    dev = _arg(k_cache, "k_cache", _BF16 + _CODES, dim=4).device
+    n_pages, page, Hkv, D, layout, dtype = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    _arg(page_table, "page_table", _I32, dim=2, device=dev)
+    n_seq, max_pages = page_table.shape
+    _arg(cu_seqlens, "cu_seqlens", _I32, shape=(n_seq + 1,), device=dev)
+    total = int(total)
+    for n, t in (("k_out", k_out), ("v_out", v_out)):
+        _opt(t, n, _BF16, shape=(total, Hkv, D), device=dev)
+    k_out = _new((total, Hkv, D), torch.bfloat16, dev, stream) if k_out is None else k_out
+    v_out = _new((total, Hkv, D), torch.bfloat16, dev, stream) if v_out is None else v_out
+    _run(dev, stream, "kv_cache_gather", _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+         _ptr(cu_seqlens), _ptr(k_out), _ptr(v_out), n_seq, total, Hkv, D, n_pages, page, max_pages, layout, dtype)
+    return k_out, v_out
+
+
+def decode_paged_workspace_bytes(B, T, Hq, Hkv, D, page_size, max_pages):
+    """Bytes of workspace attn_decode_paged needs for this shape on the current device."""
+    return int(_lib.load().attn_decode_paged_workspace_bytes(int(B), int(T), int(Hq), int(Hkv), int(D),
+                                                             int(page_size), int(max_pages)))
+
+
+def attn_decode_paged(q, k_cache, v_cache, page_table, ctx_lens, k_scale=None, v_scale=None, q_lens=None,
+                      tree_mask=None, scale=0.0, token_major=False, out=None, lse=None, want_lse=True, workspace=None,
+                      stream=None):
+    """Attention of q [B, T, Hq, D] bf16 -- T = 1 token, or T drafted tokens whose keys follow the
+    context in the cache -- over a paged cache.  ``ctx_lens`` int32 [B]: keys before the drafted ones;
+    ``q_lens`` int32 [B]: drafted tokens of each sequence (None: T); ``tree_mask`` int64 [B, T]: bit i of
+    entry (b, t) lets drafted token t see drafted token i (None: i <= t).  Returns (o [B, T, Hq, D]
+    bf16, lse fp32 [B, Hq, T] or None); rows t >= q_lens[b] are not written."""
+    dev = _arg(q, "q", _BF16, dim=4).device
+    B, T, Hq, D = q.shape
+    n_pages, page, Hkv, Dc, layout, dtype = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    if Dc != D:
+        raise ValueError(f"q has head dimension {D}, the cache {Dc}")
+    _arg(page_table, "page_table", _I32, dim=2, device=dev)
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table: expected {B} rows, got shape {tuple(page_table.shape)}")
+    max_pages = page_table.shape[1]
+    _arg(ctx_lens, "ctx_lens", _I32, shape=(B,), device=dev)
+    _opt(q_lens, "q_lens", _I32, shape=(B,), device=dev)
+    _opt(tree_mask, "tree_mask", _I64, shape=(B, T), device=dev)
+    _opt(out, "out", _BF16, shape=q.shape, device=dev)
+    _opt(lse, "lse", _F32, shape=(B, Hq, T), device=dev)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = decode_paged_workspace_bytes(B, T, Hq, Hkv, D, page, max_pages)
+        workspace = _new((need,), torch.uint8, dev, stream) if need else None
+    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    if out is None:
+        out = _new(q.shape, torch.bfloat16, dev, stream)
+    if lse is None and want_lse:
+        lse = _new((B, Hq, T), torch.float32, dev, stream)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(dev, stream, "attn_decode_paged", _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(out),
+         _ptr(lse), _ptr(page_table), _ptr(ctx_lens), _ptr(q_lens), _ptr(tree_mask), _ptr(workspace) if wsb else None, wsb,
+         B, T, Hq, Hkv, D, n_pages, page, max_pages, layout, dtype, float(scale))
+    return out, lse

@@ -391,6 +391,134 @@ int rope_hadamard_rotate_quant_fp8(const void* x, const float* rope_cs, int n_po
                                    float* scale, const float* signs, int B, int H, int S, int D,
                                    void* stream);
 
+/*
+ * Rotary positions and the paged key/value cache.  The pages have no counterpart: [HADA] names
+ *   rotary embedding as the bandwidth-bound op beside the quantiser and LLM inference as
+ *   future work, and defines neither a cache nor a table of pages.  Readings:
+ *   A cache is two arrays of n_pages pages of page_size rows (a power of two, 16 .. 1024) of
+ *   Hkv heads of D elements, bf16 (ATTN_BF16) or E4M3 codes (ATTN_FP8_E4M3) with one fp32 scale
+ *   per row -- a row is one token's one head, so a token can be written without its neighbours:
+ *     ATTN_CACHE_HEAD_MAJOR   [n_pages, Hkv, page_size, D]
+ *     ATTN_CACHE_TOKEN_MAJOR  [n_pages, page_size, Hkv, D]
+ *     k_scale, v_scale        [n_pages, Hkv, page_size] fp32 (E4M3), NULL (bf16)
+ *   16-byte aligned, contiguous.  Key j of a sequence lies in page page_table[seq][j / page_size]
+ *   at offset j % page_size.  Page tables, lengths, slots and positions are device memory, so
+ *   their contents are checked by the kernels: what lies outside the cache or the table is neither
+ *   read nor written and leaves ATTN_ERR_INVALID_ARG in the device error word (attn_check()).
+ *   The calls enqueue kernels only (no allocation, no synchronisation) and can be captured into
+ *   a CUDA graph; replays read the lengths and tables they then find.
+ */
+typedef enum { ATTN_CACHE_HEAD_MAJOR = 0, ATTN_CACHE_TOKEN_MAJOR = 1 } attn_cache_layout;
+
+/* Pairs of a rotary turn: (x[2i], x[2i+1]) or (x[i], x[i + rot_dim/2]). */
+typedef enum { ATTN_ROPE_INTERLEAVED = 0, ATTN_ROPE_HALF = 1 } attn_rope_layout;
+
+typedef enum {
+  ATTN_ROPE_UNSCALED = 0,
+  ATTN_ROPE_LINEAR = 1,       /* theta_i / factor (position interpolation) */
+  ATTN_ROPE_NTK = 2,          /* base * factor^(rot_dim / (rot_dim - 2)) */
+  ATTN_ROPE_YARN = 3          /* by parts, see rope_scaled_table */
+} attn_rope_scaling;
+
+/*
+ * rope_scaled_table -- rope_cos_sin_table for rot_dim rotated elements and a context stretched by
+ *   `factor` (>= 1).  ATTN_ROPE_YARN (Peng et al. 2023, "YaRN", sections 3.2-3.4): with
+ *   r = original_length * theta_i / (2 pi) turns and g = clamp((r - 1) / 31, 0, 1),
+ *   theta_i' = (1 - g) theta_i / factor + g theta_i, and cos and sin are multiplied by
+ *   0.1 ln(factor) + 1.  original_length (>= 1) is read by that scaling only.
+ *   cs : [n_pos, rot_dim/2, 2] fp32, evaluated in fp64, 8-byte aligned; 1 <= n_pos <= 2^26;
+ *   rot_dim even, 4 .. 4096.
+ */
+int rope_scaled_table(float* cs, int n_pos, int rot_dim, double base, int scaling, double factor,
+                      double original_length, void* stream);
+
+/*
+ * rope_apply -- rotary positions of the first rot_dim elements of every row; the rest is copied.
+ *   x, out   : bf16 rows of H heads of D elements (64, 128, 256), contiguous within a token;
+ *              token t starts at element t * x_stride / t * out_stride (multiples of 8, at
+ *              least H * D; a view of a fused projection).  out may be x (same stride); otherwise
+ *              they must not overlap.
+ *   rope_cs  : [n_pos, rot_dim/2, 2] fp32 from rope_scaled_table or rope_cos_sin_table (D =
+ *              rot_dim), 16-byte aligned.  rot_dim: a multiple of 16, 16 .. D.
+ *   positions: int32 [n_tokens], 0 .. n_pos-1; a token whose position lies outside is not
+ *              written.  NULL: token t has position t % seq_len (seq_len <= n_pos).
+ *   transpose: 0 = rotate; 1 = the transposed rotation, which takes the gradient of the output
+ *              to the gradient of x (angle negated, the table's multiplier kept).
+ *   fp32 arithmetic, one rounding to bf16.
+ */
+int rope_apply(const void* x, void* out, const float* rope_cs, const int* positions, int n_tokens,
+               int seq_len, int H, int D, long long x_stride, long long out_stride, int n_pos,
+               int rot_dim, int rope_layout, int transpose, void* stream);
+
+/*
+ * kv_cache_append -- write tokens' keys and values to a cache.
+ *   k, v  : bf16 rows of Hkv heads of D elements (64, 128, 256), tokens k_stride / v_stride
+ *           elements apart (as rope_apply).
+ *   slots : int64 [n_tokens], page * page_size + offset.  A negative slot is a padded token and is
+ *           not written; one past the cache is reported and not written.  The slots of a call
+ *           must be distinct: of a slot given twice the row may mix its tokens.
+ *   E4M3  : row scale = max |x| / 448 and code = E4M3(x / scale) in fp32, nearest even.  A row
+ *           below 2^-117 throughout is written as zeros with scale 1; a row with a NaN or an
+ *           infinity reads back as NaN.  bf16 rows are copied.
+ *   Rows no slot names are left as they are.
+ *
+ * rope_kv_cache_append -- the same with rope_apply's rotation of q and k in front, in one launch:
+ *   q_out [n_tokens, Hq, D] bf16 gets the rotated q of every token (padded ones too); the keys are rotated in fp32 and rounded once, into the cache; v is not rotated.
+ *   positions: int32 [n_tokens], required; a token whose position lies outside the table is
+ *   reported and its q_out row and key are not written.
+ */
+int kv_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale,
+                    float* v_scale, const long long* slots, int n_tokens, int Hkv, int D,
+                    long long k_stride, long long v_stride, int n_pages, int page_size,
+                    int cache_layout, int dtype, void* stream);
+int rope_kv_cache_append(const void* q, const void* k, const void* v, void* q_out,
+                         const float* rope_cs, const int* positions, void* k_cache, void* v_cache,
+                         float* k_scale, float* v_scale, const long long* slots, int n_tokens, int Hq,
+                         int Hkv, int D, long long q_stride, long long k_stride, long long v_stride,
+                         int n_pages, int page_size, int cache_layout, int dtype, int n_pos,
+                         int rot_dim, int rope_layout, void* stream);
+
+/*
+ * kv_cache_gather -- read sequences back as packed bf16 rows, the layout attn_fwd_varlen takes.
+ *   page_table : int32 [n_seq, max_pages].  cu_seqlens : int32 [n_seq + 1], 0 .. total,
+ *   non-decreasing; row t of the output is token t - cu_seqlens[s] of the sequence s that holds t.
+ *   k_out, v_out : [total, Hkv, D] bf16 (code * scale for E4M3).  A row that lies in no sequence,
+ *   past the page table or in a page outside the cache is reported and not written.
+ *   D in {64, 128, 256}.
+ */
+int kv_cache_gather(const void* k_cache, const void* v_cache, const float* k_scale,
+                    const float* v_scale, const int* page_table, const int* cu_seqlens, void* k_out,
+                    void* v_out, int n_seq, int total, int Hkv, int D, int n_pages, int page_size,
+                    int max_pages, int cache_layout, int dtype, void* stream);
+
+/*
+ * attn_decode_paged -- attention of T (drafted) query tokens per sequence over a paged cache: one
+ *   decoding step (T = 1), a chain or a tree of drafted tokens.  The drafted tokens' own keys and
+ *   values are in the cache already, behind the ctx_lens[b] keys of the context.
+ *   q, o      : [B, T, Hq, D] bf16, D in {64, 128}.  lse : [B, Hq, T] fp32 or NULL.
+ *   ctx_lens  : int32 [B] >= 0.  q_lens : int32 [B], 0 .. T drafted tokens of each sequence, or
+ *               NULL (T).  ctx_lens[b] + q_lens[b] <= max_pages * page_size.
+ *   tree_mask : uint64 [B, T] or NULL.  Drafted token t sees the context, and drafted token i < q_len
+ *               iff bit i of tree_mask[b, t] is set (its own bit too); NULL: i <= t.
+ *   page_table: int32 [B, max_pages]; entries behind a sequence's last key are not read.
+ *   Query head h reads key/value head h / (Hq / Hkv).  Rows t >= q_lens[b] of o and lse are left as
+ *   they are; a row that sees no key gets o = 0 and lse = -inf.  What a row does not see never
+ *   reaches it, whatever its bytes hold.
+ *   B <= 1024, T <= 64.  scale : as attn_fwd.
+ *   workspace : attn_decode_paged_workspace_bytes(...) bytes of device scratch, 16-byte aligned,
+ *               overwritten (NULL when that is 0); calls whose kernels may overlap need their own.
+ *   The launches depend on shapes and the device's SM count only; results are the same from run
+ *   to run.  Lengths out of range: nothing is written, attn_check() reports it.
+ */
+size_t attn_decode_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int page_size,
+                                         int max_pages);
+int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                      const float* v_scale, void* o, float* lse, const int* page_table,
+                      const int* ctx_lens, const int* q_lens, const unsigned long long* tree_mask,
+                      void* workspace, size_t workspace_bytes, int B, int T, int Hq, int Hkv, int D,
+                      int n_pages, int page_size, int max_pages, int cache_layout, int dtype,
+                      float scale, void* stream);
+
 /* Message for the last non-OK status returned on the calling host thread ("" if none). */
 const char* attn_get_last_error(void);
 
@@ -398,8 +526,8 @@ const char* attn_get_last_error(void);
  * attn_check -- synchronise `stream`, then read and clear the current
  * device's error word.  Returns ATTN_OK, ATTN_ERR_TIMEOUT (a kernel's bounded
  * wait ran out; its outputs are undefined), ATTN_ERR_INVALID_ARG (a
- * variable-length launch found bad cu_seqlens; it wrote nothing) or
- * ATTN_ERR_CUDA.
+ * kernel rejected device-side input -- cu_seqlens, lengths, slots, positions or
+ * pages; the message says which) or ATTN_ERR_CUDA.
  */
 int attn_check(void* stream);
 

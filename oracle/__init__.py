@@ -32,9 +32,11 @@ Modules:
 * ``rope``       -- rotary position embedding (the pages' example of a
   memory-bound op to fuse the rotation with) and its fusion with the
   quantiser.
+* ``paged``      -- rotary positions in both pair layouts and stretched contexts,
+  a row-scaled key/value cache, attention of a drafted tree over it.
 
 Every array is numpy float64 unless stated; inputs are the exact values the
 GPU sees (bf16 or E4M3 values widened to fp64).
 """
 
-from . import attention, backward, gqa, hadamard, e4m3, quantise, fp8_path, rope, varlen  # noqa: F401
+from . import attention, backward, gqa, hadamard, e4m3, quantise, fp8_path, paged, rope, varlen  # noqa: F401
