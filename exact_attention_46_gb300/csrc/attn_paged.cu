@@ -20,18 +20,19 @@
 //     in a fixed order;
 //   * a producer warp looks the pages up and fills a ring of (K tile, V tile) stages by TMA, one
 //     box per page and swizzle panel; a page number outside the cache is not loaded and reported;
-//   * eight consumer warps take 16 keys of every tile each, from S = Q K^T to their own running
-//     (max, sum, O): no barrier between warps inside a unit.  With at most 32 rows an MMA
-//     tile of 128 rows would stand mostly empty and its hand-offs (S, P, O through Tensor Memory)
-//     would set the pace, so the products run on mma.sync m16n8k16 from registers;
-//   * E4M3 rows become fp16 in registers, exactly (sign and exponent-mantissa field shifted, a
-//     factor 2^-8), with queries in fp16 after an exact power-of-two scaling of each row; the
-//     key's scale multiplies its logit, the value's scale its numerator, over a power-of-two
-//     reference that keeps fp16 in range.  Numerators are rounded to bf16 (fp16 with E4M3)
+//   * a consumer warp takes 32 keys of a tile, from S = Q K^T to its own running (max, sum, O): no
+//     barrier between warps inside a unit.  With at most 32 rows an MMA tile of 128 rows would
+//     stand mostly empty and its hand-offs (S, P, O through Tensor Memory) would set the pace, so
+//     the products run on mma.sync m16n8k16 from registers.  Two groups of four warps: with up to
+//     16 rows they take every other tile, with up to 32 each takes 16 of the rows;
+//   * E4M3 rows become fp16 in registers (exact), with queries in fp16 after an exact
+//     power-of-two scaling of each row; the key's scale multiplies its logit, the value's scale
+//     its numerator, over a power-of-two reference that keeps fp16 in range.  Numerators are rounded to bf16 (fp16 with E4M3)
 //     because the tensor core takes no wider operand; sums and statistics are fp32.
 // Hidden keys never reach a sum: their logit is replaced by -inf, their numerator by 0, and in tiles
-// that hold drafted keys or the end of the sequence a bf16 value row that is past the end or not
-// finite is taken out of the product and added (where it is seen) element by element.
+// that hold drafted keys or the end of the sequence a value row that is past the end or not finite
+// is masked out of the product and, where it is seen, enters by itself (bf16: element by element;
+// E4M3: by its scale, which is not finite where a code is NaN).
 // Every mbarrier wait is bounded.
 #include <atomic>
 #include <cstdint>
@@ -50,9 +51,10 @@ constexpr int NWARP = 8;                        // consumer warps
 constexpr int NTHREADS = 32 * (NWARP + 1);
 enum : int { WHERE_PAGED_LOAD = 51, WHERE_PAGED_USE = 52, WHERE_PAGED_LENS = 53, WHERE_PAGED_PAGE = 54 };
 
-template <int D, bool FP8, int MT>
+// WIDE: 32 rows per unit, one warp group per 16; otherwise 16 rows, the groups take turns by tile.
+template <int D, bool FP8, bool WIDE>
 struct PagedCfg {
-  static constexpr int RB = 16 * MT;
+  static constexpr int RB = WIDE ? 32 : 16;
   static constexpr int ESZ = FP8 ? 1 : 2;
   static constexpr int ROW_BYTES = D * ESZ;
   static constexpr int PANEL_ROW = ROW_BYTES >= 128 ? 128 : ROW_BYTES;
@@ -63,19 +65,20 @@ struct PagedCfg {
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES + SCALE_BYTES;
   static constexpr int KS = D / 16;                          // k-steps of Q K^T
   static constexpr int NB = D / 8;                           // n-blocks of O
-  static constexpr int MCOLS = MT == 1 ? 32 : (FP8 ? 16 : 8);  // columns merged at a time
+  static constexpr int PARTS = WIDE ? 4 : 8;                 // warps that hold a part of a row
+  static constexpr int MCOLS = 32;                           // columns merged at a time
   static constexpr int MSTRIDE = MCOLS + 8;
-  static constexpr int Q_BYTES = MT * KS * 32 * 16;
-  static constexpr int REST = 1024 + Q_BYTES + NWARP * RB * MSTRIDE * 4 + NWARP * RB * 8 + RB * 12 +
+  static constexpr int Q_BYTES = RB / 16 * KS * 32 * 16;
+  static constexpr int REST = 1024 + Q_BYTES + NWARP * 16 * MSTRIDE * 4 + NWARP * 16 * 8 + RB * 12 +
                               (PAGED_MAX_BATCH + 2) * 4 + 16 * 16 + 64;
   static constexpr int FIT = (227 * 1024 - REST) / STAGE_BYTES, WANT = 196608 / (2 * TILE_BYTES);
   static constexpr int NSTAGE = FIT < WANT ? FIT : WANT;     // up to 192 KB of K/V in flight
   static constexpr int Q_OFF = NSTAGE * STAGE_BYTES;
-  static constexpr int M_OFF = Q_OFF + Q_BYTES;              // merge buffer [NWARP][RB][MSTRIDE]
-  static constexpr int M_BYTES = NWARP * RB * MSTRIDE * 4;
-  static constexpr int ML_OFF = M_OFF + M_BYTES;             // [NWARP][RB] (max, sum)
-  static constexpr int BITS_OFF = ML_OFF + NWARP * RB * 8;   // [RB] visible drafts
-  static constexpr int RQ_OFF = BITS_OFF + RB * 8;           // [RB] logit multiplier
+  static constexpr int M_OFF = Q_OFF + Q_BYTES;              // merge buffer [NWARP][16][MSTRIDE]
+  static constexpr int M_BYTES = NWARP * 16 * MSTRIDE * 4;
+  static constexpr int ML_OFF = M_OFF + M_BYTES;             // [NWARP][16] (max, sum)
+  static constexpr int BITS_OFF = ML_OFF + NWARP * 16 * 8;   // [RB] visible drafts
+  static constexpr int RQ_OFF = BITS_OFF + RB * 8;           // [RB] power of two of a query row
   static constexpr int PRE_OFF = RQ_OFF + RB * 4;            // [PAGED_MAX_BATCH + 1] tile prefix
   static constexpr int BAR_OFF = PRE_OFF + (PAGED_MAX_BATCH + 2) * 4;
   static constexpr int SMEM_BYTES = 1024 + BAR_OFF + 2 * NSTAGE * 8 + 64;
@@ -123,10 +126,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// Two E4M3 bytes in the high halves' upper bytes -> two fp16 of value * 2^-8 (exact: the 4-bit
-// exponent and 3-bit mantissa land in fp16's low exponent bits and top mantissa bits).
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
-  return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+// Four E4M3 bytes -> fp16 pairs (bytes 0, 1) and (bytes 2, 3); exact.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
 __device__ __forceinline__ void wait_drain_paged(uint32_t bar, uint32_t parity, long long limit) {
@@ -200,11 +203,11 @@ __device__ __forceinline__ Segment find_segment(const PagedParams& p, const int*
 
 __device__ __forceinline__ long long cta_start(long long i, long long W, long long N) { return i * W / N; }
 
-template <int D, bool FP8, int MT>
+template <int D, bool FP8, bool WIDE>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const PagedParams p) {
-  using C = PagedCfg<D, FP8, MT>;
+  using C = PagedCfg<D, FP8, WIDE>;
   constexpr int RB = C::RB, NSTAGE = C::NSTAGE;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -289,15 +292,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     return;
   }
 
-  // ---- consumers: warp w takes keys 16 w .. 16 w + 15 of every tile ----
+  // ---- consumers: warp w takes keys 32 (w & 3) .. of a tile; the two groups of four warps take
+  // the unit's row halves (WIDE) or every other tile ----
   const int g = lane >> 2, t4 = lane & 3;
-  const int kw = 16 * warp;
+  const int kw = 32 * (warp & 3), group = warp >> 2;
+  const int rlo = WIDE ? 16 * group : 0;         // first row of this warp
   uint4* qfrag = reinterpret_cast<uint4*>(base + C::Q_OFF);
   float* mbuf = reinterpret_cast<float*>(base + C::M_OFF);
   float2* ml = reinterpret_cast<float2*>(base + C::ML_OFF);
   unsigned long long* bits = reinterpret_cast<unsigned long long*>(base + C::BITS_OFF);
   float* rq = reinterpret_cast<float*>(base + C::RQ_OFF);
-  // key (within the warp's 16) of column e of n-block nb of this thread's S, and of value rows
+  // key (within the warp's 32) of column e of n-block nb of this thread's S
   auto key_of = [&](int nb, int e) { return FP8 ? 8 * nb + t4 + 4 * e : 8 * nb + 2 * t4 + e; };
   int it = 0;
   for (long long x = x0; x < x1;) {
@@ -311,10 +316,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       return t < ql ? qb + (static_cast<long long>(t) * p.Hq + pr % p.G) * D : nullptr;
     };
     // the last segment's readers of the shared arrays below are past them (barrier at its end).
-    // Query fragments: entry (mt, ks, lane) holds the A registers of that lane
+    // Query fragments: entry (16-row block, k-step, lane) holds the A registers of that lane
     if (FP8) {
       // per-row power of two that brings the largest element into [1, 2): exact, and the logit
-      // multiplier takes it back (with the 2^8 of the key codes)
+      // multiplier takes it back
       for (int r = warp; r < RB; r += NWARP) {
         const __nv_bfloat16* src = row_ptr(r);
         float m = 0.f;
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       named_bar_sync(1, 32 * NWARP);
     }
-    for (int i = threadIdx.x; i < MT * C::KS * 32; i += 32 * NWARP) {
+    for (int i = threadIdx.x; i < RB / 16 * C::KS * 32; i += 32 * NWARP) {
       const int l = i & 31, ks = (i >> 5) % C::KS, mt = (i >> 5) / C::KS;
       const int lg = l >> 2, lt = l & 3;
       uint32_t a[4];
@@ -366,51 +371,47 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       bits[threadIdx.x] = m;
     }
     named_bar_sync(1, 32 * NWARP);
-    float cr[MT][2];                               // logit multiplier of rows g, g + 8
+    float cr[2];                                   // logit multiplier of rows g, g + 8
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) cr[mt][h] = FP8 ? p.c_log2 * 256.f * rq[16 * mt + g + 8 * h] : p.c_log2;
+    for (int h = 0; h < 2; ++h) cr[h] = FP8 ? p.c_log2 * rq[rlo + g + 8 * h] : p.c_log2;
+    const uint4* qf = qfrag + (WIDE ? group : 0) * C::KS * 32 + lane;
 
-    float o[MT][C::NB][4];
-    float m_run[MT][2], l_run[MT][2];
+    float o[C::NB][4];
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     float vref = 0.f;                              // E4M3: power of two above the value scales seen
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
-      for (int nb = 0; nb < C::NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[mt][nb][i] = 0.f;
-      m_run[mt][0] = m_run[mt][1] = -INFINITY;
-      l_run[mt][0] = l_run[mt][1] = 0.f;
-    }
+      for (int i = 0; i < 4; ++i) o[nb][i] = 0.f;
 
     for (int j = sg.t0; j < sg.t1; ++j, ++it) {
       const int slot = it % NSTAGE;
+      // every warp waits for and frees every tile, its own or not: a parity wait can only follow a
+      // barrier whose phases it sees one by one
       const bool ok = warp_wait(BAR_FULL(slot), (it / NSTAGE) & 1, ctl, WHERE_PAGED_USE);
       const int k0 = 128 * j + kw;                 // first key of this warp
-      if (ok && k0 < L) {
+      if (ok && k0 < L && (WIDE || (it & 1) == group)) {
         const uint32_t sK = base_u32 + slot * C::STAGE_BYTES, sV = sK + C::TILE_BYTES;
-        const bool tail = k0 + 16 > ctx;           // drafted keys, or the end of the sequence
-        float s[MT][2][4];
+        const bool tail = k0 + 32 > ctx;           // drafted keys, or the end of the sequence
+        float s[4][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][nb][i] = 0.f;
+          for (int i = 0; i < 4; ++i) s[nb][i] = 0.f;
         // ---- S = Q K^T ----
         if constexpr (!FP8) {
           const int r = kw + (lane & 7) + 8 * (lane >> 4), half = (lane >> 3) & 1;
 #pragma unroll
           for (int ks = 0; ks < C::KS; ++ks) {
-            uint32_t kf[4];
-            ldsm4(sK + (ks >> 2) * C::PANEL_BYTES + r * 128 + (((2 * (ks & 3) + half) ^ (r & 7)) << 4), kf);
+            uint32_t kf[2][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const uint4 a = qfrag[(mt * C::KS + ks) * 32 + lane];
-              mma16816<false>(s[mt][0], a, kf[0], kf[1]);
-              mma16816<false>(s[mt][1], a, kf[2], kf[3]);
+            for (int y = 0; y < 2; ++y)
+              ldsm4(sK + (ks >> 2) * C::PANEL_BYTES + (r + 16 * y) * 128 + (((2 * (ks & 3) + half) ^ (r & 7)) << 4), kf[y]);
+            const uint4 a = qf[ks * 32];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              mma16816<false>(s[2 * y], a, kf[y][0], kf[y][1]);
+              mma16816<false>(s[2 * y + 1], a, kf[y][2], kf[y][3]);
             }
           }
         } else {
@@ -419,43 +420,41 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const int rg = (g >> 1) + 4 * (g & 1);
 #pragma unroll
           for (int i = 0; i < C::KS / 4; ++i) {
-            uint4 w[2];
+            uint4 w[4];
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
+            for (int nb = 0; nb < 4; ++nb) {
               const int r = kw + 8 * nb + rg;
               const int ch = C::PANEL_ROW == 128 ? ((t4 + 4 * i) ^ rg) : (t4 ^ ((r >> 1) & 3));
               w[nb] = lds128(sK + r * C::PANEL_ROW + 16 * ch);
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              uint32_t b[2][2];
+              const uint4 a = qf[(4 * i + c) * 32];
 #pragma unroll
-              for (int nb = 0; nb < 2; ++nb) {
-                const uint32_t word = c == 0 ? w[nb].x : (c == 1 ? w[nb].y : (c == 2 ? w[nb].z : w[nb].w));
-                b[nb][0] = e4m3_pair(__byte_perm(word, 0, 0x1404));
-                b[nb][1] = e4m3_pair(__byte_perm(word, 0, 0x3424));
-              }
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                const uint4 a = qfrag[(mt * C::KS + 4 * i + c) * 32 + lane];
-                mma16816<true>(s[mt][0], a, b[0][0], b[0][1]);
-                mma16816<true>(s[mt][1], a, b[1][0], b[1][1]);
+              for (int nb = 0; nb < 4; ++nb) {
+                uint32_t b0, b1;
+                e4m3x4_to_f16(c == 0 ? w[nb].x : (c == 1 ? w[nb].y : (c == 2 ? w[nb].z : w[nb].w)), b0, b1);
+                mma16816<true>(s[nb], a, b0, b1);
               }
             }
           }
         }
-        // ---- scales of this thread's four keys ----
-        float ksc[2][2], vsc[2][2];
+        // ---- scales of this thread's eight keys ----
+        float ksc[4][2], vsc[4][2];
+        uint32_t vbad = 0;                         // E4M3, tail: value rows past the end or without a finite scale
         if constexpr (FP8) {
           const float* sc = reinterpret_cast<const float*>(base + slot * C::STAGE_BYTES + 2 * C::TILE_BYTES) + kw;
           float top = 0.f;
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
+          for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const bool in = k0 + key_of(nb, e) < L;
-              ksc[nb][e] = in ? sc[key_of(nb, e)] : 0.f;
-              vsc[nb][e] = in ? sc[128 + key_of(nb, e)] : 0.f;
+              ksc[nb][e] = sc[key_of(nb, e)];
+              vsc[nb][e] = sc[128 + key_of(nb, e)];
+              if (tail) {
+                if (k0 + key_of(nb, e) >= L) vsc[nb][e] = 0.f;
+                if (!(vsc[nb][e] < INFINITY) || k0 + key_of(nb, e) >= L) vbad |= 1u << (2 * nb + e);
+              }
               top = fmaxf(top, vsc[nb][e] < INFINITY ? vsc[nb][e] : 0.f);
             }
           if (__any_sync(0xffffffffu, top > vref)) {
@@ -465,181 +464,188 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const float nref = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + (top < 0x1p126f ? 0x00800000u : 0u));
             const float f = vref / nref;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
-              for (int nb = 0; nb < C::NB; ++nb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[mt][nb][i] *= f;
+              for (int i = 0; i < 4; ++i) o[nb][i] *= f;
             vref = nref;
           }
           const float up = vref > 0.f ? 1024.f / vref : 0.f;     // numerators times 2^10 at the largest scale
 #pragma unroll
-          for (int nb = 0; nb < 2; ++nb)
+          for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) vsc[nb][e] *= up;
         }
         // ---- logits, mask, running maximum ----
-        float mt_max[MT][2];
+        float mt_max[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < 2; ++h) {
+          float mx = -INFINITY;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float mx = -INFINITY;
+          for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float v = s[mt][nb][2 * h + e] * (FP8 ? cr[mt][h] * ksc[nb][e] : cr[mt][h]);
-                if (tail) {
-                  const int key = k0 + key_of(nb, e);
-                  const bool sees = key < ctx || (key < L && ((bits[16 * mt + g + 8 * h] >> (key - ctx)) & 1));
-                  v = sees ? v : -INFINITY;
-                }
-                s[mt][nb][2 * h + e] = v;
-                mx = fmaxf(mx, v);
+            for (int e = 0; e < 2; ++e) {
+              float v = s[nb][2 * h + e] * (FP8 ? cr[h] * ksc[nb][e] : cr[h]);
+              if (tail) {
+                const int key = k0 + key_of(nb, e);
+                const bool sees = key < ctx || (key < L && ((bits[rlo + g + 8 * h] >> (key - ctx)) & 1));
+                v = sees ? v : -INFINITY;
               }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            mt_max[mt][h] = mx;
-          }
-        bool grow = false;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) grow = grow || mt_max[mt][h] > m_run[mt][h] + 4.f;
-        if (__any_sync(0xffffffffu, grow)) {
+              s[nb][2 * h + e] = v;
+              mx = fmaxf(mx, v);
+            }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          mt_max[h] = mx;
+        }
+        if (__any_sync(0xffffffffu, mt_max[0] > m_run[0] + 4.f || mt_max[1] > m_run[1] + 4.f)) {
           // lazily: O and the sum are only rescaled when some maximum moved by a factor of 2^4
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int h = 0; h < 2; ++h) {
+            const float mn = fmaxf(m_run[h], mt_max[h]);
+            const float f = m_run[h] == -INFINITY ? 0.f : ex2(m_run[h] - mn);
+            m_run[h] = mn;
+            l_run[h] *= f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float mn = fmaxf(m_run[mt][h], mt_max[mt][h]);
-              const float f = m_run[mt][h] == -INFINITY ? 0.f : ex2(m_run[mt][h] - mn);
-              m_run[mt][h] = mn;
-              l_run[mt][h] *= f;
-#pragma unroll
-              for (int nb = 0; nb < C::NB; ++nb) {
-                o[mt][nb][2 * h] *= f;
-                o[mt][nb][2 * h + 1] *= f;
-              }
+            for (int nb = 0; nb < C::NB; ++nb) {
+              o[nb][2 * h] *= f;
+              o[nb][2 * h + 1] *= f;
             }
+          }
         }
         // ---- numerators ----
-        uint4 pa[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t w[2][2];
+        uint4 pa[2];
+        {
+          uint32_t w[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float off = m_run[mt][h] == -INFINITY ? 0.f : m_run[mt][h];
+            const float off = m_run[h] == -INFINITY ? 0.f : m_run[h];
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-              float q0 = ex2(s[mt][nb][2 * h] - off), q1 = ex2(s[mt][nb][2 * h + 1] - off);
-              l_run[mt][h] += q0 + q1;
+            for (int nb = 0; nb < 4; ++nb) {
+              float q0 = ex2(s[nb][2 * h] - off), q1 = ex2(s[nb][2 * h + 1] - off);
+              l_run[h] += q0 + q1;
               if constexpr (FP8) {
                 // a hidden key's scale may be anything: its numerator is 0 whatever it is
                 q0 = tail && q0 == 0.f ? 0.f : q0 * vsc[nb][0];
                 q1 = tail && q1 == 0.f ? 0.f : q1 * vsc[nb][1];
                 w[h][nb] = pack_f16x2(q0, q1);
               } else {
-                s[mt][nb][2 * h] = q0;
-                s[mt][nb][2 * h + 1] = q1;
+                s[nb][2 * h] = q0;
+                s[nb][2 * h + 1] = q1;
                 w[h][nb] = pack_bf16x2(q0, q1);
               }
             }
           }
-          pa[mt] = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
+          pa[0] = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
+          pa[1] = make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]);
         }
         // ---- O += P V ----
         if constexpr (!FP8) {
+          uint32_t odd = 0;                        // value rows past the end, or not finite: out of the product
           if (tail) {
-            // value rows past the end, or not finite: out of the product
-            uint32_t odd = 0;
-            for (int r = 0; r < 16; ++r) {
+            for (int r = 0; r < 32; ++r) {
               bool strange = k0 + r >= L;
               if (!strange && k0 + r >= ctx) {
                 bool inf = false;
                 for (int c = lane; c < D / 2; c += 32) {
-                  const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                      base + (sV - base_u32) + (c >> 5) * C::PANEL_BYTES + (kw + r) * 128 +
-                      ((((c & 31) >> 2) ^ ((kw + r) & 7)) << 4) + (c & 3) * 4);
+                  const uint32_t w = *reinterpret_cast<const uint32_t*>(base + (sV - base_u32) + (c >> 5) * C::PANEL_BYTES +
+                                                                        (kw + r) * 128 + (c & 31) * 4);
                   inf = inf || (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
                 }
                 strange = __any_sync(0xffffffffu, inf);
               }
               if (strange) odd |= 1u << r;
             }
-            if (odd != 0) {
-              for (int r = 0; r < 16; ++r) {
-                if (!((odd >> r) & 1)) continue;
-                if (k0 + r < L) {
-                  // the lane of each quad that holds key r's numerators
-                  const int src = (lane & ~3) | ((r & 7) >> 1);
+            // those that some row may see are added element by element
+            const uint32_t seen = k0 + 32 <= L ? odd : odd & ((1u << (L - k0)) - 1);
+            if (seen != 0) {
 #pragma unroll
-                  for (int mt = 0; mt < MT; ++mt)
+              for (int rb = 0; rb < 4; ++rb)
+                for (int r8 = 0; r8 < 8; ++r8) {
+                  const int r = 8 * rb + r8;
+                  if (!((seen >> r) & 1)) continue;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                      float pv = r < 8 ? ((r & 1) ? s[mt][0][2 * h + 1] : s[mt][0][2 * h])
-                                       : ((r & 1) ? s[mt][1][2 * h + 1] : s[mt][1][2 * h]);
-                      pv = __shfl_sync(0xffffffffu, pv, src);
-                      if (pv != 0.f) {
+                  for (int h = 0; h < 2; ++h) {
+                    // the lane of each quad that holds key r's numerators
+                    float pv = (r8 & 1) ? s[rb][2 * h + 1] : s[rb][2 * h];
+                    pv = __shfl_sync(0xffffffffu, pv, (lane & ~3) | (r8 >> 1));
+                    if (pv != 0.f) {
 #pragma unroll
-                        for (int nb = 0; nb < C::NB; ++nb) {
-                          const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                              base + (sV - base_u32) + (nb >> 3) * C::PANEL_BYTES + (kw + r) * 128 +
-                              (((nb & 7) ^ ((kw + r) & 7)) << 4) + 4 * t4);
-                          o[mt][nb][2 * h] += pv * __uint_as_float(w << 16);
-                          o[mt][nb][2 * h + 1] += pv * __uint_as_float(w & 0xffff0000u);
-                        }
+                      for (int nb = 0; nb < C::NB; ++nb) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                            base + (sV - base_u32) + (nb >> 3) * C::PANEL_BYTES + (kw + r) * 128 +
+                            (((nb & 7) ^ ((kw + r) & 7)) << 4) + 4 * t4);
+                        o[nb][2 * h] += pv * __uint_as_float(w << 16);
+                        o[nb][2 * h + 1] += pv * __uint_as_float(w & 0xffff0000u);
                       }
                     }
+                  }
                 }
-                __syncwarp();
-                for (int c = lane; c < D / 2; c += 32)
-                  *reinterpret_cast<uint32_t*>(base + (sV - base_u32) + (c >> 5) * C::PANEL_BYTES + (kw + r) * 128 +
-                                               (c & 31) * 4) = 0u;
-              }
-              fence_proxy_async_smem();            // before the ring's next load of this stage
-              __syncwarp();
             }
           }
+          // value fragment register b of 16 keys: keys 2 t + 8 b and the next
+          uint32_t keep[2][2];
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t two = odd >> (16 * kk + 8 * y + 2 * t4);
+              keep[kk][y] = ((two & 1u) ? 0u : 0xffffu) | ((two & 2u) ? 0u : 0xffff0000u);
+            }
           const int r = kw + (lane & 15), hi = lane >> 4;
+          auto add = [&](bool masked) {
 #pragma unroll
-          for (int nb = 0; nb < C::NB; nb += 2) {
-            uint32_t vf[4];
-            ldsm4t(sV + (nb >> 3) * C::PANEL_BYTES + r * 128 + ((((nb & 7) + hi) ^ (r & 7)) << 4), vf);
+            for (int nb = 0; nb < C::NB; nb += 2)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma16816<false>(o[mt][nb], pa[mt], vf[0], vf[1]);
-              mma16816<false>(o[mt][nb + 1], pa[mt], vf[2], vf[3]);
-            }
-          }
+              for (int kk = 0; kk < 2; ++kk) {
+                uint32_t vf[4];
+                ldsm4t(sV + (nb >> 3) * C::PANEL_BYTES + (r + 16 * kk) * 128 + ((((nb & 7) + hi) ^ (r & 7)) << 4), vf);
+                if (masked) {
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) vf[y] &= keep[kk][y & 1];
+                }
+                mma16816<false>(o[nb], pa[kk], vf[0], vf[1]);
+                mma16816<false>(o[nb + 1], pa[kk], vf[2], vf[3]);
+              }
+          };
+          if (odd != 0) add(true);
+          else add(false);
         } else {
-          // lane g reads D / 8 bytes of rows t, t + 4, t + 8, t + 12 -- the keys of S's columns
+          // lane g reads D / 8 bytes of rows t, t + 4, t + 8, t + 12 of each 16 -- the keys of S's
+          // columns; a row that must not show is read as zeros (its codes may be NaN), and shows in
+          // the rows that see it through its scale
           constexpr int NW = D / 32;
-          uint32_t w[4][NW];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = kw + t4 + 4 * i;
-            if constexpr (D == 128) {
-              const uint4 u = lds128(sV + r * 128 + ((((g >> 1) | ((g & 1) << 2)) ^ (r & 7)) << 4));
-              w[i][0] = u.x; w[i][1] = u.y; w[i][2] = u.z; w[i][3] = u.w;
-            } else {
-              const int ch = ((g >> 2) & 1) | (((g >> 1) & 1) << 1);
-              const uint2 u = lds64(sV + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) + 8 * (g & 1));
-              w[i][0] = u.x; w[i][1] = u.y;
+          for (int kk = 0; kk < 2; ++kk) {
+            uint32_t w[4][NW];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = kw + 16 * kk + t4 + 4 * i;
+              if constexpr (D == 128) {
+                const uint4 u = lds128(sV + r * 128 + ((((g >> 1) | ((g & 1) << 2)) ^ (r & 7)) << 4));
+                w[i][0] = u.x; w[i][1] = u.y; w[i][2] = u.z; w[i][3] = u.w;
+              } else {
+                const int ch = ((g >> 2) & 1) | (((g >> 1) & 1) << 1);
+                const uint2 u = lds64(sV + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) + 8 * (g & 1));
+                w[i][0] = u.x; w[i][1] = u.y;
+              }
+              if (tail && ((vbad >> (4 * kk + i)) & 1)) {
+#pragma unroll
+                for (int c = 0; c < NW; ++c) w[i][c] = 0u;
+              }
             }
+#pragma unroll
+            for (int c = 0; c < NW; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                // bytes e, e + 1 of two rows: (row, row + 4) of element e, then of e + 1
+                const uint32_t sel = e == 0 ? 0x5140u : 0x7362u;
+                uint32_t b0, b1, d0, d1;
+                e4m3x4_to_f16(__byte_perm(w[0][c], w[1][c], sel), b0, d0);
+                e4m3x4_to_f16(__byte_perm(w[2][c], w[3][c], sel), b1, d1);
+                mma16816<true>(o[4 * c + e], pa[kk], b0, b1);
+                mma16816<true>(o[4 * c + e + 1], pa[kk], d0, d1);
+              }
           }
-#pragma unroll
-          for (int c = 0; c < NW; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t sel = static_cast<uint32_t>(e | (e << 4) | ((4 + e) << 8) | ((4 + e) << 12));
-              const uint32_t b0 = e4m3_pair(__byte_perm(w[0][c], w[1][c], sel));
-              const uint32_t b1 = e4m3_pair(__byte_perm(w[2][c], w[3][c], sel));
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816<true>(o[mt][4 * c + e], pa[mt], b0, b1);
-            }
         }
       }
       __syncwarp();
@@ -648,42 +654,37 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     // ---- the warps' partial results meet ----
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float l = l_run[mt][h];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (t4 == 0) ml[warp * RB + 16 * mt + g + 8 * h] = make_float2(m_run[mt][h], l);
-      }
+    for (int h = 0; h < 2; ++h) {
+      float l = l_run[h];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (t4 == 0) ml[warp * 16 + g + 8 * h] = make_float2(m_run[h], l);
+    }
     named_bar_sync(1, 32 * NWARP);
-    float f[MT][2];
+    // (max, sum) over the warps that hold a part of row r of the unit
+    auto whole_row = [&](int r, float& M, float& l) {
+      const float2* e = ml + (WIDE ? (r >> 4) * 4 * 16 : 0) + (r & 15);
+      M = -INFINITY;
+      l = 0.f;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int w = 0; w < C::PARTS; ++w) M = fmaxf(M, e[16 * w].x);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 16 * mt + g + 8 * h;
-        float M = -INFINITY, l = 0.f;
+      for (int w = 0; w < C::PARTS; ++w) l += e[16 * w].x == -INFINITY ? e[16 * w].y : e[16 * w].y * ex2(e[16 * w].x - M);
+    };
+    float f[2];
 #pragma unroll
-        for (int w = 0; w < NWARP; ++w) M = fmaxf(M, ml[w * RB + r].x);
-#pragma unroll
-        for (int w = 0; w < NWARP; ++w) {
-          const float2 e = ml[w * RB + r];
-          l += e.x == -INFINITY ? e.y : e.y * ex2(e.x - M);
-        }
-        f[mt][h] = m_run[mt][h] == -INFINITY ? 0.f : ex2(m_run[mt][h] - M) / l;
-        if (FP8) f[mt][h] *= vref * 0.25f;         // 2^8 of the codes / 2^10 of the numerators
-      }
+    for (int h = 0; h < 2; ++h) {
+      float M, l;
+      whole_row(rlo + g + 8 * h, M, l);
+      f[h] = m_run[h] == -INFINITY ? 0.f : ex2(m_run[h] - M) / l;
+      if (FP8) f[h] *= vref * 0x1p-10f;            // the 2^10 of the numerators
+    }
     const bool whole = sg.t0 == 0 && sg.t1 == sg.n;
     const long long ws_slot = 2ll * blockIdx.x + (sg.t0 > 0 ? 0 : 1);
     if (threadIdx.x < RB) {
       const int r = threadIdx.x;
-      float M = -INFINITY, l = 0.f;
-      for (int w = 0; w < NWARP; ++w) M = fmaxf(M, ml[w * RB + r].x);
-      for (int w = 0; w < NWARP; ++w) {
-        const float2 e = ml[w * RB + r];
-        l += e.x == -INFINITY ? e.y : e.y * ex2(e.x - M);
-      }
+      float M, l;
+      whole_row(r, M, l);
       const float lse2 = l == 0.f ? -INFINITY : M + __log2f(l);
       const int pr = sg.rt * RB + r, t = pr / p.G;
       if (!whole) p.ws_l[ws_slot * RB + r] = lse2;
@@ -695,44 +696,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int pass = 0; pass < C::NB / KB; ++pass) {
       if (pass > 0) named_bar_sync(1, 32 * NWARP);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int nb = 0; nb < KB; ++nb)
-            *reinterpret_cast<float2*>(mbuf + (warp * RB + 16 * mt + g + 8 * h) * C::MSTRIDE + 8 * nb + 2 * t4) =
-                make_float2(o[mt][pass * KB + nb][2 * h] * f[mt][h], o[mt][pass * KB + nb][2 * h + 1] * f[mt][h]);
+        for (int nb = 0; nb < KB; ++nb)
+          *reinterpret_cast<float2*>(mbuf + (warp * 16 + g + 8 * h) * C::MSTRIDE + 8 * nb + 2 * t4) =
+              make_float2(o[pass * KB + nb][2 * h] * f[h], o[pass * KB + nb][2 * h + 1] * f[h]);
       named_bar_sync(1, 32 * NWARP);
-      // thread: two output columns of one row
-      const int r = threadIdx.x / (C::MCOLS / 2), c2 = threadIdx.x % (C::MCOLS / 2);
-      if (r >= RB) continue;
-      int i0, i1, d;
-      if (FP8) {                                   // n-blocks 2y, 2y + 1 of column n: neighbours in d
-        const int n = c2 & 7, y = c2 >> 3;
-        i0 = 16 * y + n;
-        i1 = i0 + 8;
-        const int lt = n >> 1;
-        const int first = D == 128 ? 16 * (lt + 4 * (n & 1)) : 16 * (((lt & 1) << 1) | (lt >> 1)) + 8 * (n & 1);
-        d = first + pass * KB + 2 * y;
-      } else {
-        i0 = 2 * c2;
-        i1 = i0 + 1;
-        d = pass * C::MCOLS + 2 * c2;
-      }
-      float a = 0.f, b = 0.f;
 #pragma unroll
-      for (int w = 0; w < NWARP; ++w) {
-        a += mbuf[(w * RB + r) * C::MSTRIDE + i0];
-        b += mbuf[(w * RB + r) * C::MSTRIDE + i1];
-      }
-      const int pr = sg.rt * RB + r, t = pr / p.G;
-      if (t < ql) {
-        if (whole)
-          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
-                                       ((static_cast<long long>(sg.b) * p.T + t) * p.Hq + sg.hkv * p.G + pr % p.G) * D + d) =
-              pack_bf16x2(a, b);
-        else
-          *reinterpret_cast<float2*>(p.ws_o + (ws_slot * RB + r) * D + d) = make_float2(a, b);
+      for (int r0 = 0; r0 < RB; r0 += 16) {
+        // thread: two output columns of one row
+        const int r = r0 + static_cast<int>(threadIdx.x) / 16, c2 = threadIdx.x % 16;
+        int i0, i1, d;
+        if (FP8) {                                 // n-blocks 2y, 2y + 1 of column n: neighbours in d
+          const int n = c2 & 7, y = c2 >> 3;
+          i0 = 16 * y + n;
+          i1 = i0 + 8;
+          const int lt = n >> 1;
+          const int first = D == 128 ? 16 * (lt + 4 * (n & 1)) : 16 * (((lt & 1) << 1) | (lt >> 1)) + 8 * (n & 1);
+          d = first + pass * KB + 2 * y;
+        } else {
+          i0 = 2 * c2;
+          i1 = i0 + 1;
+          d = pass * C::MCOLS + 2 * c2;
+        }
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::PARTS; ++w) {
+          const float* src = mbuf + ((WIDE ? (r0 >> 4) * 4 : 0) + w) * 16 * C::MSTRIDE + (r & 15) * C::MSTRIDE;
+          a += src[i0];
+          b += src[i1];
+        }
+        const int pr = sg.rt * RB + r, t = pr / p.G;
+        if (t < ql) {
+          if (whole)
+            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
+                                         ((static_cast<long long>(sg.b) * p.T + t) * p.Hq + sg.hkv * p.G + pr % p.G) * D + d) =
+                pack_bf16x2(a, b);
+          else
+            *reinterpret_cast<float2*>(p.ws_o + (ws_slot * RB + r) * D + d) = make_float2(a, b);
+        }
       }
     }
     named_bar_sync(1, 32 * NWARP);                 // the next unit rewrites the shared arrays
@@ -788,20 +790,20 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p)
   }
 }
 
-template <int D, bool FP8, int MT>
+template <int D, bool FP8, bool WIDE>
 cudaError_t launch_paged_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, bool combine, cudaStream_t st) {
-  using C = PagedCfg<D, FP8, MT>;
+  using C = PagedCfg<D, FP8, WIDE>;
   static std::atomic<unsigned long long> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if ((configured.load() & bit) == 0) {
-    e = cudaFuncSetAttribute(attn_paged_kernel<D, FP8, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    e = cudaFuncSetAttribute(attn_paged_kernel<D, FP8, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  attn_paged_kernel<D, FP8, MT><<<p.n_cta, NTHREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
+  attn_paged_kernel<D, FP8, WIDE><<<p.n_cta, NTHREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess || !combine) return e;
   // the merge starts while the last CTAs finish and waits for them on the device
   cudaLaunchConfig_t cfg{};
@@ -818,8 +820,8 @@ cudaError_t launch_paged_d(const CUtensorMap& tk, const CUtensorMap& tv, const P
 
 template <int D, bool FP8>
 cudaError_t launch_paged_m(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, bool combine, cudaStream_t st) {
-  return paged_rows(p.G * p.T) == 16 ? launch_paged_d<D, FP8, 1>(tk, tv, p, combine, st)
-                                     : launch_paged_d<D, FP8, 2>(tk, tv, p, combine, st);
+  return paged_rows(p.G * p.T) == 16 ? launch_paged_d<D, FP8, false>(tk, tv, p, combine, st)
+                                     : launch_paged_d<D, FP8, true>(tk, tv, p, combine, st);
 }
 
 }  // namespace
