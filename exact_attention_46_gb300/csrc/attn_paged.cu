@@ -38,6 +38,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "cache.h"
 #include "ptx.cuh"
@@ -243,45 +244,58 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   if (warp == NWARP) {
     // ---- producer: page look-up and TMA ----
-    const int br = p.page_size < 128 ? p.page_size : 128;        // rows of one box
-    const int per_tile = 128 / br;
+    // Box i of the list of boxes of a segment is br rows of one page; lane i % 32 looks its page up,
+    // one batch of 32 boxes ahead of their use, and issues its copies.
+    const int ps_log = 31 - __clz(p.page_size);
+    const int br_log = ps_log < 7 ? ps_log : 7, br = 1 << br_log;
+    const int pt_log = 7 - br_log, per_tile = 1 << pt_log;       // boxes of a tile (1 .. 8)
     const uint64_t pol = l2_policy_evict_first();
     int it = 0;
     for (long long x = x0; x < x1;) {
       const Segment s = find_segment(p, pre, x, x1);
       const int L = __ldg(p.ctx_lens + s.b) + (p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T);
       const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
-      for (int j = s.t0; j < s.t1; ++j, ++it) {
-        // lane i < per_tile: box i of the tile
-        const int key = 128 * j + br * lane;
-        int page = -1;
-        const bool wanted = lane < per_tile && key < L;
-        if (wanted) page = __ldg(table + key / p.page_size);
+      // first key of this lane's box in the batch that starts at tile j, and its page (-1: past the end)
+      auto look_up = [&](int j) {
+        const int key = 128 * j + (lane << br_log);
+        return j < s.t1 && key < L ? __ldg(table + (key >> ps_log)) : -1;
+      };
+      const int batch = 32 >> pt_log;              // tiles of a batch
+      int next = look_up(s.t0);
+      for (int j0 = s.t0; j0 < s.t1; j0 += batch) {
+        const int page = next;
+        next = look_up(j0 + batch);
+        const int key = 128 * j0 + (lane << br_log);
+        const bool wanted = key < L && j0 + (lane >> pt_log) < s.t1;
         const bool good = wanted && page >= 0 && page < p.n_pages;
         if (wanted && !good && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_PAGE);
-        const unsigned boxes = __popc(__ballot_sync(0xffffffffu, good));
-        const int slot = it % NSTAGE;
-        const bool room = warp_wait(BAR_EMPTY(slot), ((it / NSTAGE) & 1) ^ 1u, ctl, WHERE_PAGED_LOAD);
-        if (!room) break;
-        if (lane == 0)
-          mbar_arrive_expect_tx(BAR_FULL(slot), boxes * br * (2u * C::ROW_BYTES + (FP8 ? 8u : 0u)));
-        __syncwarp();
-        if (good) {
-          const uint32_t sK = base_u32 + slot * C::STAGE_BYTES + br * lane * C::PANEL_ROW;
-          const int row = key % p.page_size;
+        const unsigned boxes = __ballot_sync(0xffffffffu, good);
+        const int row = key & (p.page_size - 1);
+        const long long e = (static_cast<long long>(page) * p.Hkv + s.hkv) * p.page_size + row;
+        for (int i = 0; i < batch && j0 + i < s.t1; ++i, ++it) {
+          const int slot = it % NSTAGE;
+          if (!warp_wait(BAR_EMPTY(slot), ((it / NSTAGE) & 1) ^ 1u, ctl, WHERE_PAGED_LOAD)) break;
+          const unsigned mine = (boxes >> (i << pt_log)) & ((1u << per_tile) - 1);
+          if (lane == 0)
+            mbar_arrive_expect_tx(BAR_FULL(slot), (__popc(mine) << br_log) * (2u * C::ROW_BYTES + (FP8 ? 8u : 0u)));
+          __syncwarp();
+          if (good && (lane >> pt_log) == i) {
+            const int box = lane & (per_tile - 1);
+            const uint32_t sK = base_u32 + slot * C::STAGE_BYTES + (box << br_log) * C::PANEL_ROW;
 #pragma unroll
-          for (int pn = 0; pn < C::NPANEL; ++pn) {
-            tma_load_4d(sK + pn * C::PANEL_BYTES, &tmK, BAR_FULL(slot), pn * (C::PANEL_ROW / C::ESZ), row, s.hkv, page, pol);
-            tma_load_4d(sK + C::TILE_BYTES + pn * C::PANEL_BYTES, &tmV, BAR_FULL(slot), pn * (C::PANEL_ROW / C::ESZ),
-                        row, s.hkv, page, pol);
-          }
-          if (FP8) {
-            const uint32_t sS = base_u32 + slot * C::STAGE_BYTES + 2 * C::TILE_BYTES + 4 * br * lane;
-            const long long e = (static_cast<long long>(page) * p.Hkv + s.hkv) * p.page_size + row;
-            bulk_load(sS, p.k_scale + e, 4 * br, BAR_FULL(slot), pol);
-            bulk_load(sS + 512, p.v_scale + e, 4 * br, BAR_FULL(slot), pol);
+            for (int pn = 0; pn < C::NPANEL; ++pn) {
+              tma_load_4d(sK + pn * C::PANEL_BYTES, &tmK, BAR_FULL(slot), pn * (C::PANEL_ROW / C::ESZ), row, s.hkv, page, pol);
+              tma_load_4d(sK + C::TILE_BYTES + pn * C::PANEL_BYTES, &tmV, BAR_FULL(slot), pn * (C::PANEL_ROW / C::ESZ),
+                          row, s.hkv, page, pol);
+            }
+            if (FP8) {
+              const uint32_t sS = base_u32 + slot * C::STAGE_BYTES + 2 * C::TILE_BYTES + (4 * box << br_log);
+              bulk_load(sS, p.k_scale + e, 4 * br, BAR_FULL(slot), pol);
+              bulk_load(sS + 512, p.v_scale + e, 4 * br, BAR_FULL(slot), pol);
+            }
           }
         }
+        if (*abort_flag) break;
       }
       if (*abort_flag) break;
       x += s.t1 - s.t0;
@@ -378,7 +392,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     float o[C::NB][4];
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    float vref = 0.f;                              // E4M3: power of two above the value scales seen
+    float vref = 0.f, vup = 0.f;                   // E4M3: power of two above the value scales seen, 2^10 / vref
 #pragma unroll
     for (int nb = 0; nb < C::NB; ++nb)
 #pragma unroll
@@ -390,9 +404,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // barrier whose phases it sees one by one
       const bool ok = warp_wait(BAR_FULL(slot), (it / NSTAGE) & 1, ctl, WHERE_PAGED_USE);
       const int k0 = 128 * j + kw;                 // first key of this warp
-      if (ok && k0 < L && (WIDE || (it & 1) == group)) {
+      // TAIL: the warp's keys hold drafted ones, or the end of the sequence
+      auto visit = [&](auto tail_c) {
+        constexpr bool TAIL = decltype(tail_c)::value;
         const uint32_t sK = base_u32 + slot * C::STAGE_BYTES, sV = sK + C::TILE_BYTES;
-        const bool tail = k0 + 32 > ctx;           // drafted keys, or the end of the sequence
         float s[4][4];
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb)
@@ -439,28 +454,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
           }
         }
-        // ---- scales of this thread's eight keys ----
-        float ksc[4][2], vsc[4][2];
+        // ---- scales of this thread's eight keys (pairs: columns 0, 1 of an n-block) ----
+        uint64_t ksc[4], vsc[4];
         uint32_t vbad = 0;                         // E4M3, tail: value rows past the end or without a finite scale
         if constexpr (FP8) {
           const float* sc = reinterpret_cast<const float*>(base + slot * C::STAGE_BYTES + 2 * C::TILE_BYTES) + kw;
-          float top = 0.f;
+          float top = 0.f, vs[4][2];
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb)
+          for (int nb = 0; nb < 4; ++nb) {
+            ksc[nb] = f2_pack(sc[key_of(nb, 0)], sc[key_of(nb, 1)]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              ksc[nb][e] = sc[key_of(nb, e)];
-              vsc[nb][e] = sc[128 + key_of(nb, e)];
-              if (tail) {
-                if (k0 + key_of(nb, e) >= L) vsc[nb][e] = 0.f;
-                if (!(vsc[nb][e] < INFINITY) || k0 + key_of(nb, e) >= L) vbad |= 1u << (2 * nb + e);
+              vs[nb][e] = sc[128 + key_of(nb, e)];
+              if (TAIL) {
+                if (k0 + key_of(nb, e) >= L) vs[nb][e] = 0.f;
+                if (!(vs[nb][e] < INFINITY) || k0 + key_of(nb, e) >= L) vbad |= 1u << (2 * nb + e);
+                top = fmaxf(top, vs[nb][e] < INFINITY ? vs[nb][e] : 0.f);
               }
-              top = fmaxf(top, vsc[nb][e] < INFINITY ? vsc[nb][e] : 0.f);
             }
+            if (!TAIL) top = max3(top, vs[nb][0], vs[nb][1]);
+          }
           if (__any_sync(0xffffffffu, top > vref)) {
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // next power of two above; an infinite or NaN scale goes to the rows that see it only
+            // next power of two above
             const float nref = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + (top < 0x1p126f ? 0x00800000u : 0u));
             const float f = vref / nref;
 #pragma unroll
@@ -468,34 +485,43 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[nb][i] *= f;
             vref = nref;
+            vup = 1024.f / nref;
           }
-          const float up = vref > 0.f ? 1024.f / vref : 0.f;     // numerators times 2^10 at the largest scale
+          const uint64_t up = f2_pack(vup, vup);
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) vsc[nb][e] *= up;
+          for (int nb = 0; nb < 4; ++nb) vsc[nb] = f2_mul(f2_pack(vs[nb][0], vs[nb][1]), up);
         }
-        // ---- logits, mask, running maximum ----
+        // ---- logits (before the row's multiplier cr, which is positive), mask, running maximum ----
+        uint64_t xs[2][4];
         float mt_max[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float mx = -INFINITY;
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb)
+          for (int nb = 0; nb < 4; ++nb) {
+            xs[h][nb] = f2_pack(s[nb][2 * h], s[nb][2 * h + 1]);
+            if (FP8) xs[h][nb] = f2_mul(xs[h][nb], ksc[nb]);
+            if (TAIL) {
+              float v[2];
+              f2_unpack(xs[h][nb], v[0], v[1]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float v = s[nb][2 * h + e] * (FP8 ? cr[h] * ksc[nb][e] : cr[h]);
-              if (tail) {
+              for (int e = 0; e < 2; ++e) {
                 const int key = k0 + key_of(nb, e);
                 const bool sees = key < ctx || (key < L && ((bits[rlo + g + 8 * h] >> (key - ctx)) & 1));
-                v = sees ? v : -INFINITY;
+                v[e] = sees ? v[e] : -INFINITY;
               }
-              s[nb][2 * h + e] = v;
-              mx = fmaxf(mx, v);
+              xs[h][nb] = f2_pack(v[0], v[1]);
             }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb) {
+            float v0, v1;
+            f2_unpack(xs[h][nb], v0, v1);
+            mx = max3(mx, v0, v1);
+          }
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mt_max[h] = mx;
+          mt_max[h] = mx * cr[h];
         }
         if (__any_sync(0xffffffffu, mt_max[0] > m_run[0] + 4.f || mt_max[1] > m_run[1] + 4.f)) {
           // lazily: O and the sum are only rescaled when some maximum moved by a factor of 2^4
@@ -518,22 +544,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           uint32_t w[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float off = m_run[h] == -INFINITY ? 0.f : m_run[h];
+            const float off = m_run[h] == -INFINITY ? 0.f : -m_run[h];
+            const uint64_t off2 = f2_pack(off, off), cr2 = f2_pack(cr[h], cr[h]);
+            uint64_t sum = f2_pack(l_run[h], 0.f);
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb) {
-              float q0 = ex2(s[nb][2 * h] - off), q1 = ex2(s[nb][2 * h + 1] - off);
-              l_run[h] += q0 + q1;
+              float q0, q1;
+              f2_unpack(f2_fma(xs[h][nb], cr2, off2), q0, q1);
+              q0 = ex2(q0);
+              q1 = ex2(q1);
+              const uint64_t q = f2_pack(q0, q1);
+              sum = f2_add(sum, q);
               if constexpr (FP8) {
-                // a hidden key's scale may be anything: its numerator is 0 whatever it is
-                q0 = tail && q0 == 0.f ? 0.f : q0 * vsc[nb][0];
-                q1 = tail && q1 == 0.f ? 0.f : q1 * vsc[nb][1];
-                w[h][nb] = pack_f16x2(q0, q1);
+                float y0, y1;
+                f2_unpack(f2_mul(q, vsc[nb]), y0, y1);
+                if (TAIL) {                        // a hidden key's scale may be anything: its numerator is 0
+                  y0 = q0 == 0.f ? 0.f : y0;
+                  y1 = q1 == 0.f ? 0.f : y1;
+                }
+                w[h][nb] = pack_f16x2(y0, y1);
               } else {
                 s[nb][2 * h] = q0;
                 s[nb][2 * h + 1] = q1;
                 w[h][nb] = pack_bf16x2(q0, q1);
               }
             }
+            float l0, l1;
+            f2_unpack(sum, l0, l1);
+            l_run[h] = l0 + l1;
           }
           pa[0] = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
           pa[1] = make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]);
@@ -541,7 +579,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // ---- O += P V ----
         if constexpr (!FP8) {
           uint32_t odd = 0;                        // value rows past the end, or not finite: out of the product
-          if (tail) {
+          if (TAIL) {
             for (int r = 0; r < 32; ++r) {
               bool strange = k0 + r >= L;
               if (!strange && k0 + r >= ctx) {
@@ -607,7 +645,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 mma16816<false>(o[nb + 1], pa[kk], vf[2], vf[3]);
               }
           };
-          if (odd != 0) add(true);
+          if (TAIL && odd != 0) add(true);
           else add(false);
         } else {
           // lane g reads D / 8 bytes of rows t, t + 4, t + 8, t + 12 of each 16 -- the keys of S's
@@ -628,7 +666,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const uint2 u = lds64(sV + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) + 8 * (g & 1));
                 w[i][0] = u.x; w[i][1] = u.y;
               }
-              if (tail && ((vbad >> (4 * kk + i)) & 1)) {
+              if (TAIL && ((vbad >> (4 * kk + i)) & 1)) {
 #pragma unroll
                 for (int c = 0; c < NW; ++c) w[i][c] = 0u;
               }
@@ -647,6 +685,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               }
           }
         }
+      };
+      if (ok && k0 < L && (WIDE || (it & 1) == group)) {
+        if (k0 + 32 > ctx) visit(std::true_type{});
+        else visit(std::false_type{});
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR_EMPTY(slot));
