@@ -52,10 +52,11 @@ constexpr int NWARP = 8;                        // consumer warps
 constexpr int NTHREADS = 32 * (NWARP + 1);
 enum : int { WHERE_PAGED_LOAD = 51, WHERE_PAGED_USE = 52, WHERE_PAGED_LENS = 53, WHERE_PAGED_PAGE = 54 };
 
-// WIDE: 32 rows per unit, one warp group per 16; otherwise 16 rows, the groups take turns by tile.
-template <int D, bool FP8, bool WIDE>
+// NRB: 8-row blocks of a warp (1, 2).  WIDE: a warp group per 16 of 32 rows; otherwise the two
+// groups take the same rows and turns by tile.
+template <int D, bool FP8, int NRB, bool WIDE>
 struct PagedCfg {
-  static constexpr int RB = WIDE ? 32 : 16;
+  static constexpr int RW = 8 * NRB, RB = WIDE ? 2 * RW : RW;
   static constexpr int ESZ = FP8 ? 1 : 2;
   static constexpr int ROW_BYTES = D * ESZ;
   static constexpr int PANEL_ROW = ROW_BYTES >= 128 ? 128 : ROW_BYTES;
@@ -64,22 +65,20 @@ struct PagedCfg {
   static constexpr int TILE_BYTES = 128 * ROW_BYTES;
   static constexpr int SCALE_BYTES = FP8 ? 2 * 128 * 4 : 0;
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES + SCALE_BYTES;
-  static constexpr int KS = D / 16;                          // k-steps of Q K^T
-  static constexpr int NB = D / 8;                           // n-blocks of O
+  static constexpr int KS = D / 16;                          // k-steps of K Q^T
+  static constexpr int MB = D / 16;                          // 16-row blocks of O^T
   static constexpr int PARTS = WIDE ? 4 : 8;                 // warps that hold a part of a row
-  static constexpr int MCOLS = 32;                           // columns merged at a time
-  static constexpr int MSTRIDE = MCOLS + 8;
-  static constexpr int Q_BYTES = RB / 16 * KS * 32 * 16;
-  static constexpr int REST = 1024 + Q_BYTES + NWARP * 16 * MSTRIDE * 4 + NWARP * 16 * 8 + RB * 12 +
-                              (PAGED_MAX_BATCH + 2) * 4 + 16 * 16 + 64;
+  static constexpr int MCOLS = 32, MSTRIDE = MCOLS + 4;      // columns merged at a time
+  static constexpr int Q_BYTES = RB / 8 * KS * 32 * 8;
+  static constexpr int M_BYTES = NWARP * RW * MSTRIDE * 4;
+  static constexpr int REST = 1024 + Q_BYTES + M_BYTES + NWARP * RW * 8 + RB * 12 + (PAGED_MAX_BATCH + 2) * 4 + 16 * 16 + 64;
   static constexpr int FIT = (227 * 1024 - REST) / STAGE_BYTES, WANT = 196608 / (2 * TILE_BYTES);
   static constexpr int NSTAGE = FIT < WANT ? FIT : WANT;     // up to 192 KB of K/V in flight
-  static constexpr int Q_OFF = NSTAGE * STAGE_BYTES;
-  static constexpr int M_OFF = Q_OFF + Q_BYTES;              // merge buffer [NWARP][16][MSTRIDE]
-  static constexpr int M_BYTES = NWARP * 16 * MSTRIDE * 4;
-  static constexpr int ML_OFF = M_OFF + M_BYTES;             // [NWARP][16] (max, sum)
-  static constexpr int BITS_OFF = ML_OFF + NWARP * 16 * 8;   // [RB] visible drafts
-  static constexpr int RQ_OFF = BITS_OFF + RB * 8;           // [RB] power of two of a query row
+  static constexpr int Q_OFF = NSTAGE * STAGE_BYTES;         // query fragments [RB / 8][KS][32] x 8 bytes
+  static constexpr int M_OFF = Q_OFF + Q_BYTES;              // merge buffer [NWARP][RW][MSTRIDE]
+  static constexpr int ML_OFF = M_OFF + M_BYTES;             // [NWARP][RW] (max, sum)
+  static constexpr int BITS_OFF = ML_OFF + NWARP * RW * 8;   // [RB] visible drafts
+  static constexpr int RQ_OFF = BITS_OFF + RB * 8;           // [RB] largest magnitude of a query row (bits)
   static constexpr int PRE_OFF = RQ_OFF + RB * 4;            // [PAGED_MAX_BATCH + 1] tile prefix
   static constexpr int BAR_OFF = PRE_OFF + (PAGED_MAX_BATCH + 2) * 4;
   static constexpr int SMEM_BYTES = 1024 + BAR_OFF + 2 * NSTAGE * 8 + 64;
@@ -107,6 +106,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 template <bool F16>
@@ -204,12 +209,12 @@ __device__ __forceinline__ Segment find_segment(const PagedParams& p, const int*
 
 __device__ __forceinline__ long long cta_start(long long i, long long W, long long N) { return i * W / N; }
 
-template <int D, bool FP8, bool WIDE>
+template <int D, bool FP8, int NRB, bool WIDE>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const PagedParams p) {
-  using C = PagedCfg<D, FP8, WIDE>;
-  constexpr int RB = C::RB, NSTAGE = C::NSTAGE;
+  using C = PagedCfg<D, FP8, NRB, WIDE>;
+  constexpr int RB = C::RB, RW = C::RW, NSTAGE = C::NSTAGE;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
@@ -310,93 +315,121 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   // the unit's row halves (WIDE) or every other tile ----
   const int g = lane >> 2, t4 = lane & 3;
   const int kw = 32 * (warp & 3), group = warp >> 2;
-  const int rlo = WIDE ? 16 * group : 0;         // first row of this warp
-  uint4* qfrag = reinterpret_cast<uint4*>(base + C::Q_OFF);
+  const int rlo = WIDE ? RW * group : 0;         // first row of this warp
+  uint2* qfrag = reinterpret_cast<uint2*>(base + C::Q_OFF);
   float* mbuf = reinterpret_cast<float*>(base + C::M_OFF);
   float2* ml = reinterpret_cast<float2*>(base + C::ML_OFF);
   unsigned long long* bits = reinterpret_cast<unsigned long long*>(base + C::BITS_OFF);
-  float* rq = reinterpret_cast<float*>(base + C::RQ_OFF);
-  // key (within the warp's 32) of column e of n-block nb of this thread's S
-  auto key_of = [&](int nb, int e) { return FP8 ? 8 * nb + t4 + 4 * e : 8 * nb + 2 * t4 + e; };
-  int it = 0;
-  for (long long x = x0; x < x1;) {
-    const Segment sg = find_segment(p, pre, x, x1);
-    const int ctx = __ldg(p.ctx_lens + sg.b), ql = p.q_lens != nullptr ? __ldg(p.q_lens + sg.b) : p.T;
-    const int L = ctx + ql;
+  int* qmax = reinterpret_cast<int*>(base + C::RQ_OFF);
+  // key (within 8) that row g of an S^T block stands for.  E4M3: with the swizzle, the two rows that
+  // eight lanes read at once then lie in different banks
+  const int kg = FP8 ? (g >> 1) + 4 * (g & 1) : g;
+  auto key_of = [&](int kb, int y) { return 16 * kb + 8 * y + kg; };
+
+  // What a segment needs from memory before its first tile, fetched while the last one ends: its
+  // lengths, query elements (item i of a thread: B registers of lane i % 32, k-step, 8-row block)
+  // and visible drafts.
+  constexpr int QI = RB / 8 * C::KS * 32 / (32 * NWARP);
+  static_assert(QI >= 1 || RB / 8 * C::KS * 32 == 128, "query items");
+  constexpr int QN = QI > 0 ? QI : 1;
+  Segment sg;
+  int ctx, ql;
+  uint2 qraw[QN];
+  unsigned long long my_bits;
+  auto fetch = [&](long long x) {
+    sg = find_segment(p, pre, x, x1);
+    ctx = __ldg(p.ctx_lens + sg.b);
+    ql = p.q_lens != nullptr ? __ldg(p.q_lens + sg.b) : p.T;
     const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q) +
                               (static_cast<long long>(sg.b) * p.T * p.Hq + static_cast<long long>(sg.hkv) * p.G) * D;
-    auto row_ptr = [&](int r) -> const __nv_bfloat16* {          // packed row of the tile, or null
-      const int pr = sg.rt * RB + r, t = pr / p.G;
-      return t < ql ? qb + (static_cast<long long>(t) * p.Hq + pr % p.G) * D : nullptr;
-    };
-    // the last segment's readers of the shared arrays below are past them (barrier at its end).
-    // Query fragments: entry (16-row block, k-step, lane) holds the A registers of that lane
-    if (FP8) {
-      // per-row power of two that brings the largest element into [1, 2): exact, and the logit
-      // multiplier takes it back
-      for (int r = warp; r < RB; r += NWARP) {
-        const __nv_bfloat16* src = row_ptr(r);
-        float m = 0.f;
-        if (src != nullptr)
-          for (int d = 2 * lane; d < D; d += 64) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(src + d));
-            m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        int ex = static_cast<int>(__float_as_uint(m) >> 23) - 127;
-        ex = ex < -110 ? -110 : (ex > 110 ? 110 : ex);
-        if (lane == 0) rq[r] = __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+    for (int i = 0; i < QN; ++i) {
+      const int e = static_cast<int>(threadIdx.x) + i * 32 * NWARP;
+      const int l = e & 31, ks = (e >> 5) % C::KS, rb = (e >> 5) / C::KS;
+      const int pr = sg.rt * RB + 8 * rb + (l >> 2), t = pr / p.G;
+      qraw[i] = make_uint2(0u, 0u);
+      if (rb < RB / 8 && t < p.T) {                // rows past q_len are computed and not written
+        const __nv_bfloat16* src = qb + (static_cast<long long>(t) * p.Hq + pr % p.G) * D;
+        // bf16: k = 2t, 2t + 1 and 2t + 8, 2t + 9 of the step; E4M3: four elements in a row, the order in
+        // which a thread reads the key's bytes
+        if (FP8) {
+          qraw[i] = *reinterpret_cast<const uint2*>(src + 16 * ((l & 3) + 4 * (ks >> 2)) + 4 * (ks & 3));
+        } else {
+          qraw[i].x = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * (l & 3));
+          qraw[i].y = *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * (l & 3) + 8);
+        }
+      }
+    }
+    my_bits = 0;
+    if (threadIdx.x < RB) {
+      const int t = (sg.rt * RB + static_cast<int>(threadIdx.x)) / p.G;
+      if (t < p.T)
+        my_bits = p.tree_mask != nullptr ? __ldg(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
+                                         : (t >= 63 ? ~0ull : (2ull << t) - 1);
+    }
+  };
+  if (threadIdx.x < RB) qmax[threadIdx.x] = 0;
+  fetch(x0);
+  named_bar_sync(1, 32 * NWARP);
+  int it = 0;
+  for (long long x = x0; x < x1;) {
+    const int L = ctx + ql;
+    if (FP8) {
+#pragma unroll
+      for (int i = 0; i < QN; ++i) {
+        const int e = static_cast<int>(threadIdx.x) + i * 32 * NWARP;
+        const int rb = (e >> 5) / C::KS;
+        float m = fmaxf(fmaxf(fabsf(__uint_as_float(qraw[i].x << 16)), fabsf(__uint_as_float(qraw[i].x & 0xffff0000u))),
+                        fmaxf(fabsf(__uint_as_float(qraw[i].y << 16)), fabsf(__uint_as_float(qraw[i].y & 0xffff0000u))));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (t4 == 0 && rb < RB / 8) atomicMax(qmax + 8 * rb + g, __float_as_int(m));   // m >= 0: ordered as integers
       }
       named_bar_sync(1, 32 * NWARP);
     }
-    for (int i = threadIdx.x; i < RB / 16 * C::KS * 32; i += 32 * NWARP) {
-      const int l = i & 31, ks = (i >> 5) % C::KS, mt = (i >> 5) / C::KS;
-      const int lg = l >> 2, lt = l & 3;
-      uint32_t a[4];
+    // per-row power of two that brings the largest query element into [1, 2): exact, and the logit
+    // multiplier takes it back
+    auto row_pow2 = [&](int r) {
+      int ex = (qmax[r] >> 23) - 127;
+      ex = ex < -110 ? -110 : (ex > 110 ? 110 : ex);
+      return __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+    };
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = 16 * mt + lg + 8 * h;
-        const __nv_bfloat16* src = row_ptr(r);
-        uint32_t lo = 0, hi = 0;
-        if (src != nullptr) {
-          // bf16: k = 2t, 2t + 1 and 2t + 8, 2t + 9 of the step; E4M3: four elements in a row, the
-          // order in which a thread reads the key's bytes
-          const int d = FP8 ? 16 * (lt + 4 * (ks >> 2)) + 4 * (ks & 3) : 16 * ks + 2 * lt;
-          lo = *reinterpret_cast<const uint32_t*>(src + d);
-          hi = *reinterpret_cast<const uint32_t*>(src + d + (FP8 ? 2 : 8));
-          if (FP8) {
-            const float inv = 1.f / rq[r];
-            lo = pack_f16x2(__uint_as_float(lo << 16) * inv, __uint_as_float(lo & 0xffff0000u) * inv);
-            hi = pack_f16x2(__uint_as_float(hi << 16) * inv, __uint_as_float(hi & 0xffff0000u) * inv);
-          }
-        }
-        a[h] = lo;
-        a[2 + h] = hi;
+    for (int i = 0; i < QN; ++i) {
+      const int e = static_cast<int>(threadIdx.x) + i * 32 * NWARP;
+      uint2 v = qraw[i];
+      if ((e >> 5) / C::KS >= RB / 8) break;
+      if (FP8) {
+        const float inv = 1.f / row_pow2(8 * ((e >> 5) / C::KS) + g);
+        v.x = pack_f16x2(__uint_as_float(v.x << 16) * inv, __uint_as_float(v.x & 0xffff0000u) * inv);
+        v.y = pack_f16x2(__uint_as_float(v.y << 16) * inv, __uint_as_float(v.y & 0xffff0000u) * inv);
       }
-      qfrag[i] = make_uint4(a[0], a[1], a[2], a[3]);
+      qfrag[e] = v;
     }
-    if (threadIdx.x < RB) {
-      const int t = (sg.rt * RB + static_cast<int>(threadIdx.x)) / p.G;
-      unsigned long long m = 0;
-      if (t < ql)
-        m = p.tree_mask != nullptr ? __ldg(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
-                                   : (t >= 63 ? ~0ull : (2ull << t) - 1);
-      bits[threadIdx.x] = m;
-    }
+    if (threadIdx.x < RB) bits[threadIdx.x] = my_bits;
     named_bar_sync(1, 32 * NWARP);
-    float cr[2];                                   // logit multiplier of rows g, g + 8
+    // rows of this thread: rlo + 8 rb + 2 t4 + e; everything per row is a pair (e = 0, 1)
+    uint64_t cr[NRB];                              // logit multipliers
 #pragma unroll
-    for (int h = 0; h < 2; ++h) cr[h] = FP8 ? p.c_log2 * rq[rlo + g + 8 * h] : p.c_log2;
-    const uint4* qf = qfrag + (WIDE ? group : 0) * C::KS * 32 + lane;
+    for (int rb = 0; rb < NRB; ++rb) {
+      const int r = rlo + 8 * rb + 2 * t4;
+      cr[rb] = FP8 ? f2_pack(p.c_log2 * row_pow2(r), p.c_log2 * row_pow2(r + 1)) : f2_pack(p.c_log2, p.c_log2);
+    }
+    const uint2* qf = qfrag + (WIDE ? group * NRB : 0) * C::KS * 32 + lane;
 
-    float o[C::NB][4];
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    float o[NRB][C::MB][4];                        // O^T: (d, row 2t), (d, 2t + 1), (d', 2t), (d', 2t + 1)
+    float m_run[NRB][2];
+    uint64_t l_run[NRB];
     float vref = 0.f, vup = 0.f;                   // E4M3: power of two above the value scales seen, 2^10 / vref
 #pragma unroll
-    for (int nb = 0; nb < C::NB; ++nb)
+    for (int rb = 0; rb < NRB; ++rb) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[nb][i] = 0.f;
+      for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[rb][mb][i] = 0.f;
+      m_run[rb][0] = m_run[rb][1] = -INFINITY;
+      l_run[rb] = f2_pack(0.f, 0.f);
+    }
 
     for (int j = sg.t0; j < sg.t1; ++j, ++it) {
       const int slot = it % NSTAGE;
@@ -408,175 +441,173 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       auto visit = [&](auto tail_c) {
         constexpr bool TAIL = decltype(tail_c)::value;
         const uint32_t sK = base_u32 + slot * C::STAGE_BYTES, sV = sK + C::TILE_BYTES;
-        float s[4][4];
+        float s[2][NRB][4];                        // S^T of 16 keys: (key g, rows 2t, 2t + 1), (key g + 8, ..)
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[nb][i] = 0.f;
-        // ---- S = Q K^T ----
+          for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[kb][rb][i] = 0.f;
+        // ---- S^T = K Q^T ----
         if constexpr (!FP8) {
-          const int r = kw + (lane & 7) + 8 * (lane >> 4), half = (lane >> 3) & 1;
+          const int r = kw + (lane & 15), half = lane >> 4;
 #pragma unroll
           for (int ks = 0; ks < C::KS; ++ks) {
-            uint32_t kf[2][4];
+            uint2 q[NRB];
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-              ldsm4(sK + (ks >> 2) * C::PANEL_BYTES + (r + 16 * y) * 128 + (((2 * (ks & 3) + half) ^ (r & 7)) << 4), kf[y]);
-            const uint4 a = qf[ks * 32];
+            for (int rb = 0; rb < NRB; ++rb) q[rb] = qf[(rb * C::KS + ks) * 32];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              mma16816<false>(s[2 * y], a, kf[y][0], kf[y][1]);
-              mma16816<false>(s[2 * y + 1], a, kf[y][2], kf[y][3]);
+            for (int kb = 0; kb < 2; ++kb) {
+              uint32_t a[4];
+              ldsm4(sK + (ks >> 2) * C::PANEL_BYTES + (r + 16 * kb) * 128 + (((2 * (ks & 3) + half) ^ (r & 7)) << 4), a);
+#pragma unroll
+              for (int rb = 0; rb < NRB; ++rb)
+                mma16816<false>(s[kb][rb], make_uint4(a[0], a[1], a[2], a[3]), q[rb].x, q[rb].y);
             }
           }
         } else {
-          // S's column n of an n-block is key (n >> 1) + 4 (n & 1): with the swizzle, the two rows
-          // that eight lanes read at once then lie in different banks
-          const int rg = (g >> 1) + 4 * (g & 1);
 #pragma unroll
           for (int i = 0; i < C::KS / 4; ++i) {
-            uint4 w[4];
+            uint4 w[2][2];
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-              const int r = kw + 8 * nb + rg;
-              const int ch = C::PANEL_ROW == 128 ? ((t4 + 4 * i) ^ rg) : (t4 ^ ((r >> 1) & 3));
-              w[nb] = lds128(sK + r * C::PANEL_ROW + 16 * ch);
-            }
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int r = kw + key_of(kb, y);
+                const int ch = C::PANEL_ROW == 128 ? ((t4 + 4 * i) ^ kg) : (t4 ^ ((r >> 1) & 3));
+                w[kb][y] = lds128(sK + r * C::PANEL_ROW + 16 * ch);
+              }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint4 a = qf[(4 * i + c) * 32];
+              uint2 q[NRB];
 #pragma unroll
-              for (int nb = 0; nb < 4; ++nb) {
-                uint32_t b0, b1;
-                e4m3x4_to_f16(c == 0 ? w[nb].x : (c == 1 ? w[nb].y : (c == 2 ? w[nb].z : w[nb].w)), b0, b1);
-                mma16816<true>(s[nb], a, b0, b1);
+              for (int rb = 0; rb < NRB; ++rb) q[rb] = qf[(rb * C::KS + 4 * i + c) * 32];
+#pragma unroll
+              for (int kb = 0; kb < 2; ++kb) {
+                uint4 a;
+                e4m3x4_to_f16(c == 0 ? w[kb][0].x : (c == 1 ? w[kb][0].y : (c == 2 ? w[kb][0].z : w[kb][0].w)), a.x, a.z);
+                e4m3x4_to_f16(c == 0 ? w[kb][1].x : (c == 1 ? w[kb][1].y : (c == 2 ? w[kb][1].z : w[kb][1].w)), a.y, a.w);
+#pragma unroll
+                for (int rb = 0; rb < NRB; ++rb) mma16816<true>(s[kb][rb], a, q[rb].x, q[rb].y);
               }
             }
           }
         }
-        // ---- scales of this thread's eight keys (pairs: columns 0, 1 of an n-block) ----
-        uint64_t ksc[4], vsc[4];
-        uint32_t vbad = 0;                         // E4M3, tail: value rows past the end or without a finite scale
+        // ---- scales of this thread's four keys ----
+        float ksc[2][2], vsc[2][2];
         if constexpr (FP8) {
           const float* sc = reinterpret_cast<const float*>(base + slot * C::STAGE_BYTES + 2 * C::TILE_BYTES) + kw;
-          float top = 0.f, vs[4][2];
+          float top = 0.f;
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb) {
-            ksc[nb] = f2_pack(sc[key_of(nb, 0)], sc[key_of(nb, 1)]);
+          for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              vs[nb][e] = sc[128 + key_of(nb, e)];
-              if (TAIL) {
-                if (k0 + key_of(nb, e) >= L) vs[nb][e] = 0.f;
-                if (!(vs[nb][e] < INFINITY) || k0 + key_of(nb, e) >= L) vbad |= 1u << (2 * nb + e);
-                top = fmaxf(top, vs[nb][e] < INFINITY ? vs[nb][e] : 0.f);
-              }
+            for (int y = 0; y < 2; ++y) {
+              ksc[kb][y] = sc[key_of(kb, y)];
+              vsc[kb][y] = sc[128 + key_of(kb, y)];
+              // an infinite or NaN scale goes to the rows that see it only
+              if (TAIL && k0 + key_of(kb, y) >= L) vsc[kb][y] = 0.f;
+              top = fmaxf(top, !TAIL || vsc[kb][y] < INFINITY ? vsc[kb][y] : 0.f);
             }
-            if (!TAIL) top = max3(top, vs[nb][0], vs[nb][1]);
-          }
           if (__any_sync(0xffffffffu, top > vref)) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
             // next power of two above
             const float nref = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + (top < 0x1p126f ? 0x00800000u : 0u));
             const float f = vref / nref;
 #pragma unroll
-            for (int nb = 0; nb < C::NB; ++nb)
+            for (int rb = 0; rb < NRB; ++rb)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[nb][i] *= f;
+              for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[rb][mb][i] *= f;
             vref = nref;
             vup = 1024.f / nref;
           }
-          const uint64_t up = f2_pack(vup, vup);
-#pragma unroll
-          for (int nb = 0; nb < 4; ++nb) vsc[nb] = f2_mul(f2_pack(vs[nb][0], vs[nb][1]), up);
         }
-        // ---- logits (before the row's multiplier cr, which is positive), mask, running maximum ----
-        uint64_t xs[2][4];
-        float mt_max[2];
+        // ---- logits (before the row's multiplier, which is positive), mask, running maximum ----
+        uint64_t xs[NRB][2][2];
+        float top2[NRB][2];
+        bool grow = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int rb = 0; rb < NRB; ++rb) {
+          float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-          for (int nb = 0; nb < 4; ++nb) {
-            xs[h][nb] = f2_pack(s[nb][2 * h], s[nb][2 * h + 1]);
-            if (FP8) xs[h][nb] = f2_mul(xs[h][nb], ksc[nb]);
-            if (TAIL) {
-              float v[2];
-              f2_unpack(xs[h][nb], v[0], v[1]);
+          for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int key = k0 + key_of(nb, e);
-                const bool sees = key < ctx || (key < L && ((bits[rlo + g + 8 * h] >> (key - ctx)) & 1));
-                v[e] = sees ? v[e] : -INFINITY;
+            for (int y = 0; y < 2; ++y) {
+              uint64_t v = f2_pack(s[kb][rb][2 * y], s[kb][rb][2 * y + 1]);
+              if (FP8) v = f2_mul(v, f2_pack(ksc[kb][y], ksc[kb][y]));
+              float v0, v1;
+              f2_unpack(v, v0, v1);
+              if (TAIL) {
+                const int key = k0 + key_of(kb, y);
+                const int r = rlo + 8 * rb + 2 * t4;
+                const bool in = key < L;
+                v0 = key < ctx || (in && ((bits[r] >> (key - ctx)) & 1)) ? v0 : -INFINITY;
+                v1 = key < ctx || (in && ((bits[r + 1] >> (key - ctx)) & 1)) ? v1 : -INFINITY;
               }
-              xs[h][nb] = f2_pack(v[0], v[1]);
+              xs[rb][kb][y] = f2_pack(v0, v1);
+              m0 = fmaxf(m0, v0);
+              m1 = fmaxf(m1, v1);
             }
-          }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int nb = 0; nb < 4; ++nb) {
-            float v0, v1;
-            f2_unpack(xs[h][nb], v0, v1);
-            mx = max3(mx, v0, v1);
-          }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          mt_max[h] = mx * cr[h];
+          f2_unpack(f2_mul(f2_pack(m0, m1), cr[rb]), top2[rb][0], top2[rb][1]);
+          grow = grow || top2[rb][0] > m_run[rb][0] + 4.f || top2[rb][1] > m_run[rb][1] + 4.f;
         }
-        if (__any_sync(0xffffffffu, mt_max[0] > m_run[0] + 4.f || mt_max[1] > m_run[1] + 4.f)) {
-          // lazily: O and the sum are only rescaled when some maximum moved by a factor of 2^4
+        if (__any_sync(0xffffffffu, grow)) {
+          // lazily: the maxima are only looked up over the lanes, and O and the sum rescaled, when some
+          // logit lies a factor of 2^4 above its row's reference
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float mn = fmaxf(m_run[h], mt_max[h]);
-            const float f = m_run[h] == -INFINITY ? 0.f : ex2(m_run[h] - mn);
-            m_run[h] = mn;
-            l_run[h] *= f;
+          for (int rb = 0; rb < NRB; ++rb) {
+            float f[2];
 #pragma unroll
-            for (int nb = 0; nb < C::NB; ++nb) {
-              o[nb][2 * h] *= f;
-              o[nb][2 * h + 1] *= f;
+            for (int e = 0; e < 2; ++e) {
+              float mx = top2[rb][e];
+#pragma unroll
+              for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+              const float mn = fmaxf(m_run[rb][e], mx);
+              f[e] = m_run[rb][e] == -INFINITY ? 0.f : ex2(m_run[rb][e] - mn);
+              m_run[rb][e] = mn;
             }
+            l_run[rb] = f2_mul(l_run[rb], f2_pack(f[0], f[1]));
+#pragma unroll
+            for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[rb][mb][i] *= f[i & 1];
           }
         }
-        // ---- numerators ----
-        uint4 pa[2];
-        {
-          uint32_t w[2][4];
+        // ---- numerators, and their blocks turned into B operands (keys along k) ----
+        uint32_t pb[NRB][2][2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float off = m_run[h] == -INFINITY ? 0.f : -m_run[h];
-            const uint64_t off2 = f2_pack(off, off), cr2 = f2_pack(cr[h], cr[h]);
-            uint64_t sum = f2_pack(l_run[h], 0.f);
+        for (int rb = 0; rb < NRB; ++rb) {
+          const uint64_t off = f2_pack(m_run[rb][0] == -INFINITY ? 0.f : -m_run[rb][0],
+                                       m_run[rb][1] == -INFINITY ? 0.f : -m_run[rb][1]);
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
               float q0, q1;
-              f2_unpack(f2_fma(xs[h][nb], cr2, off2), q0, q1);
+              f2_unpack(f2_fma(xs[rb][kb][y], cr[rb], off), q0, q1);
               q0 = ex2(q0);
               q1 = ex2(q1);
               const uint64_t q = f2_pack(q0, q1);
-              sum = f2_add(sum, q);
+              l_run[rb] = f2_add(l_run[rb], q);
               if constexpr (FP8) {
+                const float vs = vsc[kb][y] * vup;
                 float y0, y1;
-                f2_unpack(f2_mul(q, vsc[nb]), y0, y1);
+                f2_unpack(f2_mul(q, f2_pack(vs, vs)), y0, y1);
                 if (TAIL) {                        // a hidden key's scale may be anything: its numerator is 0
                   y0 = q0 == 0.f ? 0.f : y0;
                   y1 = q1 == 0.f ? 0.f : y1;
                 }
-                w[h][nb] = pack_f16x2(y0, y1);
+                pb[rb][kb][y] = transpose8x8(pack_f16x2(y0, y1));
               } else {
-                s[nb][2 * h] = q0;
-                s[nb][2 * h + 1] = q1;
-                w[h][nb] = pack_bf16x2(q0, q1);
+                s[kb][rb][2 * y] = q0;
+                s[kb][rb][2 * y + 1] = q1;
+                pb[rb][kb][y] = transpose8x8(pack_bf16x2(q0, q1));
               }
             }
-            float l0, l1;
-            f2_unpack(sum, l0, l1);
-            l_run[h] = l0 + l1;
-          }
-          pa[0] = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
-          pa[1] = make_uint4(w[0][2], w[1][2], w[0][3], w[1][3]);
         }
-        // ---- O += P V ----
+        // ---- O^T += V^T P^T ----
         if constexpr (!FP8) {
           uint32_t odd = 0;                        // value rows past the end, or not finite: out of the product
           if (TAIL) {
@@ -597,30 +628,33 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const uint32_t seen = k0 + 32 <= L ? odd : odd & ((1u << (L - k0)) - 1);
             if (seen != 0) {
 #pragma unroll
-              for (int rb = 0; rb < 4; ++rb)
+              for (int ky = 0; ky < 4; ++ky)
                 for (int r8 = 0; r8 < 8; ++r8) {
-                  const int r = 8 * rb + r8;
+                  const int r = 8 * ky + r8;
                   if (!((seen >> r) & 1)) continue;
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    // the lane of each quad that holds key r's numerators
-                    float pv = (r8 & 1) ? s[rb][2 * h + 1] : s[rb][2 * h];
-                    pv = __shfl_sync(0xffffffffu, pv, (lane & ~3) | (r8 >> 1));
-                    if (pv != 0.f) {
+                  for (int rb = 0; rb < NRB; ++rb)
 #pragma unroll
-                      for (int nb = 0; nb < C::NB; ++nb) {
-                        const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                            base + (sV - base_u32) + (nb >> 3) * C::PANEL_BYTES + (kw + r) * 128 +
-                            (((nb & 7) ^ ((kw + r) & 7)) << 4) + 4 * t4);
-                        o[nb][2 * h] += pv * __uint_as_float(w << 16);
-                        o[nb][2 * h + 1] += pv * __uint_as_float(w & 0xffff0000u);
+                    for (int e = 0; e < 2; ++e) {
+                      // lane (r8, t) holds key r's numerators of rows 2t, 2t + 1
+                      const float pv = __shfl_sync(0xffffffffu, s[ky >> 1][rb][2 * (ky & 1) + e], 4 * r8 + t4);
+                      if (pv != 0.f) {
+#pragma unroll
+                        for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+                          for (int y = 0; y < 2; ++y) {
+                            const int ch = 2 * mb + y;
+                            const __nv_bfloat16 v = *reinterpret_cast<const __nv_bfloat16*>(
+                                base + (sV - base_u32) + (ch >> 3) * C::PANEL_BYTES + (kw + r) * 128 +
+                                (((ch & 7) ^ ((kw + r) & 7)) << 4) + 2 * g);
+                            o[rb][mb][2 * y + e] += pv * __bfloat162float(v);
+                          }
                       }
                     }
-                  }
                 }
             }
           }
-          // value fragment register b of 16 keys: keys 2 t + 8 b and the next
+          // value fragment registers 0, 1 (2, 3) of 16 keys hold keys 2t, 2t + 1 (+ 8)
           uint32_t keep[2][2];
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
@@ -629,35 +663,36 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               const uint32_t two = odd >> (16 * kk + 8 * y + 2 * t4);
               keep[kk][y] = ((two & 1u) ? 0u : 0xffffu) | ((two & 2u) ? 0u : 0xffff0000u);
             }
-          const int r = kw + (lane & 15), hi = lane >> 4;
+          const int r = kw + (lane & 7) + 8 * (lane >> 4), half = (lane >> 3) & 1;
           auto add = [&](bool masked) {
 #pragma unroll
-            for (int nb = 0; nb < C::NB; nb += 2)
+            for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk) {
-                uint32_t vf[4];
-                ldsm4t(sV + (nb >> 3) * C::PANEL_BYTES + (r + 16 * kk) * 128 + ((((nb & 7) + hi) ^ (r & 7)) << 4), vf);
+                uint32_t a[4];
+                ldsm4t(sV + (mb >> 2) * C::PANEL_BYTES + (r + 16 * kk) * 128 + (((2 * (mb & 3) + half) ^ (r & 7)) << 4), a);
                 if (masked) {
 #pragma unroll
-                  for (int y = 0; y < 4; ++y) vf[y] &= keep[kk][y & 1];
+                  for (int y = 0; y < 4; ++y) a[y] &= keep[kk][y >> 1];
                 }
-                mma16816<false>(o[nb], pa[kk], vf[0], vf[1]);
-                mma16816<false>(o[nb + 1], pa[kk], vf[2], vf[3]);
+#pragma unroll
+                for (int rb = 0; rb < NRB; ++rb)
+                  mma16816<false>(o[rb][mb], make_uint4(a[0], a[1], a[2], a[3]), pb[rb][kk][0], pb[rb][kk][1]);
               }
           };
           if (TAIL && odd != 0) add(true);
           else add(false);
         } else {
-          // lane g reads D / 8 bytes of rows t, t + 4, t + 8, t + 12 of each 16 -- the keys of S's
-          // columns; a row that must not show is read as zeros (its codes may be NaN), and shows in
-          // the rows that see it through its scale
+          // lane g reads D / 8 bytes of rows t, t + 4, t + 8, t + 12 of each 16 -- the keys of S^T's rows
+          // 2t, 2t + 1 (+ 8).  A row that must not show is read as zeros (its codes may be NaN), and
+          // shows in the rows that see it through its scale
           constexpr int NW = D / 32;
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk) {
             uint32_t w[4][NW];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int r = kw + 16 * kk + t4 + 4 * i;
+              const int kr = 16 * kk + t4 + 4 * i, r = kw + kr;
               if constexpr (D == 128) {
                 const uint4 u = lds128(sV + r * 128 + ((((g >> 1) | ((g & 1) << 2)) ^ (r & 7)) << 4));
                 w[i][0] = u.x; w[i][1] = u.y; w[i][2] = u.z; w[i][3] = u.w;
@@ -666,23 +701,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 const uint2 u = lds64(sV + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) + 8 * (g & 1));
                 w[i][0] = u.x; w[i][1] = u.y;
               }
-              if (TAIL && ((vbad >> (4 * kk + i)) & 1)) {
+              if (TAIL) {
+                const float vs = reinterpret_cast<const float*>(base + slot * C::STAGE_BYTES + 2 * C::TILE_BYTES)[128 + r];
+                if (k0 + kr >= L || !(vs < INFINITY)) {
 #pragma unroll
-                for (int c = 0; c < NW; ++c) w[i][c] = 0u;
+                  for (int c = 0; c < NW; ++c) w[i][c] = 0u;
+                }
               }
             }
 #pragma unroll
-            for (int c = 0; c < NW; ++c)
+            for (int mb = 0; mb < C::MB; ++mb) {
+              // bytes 2 mb, 2 mb + 1 of the lane's piece, of rows (t, t + 4) and (t + 8, t + 12)
+              const int c = mb >> 1;
+              const uint32_t sel = (mb & 1) == 0 ? 0x5140u : 0x7362u;
+              uint4 a;
+              e4m3x4_to_f16(__byte_perm(w[0][c], w[1][c], sel), a.x, a.y);
+              e4m3x4_to_f16(__byte_perm(w[2][c], w[3][c], sel), a.z, a.w);
 #pragma unroll
-              for (int e = 0; e < 4; e += 2) {
-                // bytes e, e + 1 of two rows: (row, row + 4) of element e, then of e + 1
-                const uint32_t sel = e == 0 ? 0x5140u : 0x7362u;
-                uint32_t b0, b1, d0, d1;
-                e4m3x4_to_f16(__byte_perm(w[0][c], w[1][c], sel), b0, d0);
-                e4m3x4_to_f16(__byte_perm(w[2][c], w[3][c], sel), b1, d1);
-                mma16816<true>(o[4 * c + e], pa[kk], b0, b1);
-                mma16816<true>(o[4 * c + e + 1], pa[kk], d0, d1);
-              }
+              for (int rb = 0; rb < NRB; ++rb) mma16816<true>(o[rb][mb], a, pb[rb][kk][0], pb[rb][kk][1]);
+            }
           }
         }
       };
@@ -694,85 +731,99 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (lane == 0) mbar_arrive(BAR_EMPTY(slot));
     }
 
-    // ---- the warps' partial results meet ----
+    // ---- the warps' partial results meet; the next segment's inputs are on their way meanwhile ----
+    const Segment dn = sg;
+    const int ql_dn = ql;
+    x += sg.t1 - sg.t0;
+    if (x < x1) fetch(x);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float l = l_run[h];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (t4 == 0) ml[warp * 16 + g + 8 * h] = make_float2(m_run[h], l);
+    for (int rb = 0; rb < NRB; ++rb) {
+      float l[2];
+      f2_unpack(l_run[rb], l[0], l[1]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], sh);
+        if (g == 0) ml[warp * RW + 8 * rb + 2 * t4 + e] = make_float2(m_run[rb][e], l[e]);
+      }
     }
     named_bar_sync(1, 32 * NWARP);
     // (max, sum) over the warps that hold a part of row r of the unit
     auto whole_row = [&](int r, float& M, float& l) {
-      const float2* e = ml + (WIDE ? (r >> 4) * 4 * 16 : 0) + (r & 15);
+      const float2* e = ml + (WIDE ? (r / RW) * 4 * RW : 0) + r % RW;
       M = -INFINITY;
       l = 0.f;
 #pragma unroll
-      for (int w = 0; w < C::PARTS; ++w) M = fmaxf(M, e[16 * w].x);
+      for (int w = 0; w < C::PARTS; ++w) M = fmaxf(M, e[RW * w].x);
 #pragma unroll
-      for (int w = 0; w < C::PARTS; ++w) l += e[16 * w].x == -INFINITY ? e[16 * w].y : e[16 * w].y * ex2(e[16 * w].x - M);
+      for (int w = 0; w < C::PARTS; ++w) l += e[RW * w].x == -INFINITY ? e[RW * w].y : e[RW * w].y * ex2(e[RW * w].x - M);
     };
-    float f[2];
+    float f[NRB][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float M, l;
-      whole_row(rlo + g + 8 * h, M, l);
-      f[h] = m_run[h] == -INFINITY ? 0.f : ex2(m_run[h] - M) / l;
-      if (FP8) f[h] *= vref * 0x1p-10f;            // the 2^10 of the numerators
-    }
-    const bool whole = sg.t0 == 0 && sg.t1 == sg.n;
-    const long long ws_slot = 2ll * blockIdx.x + (sg.t0 > 0 ? 0 : 1);
+    for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float M, l;
+        whole_row(rlo + 8 * rb + 2 * t4 + e, M, l);
+        f[rb][e] = m_run[rb][e] == -INFINITY ? 0.f : ex2(m_run[rb][e] - M) / l;
+        if (FP8) f[rb][e] *= vref * 0x1p-10f;      // the 2^10 of the numerators
+      }
+    const bool whole = dn.t0 == 0 && dn.t1 == dn.n;
+    const long long ws_slot = 2ll * blockIdx.x + (dn.t0 > 0 ? 0 : 1);
     if (threadIdx.x < RB) {
       const int r = threadIdx.x;
+      qmax[r] = 0;
       float M, l;
       whole_row(r, M, l);
       const float lse2 = l == 0.f ? -INFINITY : M + __log2f(l);
-      const int pr = sg.rt * RB + r, t = pr / p.G;
+      const int pr = dn.rt * RB + r, t = pr / p.G;
       if (!whole) p.ws_l[ws_slot * RB + r] = lse2;
-      else if (t < ql && p.lse != nullptr)
-        p.lse[(static_cast<long long>(sg.b) * p.Hq + sg.hkv * p.G + pr % p.G) * p.T + t] = lse2 * LN2_P;
+      else if (t < ql_dn && p.lse != nullptr)
+        p.lse[(static_cast<long long>(dn.b) * p.Hq + dn.hkv * p.G + pr % p.G) * p.T + t] = lse2 * LN2_P;
     }
-    constexpr int KB = C::MCOLS / 8;               // n-blocks per pass
+    // 32 columns at a time: column 16 m + 8 y + g of the buffer is row g + 8 y of O^T's block m
 #pragma unroll
-    for (int pass = 0; pass < C::NB / KB; ++pass) {
+    for (int pass = 0; pass < D / 32; ++pass) {
       if (pass > 0) named_bar_sync(1, 32 * NWARP);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int rb = 0; rb < NRB; ++rb)
 #pragma unroll
-        for (int nb = 0; nb < KB; ++nb)
-          *reinterpret_cast<float2*>(mbuf + (warp * 16 + g + 8 * h) * C::MSTRIDE + 8 * nb + 2 * t4) =
-              make_float2(o[pass * KB + nb][2 * h] * f[h], o[pass * KB + nb][2 * h + 1] * f[h]);
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mbuf[(warp * RW + 8 * rb + 2 * t4 + (i & 1)) * C::MSTRIDE + 16 * m + 8 * (i >> 1) + g] =
+                o[rb][2 * pass + m][i] * f[rb][i & 1];
       named_bar_sync(1, 32 * NWARP);
 #pragma unroll
       for (int r0 = 0; r0 < RB; r0 += 16) {
         // thread: two output columns of one row
         const int r = r0 + static_cast<int>(threadIdx.x) / 16, c2 = threadIdx.x % 16;
+        if (r >= RB) continue;
         int i0, i1, d;
-        if (FP8) {                                 // n-blocks 2y, 2y + 1 of column n: neighbours in d
-          const int n = c2 & 7, y = c2 >> 3;
-          i0 = 16 * y + n;
+        if (FP8) {                                 // d of block m, row g + 8 y: piece(g) + 2 m + y
+          const int n = c2 & 7, m = c2 >> 3;
+          i0 = 16 * m + n;
           i1 = i0 + 8;
-          const int lt = n >> 1;
-          const int first = D == 128 ? 16 * (lt + 4 * (n & 1)) : 16 * (((lt & 1) << 1) | (lt >> 1)) + 8 * (n & 1);
-          d = first + pass * KB + 2 * y;
+          const int first = D == 128 ? 16 * ((n >> 1) | ((n & 1) << 2))
+                                     : 16 * (((n >> 2) & 1) | (((n >> 1) & 1) << 1)) + 8 * (n & 1);
+          d = first + 2 * (2 * pass + m);
         } else {
           i0 = 2 * c2;
           i1 = i0 + 1;
-          d = pass * C::MCOLS + 2 * c2;
+          d = 32 * pass + 2 * c2;
         }
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int w = 0; w < C::PARTS; ++w) {
-          const float* src = mbuf + ((WIDE ? (r0 >> 4) * 4 : 0) + w) * 16 * C::MSTRIDE + (r & 15) * C::MSTRIDE;
+          const float* src = mbuf + ((WIDE ? (r / RW) * 4 : 0) + w) * RW * C::MSTRIDE + (r % RW) * C::MSTRIDE;
           a += src[i0];
           b += src[i1];
         }
-        const int pr = sg.rt * RB + r, t = pr / p.G;
-        if (t < ql) {
+        const int pr = dn.rt * RB + r, t = pr / p.G;
+        if (t < ql_dn) {
           if (whole)
             *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
-                                         ((static_cast<long long>(sg.b) * p.T + t) * p.Hq + sg.hkv * p.G + pr % p.G) * D + d) =
+                                         ((static_cast<long long>(dn.b) * p.T + t) * p.Hq + dn.hkv * p.G + pr % p.G) * D + d) =
                 pack_bf16x2(a, b);
           else
             *reinterpret_cast<float2*>(p.ws_o + (ws_slot * RB + r) * D + d) = make_float2(a, b);
@@ -780,7 +831,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
     named_bar_sync(1, 32 * NWARP);                 // the next unit rewrites the shared arrays
-    x += sg.t1 - sg.t0;
   }
 }
 
@@ -832,20 +882,20 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p)
   }
 }
 
-template <int D, bool FP8, bool WIDE>
+template <int D, bool FP8, int NRB, bool WIDE>
 cudaError_t launch_paged_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, bool combine, cudaStream_t st) {
-  using C = PagedCfg<D, FP8, WIDE>;
+  using C = PagedCfg<D, FP8, NRB, WIDE>;
   static std::atomic<unsigned long long> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if ((configured.load() & bit) == 0) {
-    e = cudaFuncSetAttribute(attn_paged_kernel<D, FP8, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    e = cudaFuncSetAttribute(attn_paged_kernel<D, FP8, NRB, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  attn_paged_kernel<D, FP8, WIDE><<<p.n_cta, NTHREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
+  attn_paged_kernel<D, FP8, NRB, WIDE><<<p.n_cta, NTHREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess || !combine) return e;
   // the merge starts while the last CTAs finish and waits for them on the device
   cudaLaunchConfig_t cfg{};
@@ -862,8 +912,10 @@ cudaError_t launch_paged_d(const CUtensorMap& tk, const CUtensorMap& tv, const P
 
 template <int D, bool FP8>
 cudaError_t launch_paged_m(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, bool combine, cudaStream_t st) {
-  return paged_rows(p.G * p.T) == 16 ? launch_paged_d<D, FP8, false>(tk, tv, p, combine, st)
-                                     : launch_paged_d<D, FP8, true>(tk, tv, p, combine, st);
+  const int rb = paged_rows(p.G * p.T);
+  return rb == 8    ? launch_paged_d<D, FP8, 1, false>(tk, tv, p, combine, st)
+         : rb == 16 ? launch_paged_d<D, FP8, 2, false>(tk, tv, p, combine, st)
+                    : launch_paged_d<D, FP8, 2, true>(tk, tv, p, combine, st);
 }
 
 }  // namespace

@@ -99,7 +99,7 @@ constexpr int PAGED_MAX_BATCH = 1024;
 constexpr int PAGED_MAX_DRAFT = 64;
 
 // Query rows per work unit for R = G * T packed rows.
-constexpr int paged_rows(int R) { return R <= 16 ? 16 : 32; }
+constexpr int paged_rows(int R) { return R <= 8 ? 8 : (R <= 16 ? 16 : 32); }
 
 // tk, tv: the cache as (D, page_size, Hkv, n_pages) with a box of one swizzle panel x
 // min(page_size, 128) rows.
