@@ -314,7 +314,11 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
     return api_fail(ATTN_ERR_INVALID_ARG, "need max_pages >= 1 and max_pages * page_size < 2^31 (got %d)", max_pages);
   const long long tiles = (static_cast<long long>(max_pages) * page_size + 127) / 128;
   if (tiles * B > 0x7fffffffll) return api_fail(ATTN_ERR_INVALID_ARG, "the page table spans too many keys");
-  const int G = Hq / Hkv, RB = paged_rows(G * T), row_tiles = (G * T + RB - 1) / RB;
+  const int G = Hq / Hkv;
+  if (G * static_cast<long long>(T) > 65535)
+    return api_fail(ATTN_ERR_UNSUPPORTED, "(Hq / Hkv) * T = %lld query rows per key/value head, at most 65535",
+                    G * static_cast<long long>(T));
+  const int RB = paged_rows(G * T), row_tiles = (G * T + RB - 1) / RB;
   if (static_cast<long long>(B) * Hkv * row_tiles > 0x7fffffffll) return api_fail(ATTN_ERR_INVALID_ARG, "too many work units");
   const size_t need = attn_decode_paged_workspace_bytes(B, T, Hq, Hkv, D, page_size, max_pages);
   if (need > 0) {
@@ -349,6 +353,7 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = G;
+  p.g_magic = G == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + G - 1) / G);
   p.n_pages = n_pages;
   p.page_size = page_size;
   p.max_pages = max_pages;

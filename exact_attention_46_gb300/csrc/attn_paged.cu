@@ -18,8 +18,8 @@
 //     any mix of lengths, and the lengths stay on the device.  A unit that several CTAs share
 //     leaves one partial (o, lse) per CTA in the workspace; a second, dependent kernel merges them
 //     in a fixed order;
-//   * a producer warp looks the pages up and fills a ring of (K tile, V tile) stages by TMA, one
-//     box per page and swizzle panel; a page number outside the cache is not loaded and reported;
+//   * producer warps look the pages up and fill a ring of (K tile, V tile) stages by TMA, one box per
+//     page and swizzle panel; a page number outside the cache is not loaded and reported;
 //   * a consumer warp takes 32 keys of a tile, from S = Q K^T to its own running (max, sum, O): no
 //     barrier between warps inside a unit.  With at most 32 rows an MMA tile of 128 rows would
 //     stand mostly empty and its hand-offs (S, P, O through Tensor Memory) would set the pace, so
@@ -49,7 +49,8 @@ namespace {
 
 constexpr float LN2_P = 0.69314718055994530942f;
 constexpr int NWARP = 8;                        // consumer warps
-constexpr int NTHREADS = 32 * (NWARP + 1);
+constexpr int NPROD = 4;                        // producer warps: (key, value) x (even, odd copies)
+constexpr int NTHREADS = 32 * (NWARP + NPROD);
 enum : int { WHERE_PAGED_LOAD = 51, WHERE_PAGED_USE = 52, WHERE_PAGED_LENS = 53, WHERE_PAGED_PAGE = 54 };
 
 // NRB: 8-row blocks of a warp (1, 2).  WIDE: a warp group per 16 of 32 rows; otherwise the two
@@ -138,6 +139,18 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
       : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
+// 16-byte asynchronous copy global -> shared, and an arrival on `bar` when this thread's copies so
+// far have landed (counted in the barrier's initial count).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ void wait_drain_paged(uint32_t bar, uint32_t parity, long long limit) {
   if (mbar_try_wait(bar, parity)) return;
   const long long t0 = clock64();
@@ -186,6 +199,17 @@ struct Segment {
   int t0, t1, n;        // tiles [t0, t1) of the unit's n
 };
 
+// x / y for y > 0, in 32 bits where both fit (the 64-bit division is a few hundred cycles).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
+// Token of packed row r: r / G by multiplication (r, G < 2^16).
+__device__ __forceinline__ int token_of(const PagedParams& p, int r) {
+  return p.g_magic == 0 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.g_magic));
+}
+
 __device__ __forceinline__ Segment find_segment(const PagedParams& p, const int* pre, long long x, long long x1) {
   const long long hr = static_cast<long long>(p.Hkv) * p.row_tiles;
   int lo = 0, hi = p.B;
@@ -198,16 +222,16 @@ __device__ __forceinline__ Segment find_segment(const PagedParams& p, const int*
   s.b = lo;
   s.n = pre[lo + 1] - pre[lo];
   const long long y = x - pre[lo] * hr;
-  const int u = static_cast<int>(y / s.n);
-  s.hkv = u / p.row_tiles;
-  s.rt = u % p.row_tiles;
+  const int u = static_cast<int>(quotient(y, s.n));
+  s.hkv = p.row_tiles == 1 ? u : u / p.row_tiles;
+  s.rt = u - s.hkv * p.row_tiles;
   s.t0 = static_cast<int>(y - static_cast<long long>(u) * s.n);
   const long long left = x1 - x;
   s.t1 = left < s.n - s.t0 ? s.t0 + static_cast<int>(left) : s.n;
   return s;
 }
 
-__device__ __forceinline__ long long cta_start(long long i, long long W, long long N) { return i * W / N; }
+__device__ __forceinline__ long long cta_start(long long i, long long W, long long N) { return quotient(i * W, N); }
 
 template <int D, bool FP8, int NRB, bool WIDE>
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -225,12 +249,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   auto BAR_EMPTY = [&](int s) { return bar0 + 8u * (NSTAGE + s); };
   int* flags = reinterpret_cast<int*>(base + C::BAR_OFF + 2 * NSTAGE * 8);
   volatile int* abort_flag = flags;
-  int* scratch = flags + 1;                      // [NWARP + 1]
+  int* scratch = flags + 1;                      // [NWARP + NPROD]
 
   const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
   if (threadIdx.x == 0) {
     for (int s = 0; s < NSTAGE; ++s) {
-      mbar_init(BAR_FULL(s), 1);
+      mbar_init(BAR_FULL(s), NPROD + (FP8 ? 64 : 0));
       mbar_init(BAR_EMPTY(s), NWARP);
     }
     *abort_flag = 0;
@@ -247,23 +271,31 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const long long x0 = cta_start(blockIdx.x, W, N), x1 = cta_start(blockIdx.x + 1ll, W, N);
   const WaitCtl ctl{p.spin_limit, abort_flag, p.err_word, p.err_info};
 
-  if (warp == NWARP) {
-    // ---- producer: page look-up and TMA ----
+  if (warp >= NWARP) {
+    // ---- producers: page look-up and copies.  Warp pw takes the keys (pw even) or the values, and
+    // every other copy of a tile; with E4M3 the first two also bring the scales ----
     // Box i of the list of boxes of a segment is br rows of one page; lane i % 32 looks its page up,
     // one batch of 32 boxes ahead of their use, and issues its copies.
+    const int pw = warp - NWARP, kv = pw & 1, odd = pw >> 1;
+    const CUtensorMap* tm = kv == 0 ? &tmK : &tmV;
+    const float* scales = kv == 0 ? p.k_scale : p.v_scale;
     const int ps_log = 31 - __clz(p.page_size);
-    const int br_log = ps_log < 7 ? ps_log : 7, br = 1 << br_log;
+    const int br_log = ps_log < 7 ? ps_log : 7;
     const int pt_log = 7 - br_log, per_tile = 1 << pt_log;       // boxes of a tile (1 .. 8)
+    // two panels: this warp's panel of every box; one panel: every other box
+    const unsigned my_boxes = C::NPANEL == 2 ? 0xffu : (odd ? 0xaau : 0x55u);
+    const int panel = C::NPANEL == 2 ? odd : 0;
     const uint64_t pol = l2_policy_evict_first();
     int it = 0;
     for (long long x = x0; x < x1;) {
       const Segment s = find_segment(p, pre, x, x1);
       const int L = __ldg(p.ctx_lens + s.b) + (p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T);
       const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
-      // first key of this lane's box in the batch that starts at tile j, and its page (-1: past the end)
+      // page of this lane's box in the batch that starts at tile j (-1: past the end).  The entry is
+      // read before the length is known -- it lies in the table -- so the two loads overlap
       auto look_up = [&](int j) {
-        const int key = 128 * j + (lane << br_log);
-        return j < s.t1 && key < L ? __ldg(table + (key >> ps_log)) : -1;
+        const int at = (128 * j + (lane << br_log)) >> ps_log;
+        return j < s.t1 && at < p.max_pages ? __ldg(table + at) : -1;
       };
       const int batch = 32 >> pt_log;              // tiles of a batch
       int next = look_up(s.t0);
@@ -273,31 +305,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int key = 128 * j0 + (lane << br_log);
         const bool wanted = key < L && j0 + (lane >> pt_log) < s.t1;
         const bool good = wanted && page >= 0 && page < p.n_pages;
-        if (wanted && !good && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_PAGE);
+        if (pw == 0 && wanted && !good && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_PAGE);
         const unsigned boxes = __ballot_sync(0xffffffffu, good);
         const int row = key & (p.page_size - 1);
-        const long long e = (static_cast<long long>(page) * p.Hkv + s.hkv) * p.page_size + row;
         for (int i = 0; i < batch && j0 + i < s.t1; ++i, ++it) {
           const int slot = it % NSTAGE;
           if (!warp_wait(BAR_EMPTY(slot), ((it / NSTAGE) & 1) ^ 1u, ctl, WHERE_PAGED_LOAD)) break;
-          const unsigned mine = (boxes >> (i << pt_log)) & ((1u << per_tile) - 1);
-          if (lane == 0)
-            mbar_arrive_expect_tx(BAR_FULL(slot), (__popc(mine) << br_log) * (2u * C::ROW_BYTES + (FP8 ? 8u : 0u)));
+          const unsigned mine = (boxes >> (i << pt_log)) & ((1u << per_tile) - 1) & my_boxes;
+          if (lane == 0) mbar_arrive_expect_tx(BAR_FULL(slot), (__popc(mine) << br_log) * C::PANEL_ROW);
           __syncwarp();
-          if (good && (lane >> pt_log) == i) {
-            const int box = lane & (per_tile - 1);
-            const uint32_t sK = base_u32 + slot * C::STAGE_BYTES + (box << br_log) * C::PANEL_ROW;
-#pragma unroll
-            for (int pn = 0; pn < C::NPANEL; ++pn) {
-              tma_load_4d(sK + pn * C::PANEL_BYTES, &tmK, BAR_FULL(slot), pn * (C::PANEL_ROW / C::ESZ), row, s.hkv, page, pol);
-              tma_load_4d(sK + C::TILE_BYTES + pn * C::PANEL_BYTES, &tmV, BAR_FULL(slot), pn * (C::PANEL_ROW / C::ESZ),
-                          row, s.hkv, page, pol);
-            }
-            if (FP8) {
-              const uint32_t sS = base_u32 + slot * C::STAGE_BYTES + 2 * C::TILE_BYTES + (4 * box << br_log);
-              bulk_load(sS, p.k_scale + e, 4 * br, BAR_FULL(slot), pol);
-              bulk_load(sS + 512, p.v_scale + e, 4 * br, BAR_FULL(slot), pol);
-            }
+          const uint32_t st = base_u32 + slot * C::STAGE_BYTES;
+          const int box = lane & (per_tile - 1);
+          if ((lane >> pt_log) == i && ((mine >> box) & 1))
+            tma_load_4d(st + kv * C::TILE_BYTES + panel * C::PANEL_BYTES + (box << br_log) * C::PANEL_ROW, tm, BAR_FULL(slot),
+                        panel * (C::PANEL_ROW / C::ESZ), row, s.hkv, page, pol);
+          if (FP8 && odd == 0) {
+            // lane: the scales of four keys of the tile
+            const int src = (i << pt_log) + (lane >> (br_log - 2));
+            const int pg = __shfl_sync(0xffffffffu, page, src);
+            const int r0 = __shfl_sync(0xffffffffu, row, src) + ((4 * lane) & ((1 << br_log) - 1));
+            if ((boxes >> src) & 1)
+              cp_async16(st + 2 * C::TILE_BYTES + 512 * kv + 16 * lane,
+                         scales + (static_cast<long long>(pg) * p.Hkv + s.hkv) * p.page_size + r0);
+            cp_async_arrive(BAR_FULL(slot));
           }
         }
         if (*abort_flag) break;
@@ -305,9 +335,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (*abort_flag) break;
       x += s.t1 - s.t0;
     }
-    if (*abort_flag && lane == 0)
-      for (int i = it > NSTAGE ? it - NSTAGE : 0; i < it; ++i)
-        wait_drain_paged(BAR_FULL(i % NSTAGE), (i / NSTAGE) & 1, p.spin_limit);
+    if (*abort_flag) {
+      cp_async_wait_all();
+      if (lane == 0)
+        for (int i = it > NSTAGE ? it - NSTAGE : 0; i < it; ++i)
+          wait_drain_paged(BAR_FULL(i % NSTAGE), (i / NSTAGE) & 1, p.spin_limit);
+    }
     return;
   }
 
@@ -346,10 +379,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int i = 0; i < QN; ++i) {
       const int e = static_cast<int>(threadIdx.x) + i * 32 * NWARP;
       const int l = e & 31, ks = (e >> 5) % C::KS, rb = (e >> 5) / C::KS;
-      const int pr = sg.rt * RB + 8 * rb + (l >> 2), t = pr / p.G;
+      const int pr = sg.rt * RB + 8 * rb + (l >> 2), t = token_of(p, pr);
       qraw[i] = make_uint2(0u, 0u);
       if (rb < RB / 8 && t < p.T) {                // rows past q_len are computed and not written
-        const __nv_bfloat16* src = qb + (static_cast<long long>(t) * p.Hq + pr % p.G) * D;
+        const __nv_bfloat16* src = qb + (static_cast<long long>(t) * p.Hq + pr - t * p.G) * D;
         // bf16: k = 2t, 2t + 1 and 2t + 8, 2t + 9 of the step; E4M3: four elements in a row, the order in
         // which a thread reads the key's bytes
         if (FP8) {
@@ -362,7 +395,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     my_bits = 0;
     if (threadIdx.x < RB) {
-      const int t = (sg.rt * RB + static_cast<int>(threadIdx.x)) / p.G;
+      const int t = token_of(p, sg.rt * RB + static_cast<int>(threadIdx.x));
       if (t < p.T)
         my_bits = p.tree_mask != nullptr ? __ldg(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
                                          : (t >= 63 ? ~0ull : (2ull << t) - 1);
@@ -611,18 +644,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if constexpr (!FP8) {
           uint32_t odd = 0;                        // value rows past the end, or not finite: out of the product
           if (TAIL) {
-            for (int r = 0; r < 32; ++r) {
-              bool strange = k0 + r >= L;
-              if (!strange && k0 + r >= ctx) {
-                bool inf = false;
-                for (int c = lane; c < D / 2; c += 32) {
-                  const uint32_t w = *reinterpret_cast<const uint32_t*>(base + (sV - base_u32) + (c >> 5) * C::PANEL_BYTES +
-                                                                        (kw + r) * 128 + (c & 31) * 4);
-                  inf = inf || (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-                }
-                strange = __any_sync(0xffffffffu, inf);
+            if (k0 + 32 > L) odd = ~0u << (L - k0);
+            for (int r = ctx > k0 ? ctx - k0 : 0; r < 32 && k0 + r < L; ++r) {
+              bool inf = false;
+              for (int c = lane; c < D / 2; c += 32) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(base + (sV - base_u32) + (c >> 5) * C::PANEL_BYTES +
+                                                                      (kw + r) * 128 + (c & 31) * 4);
+                inf = inf || (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
               }
-              if (strange) odd |= 1u << r;
+              if (__any_sync(0xffffffffu, inf)) odd |= 1u << r;
             }
             // those that some row may see are added element by element
             const uint32_t seen = k0 + 32 <= L ? odd : odd & ((1u << (L - k0)) - 1);
@@ -776,10 +806,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       float M, l;
       whole_row(r, M, l);
       const float lse2 = l == 0.f ? -INFINITY : M + __log2f(l);
-      const int pr = dn.rt * RB + r, t = pr / p.G;
+      const int pr = dn.rt * RB + r, t = token_of(p, pr);
       if (!whole) p.ws_l[ws_slot * RB + r] = lse2;
       else if (t < ql_dn && p.lse != nullptr)
-        p.lse[(static_cast<long long>(dn.b) * p.Hq + dn.hkv * p.G + pr % p.G) * p.T + t] = lse2 * LN2_P;
+        p.lse[(static_cast<long long>(dn.b) * p.Hq + dn.hkv * p.G + pr - t * p.G) * p.T + t] = lse2 * LN2_P;
     }
     // 32 columns at a time: column 16 m + 8 y + g of the buffer is row g + 8 y of O^T's block m
 #pragma unroll
@@ -819,11 +849,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           a += src[i0];
           b += src[i1];
         }
-        const int pr = dn.rt * RB + r, t = pr / p.G;
+        const int pr = dn.rt * RB + r, t = token_of(p, pr);
         if (t < ql_dn) {
           if (whole)
             *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
-                                         ((static_cast<long long>(dn.b) * p.T + t) * p.Hq + dn.hkv * p.G + pr % p.G) * D + d) =
+                                         ((static_cast<long long>(dn.b) * p.T + t) * p.Hq + dn.hkv * p.G + pr - t * p.G) * D + d) =
                 pack_bf16x2(a, b);
           else
             *reinterpret_cast<float2*>(p.ws_o + (ws_slot * RB + r) * D + d) = make_float2(a, b);
@@ -850,12 +880,12 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p)
   const long long W = pre[p.B] * hr, N = W < p.n_cta ? W : p.n_cta;
   const long long a = pre[b] * hr + static_cast<long long>(u) * n;
   // the CTA that holds list position x is the last i with i W / N <= x
-  const long long c0 = ((a + 1) * N - 1) / W, c1 = ((a + n) * N - 1) / W;
+  const long long c0 = quotient((a + 1) * N - 1, W), c1 = quotient((a + n) * N - 1, W);
   if (c0 == c1) return;
   const int ql = p.q_lens != nullptr ? __ldg(p.q_lens + b) : p.T;
   const int lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < RB; r += 4) {
-    const int pr = rt * RB + r, t = pr / p.G;
+    const int pr = rt * RB + r, t = token_of(p, pr);
     if (t >= ql) break;
     float mx = -INFINITY;
     for (long long c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, p.ws_l[(2 * c + (c == c0 ? 1 : 0)) * RB + r]);
@@ -873,7 +903,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p)
       for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, p.ws_o[(slot * RB + r) * D + lane * (D / 32) + e], acc[e]);
     }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    const long long h = static_cast<long long>(hkv) * p.G + pr % p.G;
+    const long long h = static_cast<long long>(hkv) * p.G + pr - t * p.G;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * D + lane * (D / 32);
 #pragma unroll
     for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);

@@ -86,6 +86,7 @@ struct PagedParams {
   float* ws_o;          // [slots][RB][D] partial outputs
   float* ws_l;          // [slots][RB] partial lse, log2 units
   int B, T, Hq, Hkv, G;
+  uint32_t g_magic;     // ceil(2^32 / G), 0 for G = 1
   int n_pages, page_size, max_pages;
   int row_tiles;        // ceil(G * T / RB)
   int n_cta;            // CTAs of the key kernel
