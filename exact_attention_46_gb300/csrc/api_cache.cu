@@ -1,5 +1,6 @@
 // api_cache.cu -- the C ABI of rotary positions and the paged key/value cache (include/attn46.h):
 // argument checks and launches.  No computation happens here.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -160,14 +161,20 @@ int append(const void* q, const void* k, const void* v, void* q_out, const float
 
 // CTAs of attn_decode_paged's key kernel on the current device: one per SM.
 int paged_ctas() {
+  static std::atomic<int> known[64];               // SM count by device: a constant of the hardware
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-    return 152;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 152;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 152;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
 // A unit can be shared by CTAs only if some sequence can have more than one 128-key tile.
 bool paged_combines(int page_size, int max_pages) { return static_cast<long long>(page_size) * max_pages > 128; }
+
+// Two partial units a CTA (the one it starts in and the one it ends in): RB rows of D + 1 floats.
+size_t paged_workspace(int n_cta, int RB, int D) { return 8ull * n_cta * RB * (static_cast<size_t>(D) + 1); }
 
 }  // namespace
 
@@ -284,7 +291,7 @@ size_t attn_decode_paged_workspace_bytes(int B, int T, int Hq, int Hkv, int D, i
       page_size < 1 || max_pages < 1)
     return 0;
   if (!paged_combines(page_size, max_pages)) return 0;
-  return 8ull * paged_ctas() * paged_rows(Hq / Hkv * T) * (static_cast<size_t>(D) + 1);
+  return paged_workspace(paged_ctas(), paged_rows(Hq / Hkv * T), D);
 }
 
 int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
@@ -320,7 +327,8 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
                     G * static_cast<long long>(T));
   const int RB = paged_rows(G * T), row_tiles = (G * T + RB - 1) / RB;
   if (static_cast<long long>(B) * Hkv * row_tiles > 0x7fffffffll) return api_fail(ATTN_ERR_INVALID_ARG, "too many work units");
-  const size_t need = attn_decode_paged_workspace_bytes(B, T, Hq, Hkv, D, page_size, max_pages);
+  const int n_cta = paged_ctas();
+  const size_t need = paged_combines(page_size, max_pages) ? paged_workspace(n_cta, RB, D) : 0;
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need || !api_aligned16(workspace))
       return api_fail(ATTN_ERR_INVALID_ARG, "a 16-byte aligned workspace of %zu bytes is needed "
@@ -358,7 +366,7 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
   p.page_size = page_size;
   p.max_pages = max_pages;
   p.row_tiles = row_tiles;
-  p.n_cta = paged_ctas();
+  p.n_cta = n_cta;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_l = need > 0 ? p.ws_o + 2ll * p.n_cta * RB * D : nullptr;
   const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));

@@ -864,51 +864,103 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-// Merge of the units that several CTAs share: one block per unit, one warp per row.
+// Merge of the units that several CTAs share.  Block i looks at the start of CTA i + 1's tiles: where
+// that is the first cut inside a unit, the block merges the unit -- N - 1 blocks whatever the batch.
+// Its warps take the rows; with fewer rows than warps several warps share a row's parts.
 template <int D, int RB>
-__global__ void __launch_bounds__(128) paged_combine_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p) {
+  constexpr int NW = 8, E = D / 32;
   __shared__ int pre[PAGED_MAX_BATCH + 1];
-  __shared__ int scratch[4];
-  const bool ok = tile_prefix(p, pre, scratch, 128);
-  grid_dependency_wait();       // in every block: this grid's end stands for the key kernel's too
-  if (!ok) return;
+  __shared__ int scratch[NW];
+  __shared__ float part[NW][D + 2];
+  const bool ok = tile_prefix(p, pre, scratch, 32 * NW);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long hr = static_cast<long long>(p.Hkv) * p.row_tiles;
-  const int b = static_cast<int>(blockIdx.x / hr), u = static_cast<int>(blockIdx.x % hr);
-  const int hkv = u / p.row_tiles, rt = u % p.row_tiles;
-  const int n = pre[b + 1] - pre[b];
-  if (n == 0) return;
-  const long long W = pre[p.B] * hr, N = W < p.n_cta ? W : p.n_cta;
-  const long long a = pre[b] * hr + static_cast<long long>(u) * n;
-  // the CTA that holds list position x is the last i with i W / N <= x
-  const long long c0 = quotient((a + 1) * N - 1, W), c1 = quotient((a + n) * N - 1, W);
-  if (c0 == c1) return;
-  const int ql = p.q_lens != nullptr ? __ldg(p.q_lens + b) : p.T;
-  const int lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < RB; r += 4) {
-    const int pr = rt * RB + r, t = token_of(p, pr);
-    if (t >= ql) break;
-    float mx = -INFINITY;
-    for (long long c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, p.ws_l[(2 * c + (c == c0 ? 1 : 0)) * RB + r]);
+  const long long W = ok ? pre[p.B] * hr : 0, N = W < p.n_cta ? W : p.n_cta;
+  const long long i = blockIdx.x + 1ll;
+  bool mine = i < N;
+  Segment s{};
+  long long c1 = 0;
+  int ql = 0;
+  if (mine) {
+    const long long x = cta_start(i, W, N);
+    s = find_segment(p, pre, x, W);
+    // the CTA that holds list position y is the last c with c W / N <= y
+    mine = s.t0 > 0 && quotient((x - s.t0 + 1) * N - 1, W) == i - 1;
+    c1 = quotient((x - s.t0 + s.n) * N - 1, W);
+    ql = p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T;
+  }
+  grid_dependency_wait();       // in every block: this grid's end stands for the key kernel's too
+  if (!mine) return;
+  const int c0 = static_cast<int>(i - 1), n = static_cast<int>(c1) - c0 + 1;      // parts: CTAs c0 .. c1
+  const int left = ql * p.G - s.rt * RB, rows = left < RB ? left : RB;
+  const int share_log = rows >= 8 ? 0 : (rows > 4 ? 0 : (rows > 2 ? 1 : (rows > 1 ? 2 : 3)));   // warps of a row
+  const int share = 1 << share_log;
+  for (int r0 = 0; r0 < rows; r0 += NW >> share_log) {
+    const int r = r0 + (warp >> share_log), sub = warp & (share - 1);
+    const bool live = r < rows;
+    float mx = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    float acc[D / 32], sum = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    // c0's part is its last unit's (slot 1), the others' their first's (slot 0)
+    auto slot = [&](int c) { return 2ll * (c0 + c) + (c == 0 ? 1 : 0); };
+    if (live) {
+      for (int c = lane; c < n; c += 32) mx = fmaxf(mx, __ldcg(p.ws_l + slot(c) * RB + r));
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-    for (long long c = c0; c <= c1; ++c) {
-      const long long slot = 2 * c + (c == c0 ? 1 : 0);
-      const float l = p.ws_l[slot * RB + r];
-      const float w = l == -INFINITY ? 0.f : ex2(l - mx);
-      sum += w;
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // lane: columns E lane ..; eight parts in flight
+      for (int cb = sub; cb < n; cb += 8 * share) {
+        float l[8], v[8][E];
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, p.ws_o[(slot * RB + r) * D + lane * (D / 32) + e], acc[e]);
+        for (int k = 0; k < 8; ++k) {
+          // past the last part: that part again, with no weight (no branch between the loads)
+          const int c = cb + k * share < n ? cb + k * share : n - 1;
+          l[k] = __ldcg(p.ws_l + slot(c) * RB + r);
+          const float* src = p.ws_o + (slot(c) * RB + r) * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(src));
+            v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
+          } else {
+            const float2 u = __ldcg(reinterpret_cast<const float2*>(src));
+            v[k][0] = u.x; v[k][1] = u.y;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (cb + k * share >= n) break;
+          // a part that saw no key holds zeros (or NaN, which stays)
+          const float w = l[k] == -INFINITY ? 1.f : ex2(l[k] - mx);
+          sum += l[k] == -INFINITY ? 0.f : w;
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+        }
+      }
     }
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-    const long long h = static_cast<long long>(hkv) * p.G + pr - t * p.G;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * D + lane * (D / 32);
+    if (share > 1) {
+      __syncthreads();
+      if (live) {
 #pragma unroll
-    for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[(static_cast<long long>(b) * p.Hq + h) * p.T + t] = mx == -INFINITY ? -INFINITY : (mx + __log2f(sum)) * LN2_P;
+        for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+        if (lane == 0) part[warp][D] = sum;
+      }
+      __syncthreads();
+      if (live && sub == 0)
+        for (int w = 1; w < share; ++w) {
+          sum += part[warp + w][D];
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += part[warp + w][lane * E + e];
+        }
+    }
+    if (live && sub == 0) {
+      const int pr = s.rt * RB + r, t = token_of(p, pr);
+      const float inv = sum == 0.f ? 1.f : 1.f / sum;          // no key at all: the parts' zeros
+      const long long h = static_cast<long long>(s.hkv) * p.G + pr - t * p.G;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<long long>(s.b) * p.T + t) * p.Hq + h) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+      if (lane == 0 && p.lse != nullptr)
+        p.lse[(static_cast<long long>(s.b) * p.Hq + h) * p.T + t] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * LN2_P;
+    }
   }
 }
 
@@ -926,11 +978,11 @@ cudaError_t launch_paged_d(const CUtensorMap& tk, const CUtensorMap& tv, const P
     configured.fetch_or(bit);
   }
   attn_paged_kernel<D, FP8, NRB, WIDE><<<p.n_cta, NTHREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess || !combine) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || !combine || p.n_cta < 2) return e;
   // the merge starts while the last CTAs finish and waits for them on the device
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * p.row_tiles);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(p.n_cta - 1);
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -515,14 +515,26 @@ def selftest_bounded_wait(cycles, stream=None):
 
 # ---- rotary positions and the paged key/value cache ----
 # The calls below run on their tensors' device, whichever is current; what they allocate for a
-# given stream is allocated for that stream.
+# given stream is allocated for that stream.  A decoding step makes several of them per layer, so
+# their host time counts: a tensor that is as expected is found so by one look at its dtype, shape,
+# device and contiguity, and _arg says what is wrong with any other.
 
-def _run(dev, stream, name, *args):
-    """Call `name` with the stream appended, with `dev` current."""
-    if dev.index == torch.cuda.current_device():
-        return _lib.call(name, *args, _stream(stream))
-    with torch.cuda.device(dev):
-        return _lib.call(name, *args, _stream(stream))
+# torch.cuda.current_stream() builds a Stream object (about 3 us); the raw handle does not
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _run(index, stream, name, *args):
+    """Call `name` with the stream appended, with device `index` current."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _run(index, stream, name, *args)
+    if stream is not None:
+        raw = stream.cuda_stream
+    elif _raw_stream is not None:
+        raw = _raw_stream(index)
+    else:
+        raw = torch.cuda.current_stream().cuda_stream
+    return _lib.call(name, *args, raw)
 
 
 def _new(shape, dtype, dev, stream):
@@ -532,12 +544,24 @@ def _new(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _is(t, name, dtype, shape, dev):
+    """Check one tensor (exact dtype and shape, contiguous, device `dev`); its address."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev
+            or not t.is_contiguous()):
+        _arg(t, name, (dtype,), shape=shape, device=dev)
+    return t.data_ptr()
+
+
+def _is_opt(t, name, dtype, shape, dev):
+    return None if t is None else _is(t, name, dtype, shape, dev)
+
+
 def _rows(t, name, heads=None, D=None, device=None):
     """Check rows of heads ([tokens, heads, D], or [B, S, heads, D]): bf16 on a CUDA device, heads and
     D contiguous, tokens evenly spaced (a view of a fused projection).  Returns (tokens, stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if t.dtype not in _BF16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {_BF16[0]}")
     sh, st = t.shape, t.stride()
     n = len(sh)
@@ -560,25 +584,28 @@ def _rows(t, name, heads=None, D=None, device=None):
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev):
-    """Check a paged cache; returns (n_pages, page_size, Hkv, D, layout, dtype)."""
+    """Check a paged cache; returns ((n_pages, page_size, Hkv, D, layout, dtype), (addresses))."""
     _arg(k_cache, "k_cache", _BF16 + _CODES, dim=4, device=dev)
-    _arg(v_cache, "v_cache", (k_cache.dtype,), shape=k_cache.shape, device=dev)
-    n_pages, a, b, D = k_cache.shape
+    shape, dtype = k_cache.shape, k_cache.dtype
+    pv = _is(v_cache, "v_cache", dtype, shape, dev)
+    n_pages, a, b, D = shape
     page, Hkv = (a, b) if token_major else (b, a)
-    if k_cache.element_size() == 1:
-        _arg(k_scale, "k_scale", _F32, shape=(n_pages, Hkv, page), device=dev)
-        _arg(v_scale, "v_scale", _F32, shape=(n_pages, Hkv, page), device=dev)
-        return n_pages, page, Hkv, D, int(bool(token_major)), ATTN_FP8_E4M3
+    if dtype is not torch.bfloat16:
+        sh = (n_pages, Hkv, page)
+        return ((n_pages, page, Hkv, D, int(bool(token_major)), ATTN_FP8_E4M3),
+                (k_cache.data_ptr(), pv, _is(k_scale, "k_scale", torch.float32, sh, dev),
+                 _is(v_scale, "v_scale", torch.float32, sh, dev)))
     if k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale go with an E4M3 cache")
-    return n_pages, page, Hkv, D, int(bool(token_major)), ATTN_BF16
+    return (n_pages, page, Hkv, D, int(bool(token_major)), ATTN_BF16), (k_cache.data_ptr(), pv, None, None)
 
 
 def _table_rot(rope_cs, dev):
-    _arg(rope_cs, "rope_cs", _F32, dim=3, device=dev)
-    if rope_cs.shape[2] != 2:
-        raise ValueError(f"rope_cs: expected shape (n_pos, rot_dim / 2, 2), got {tuple(rope_cs.shape)}")
-    return int(rope_cs.shape[0]), 2 * int(rope_cs.shape[1])
+    sh = getattr(rope_cs, "shape", ())
+    if len(sh) != 3 or sh[2] != 2:
+        _arg(rope_cs, "rope_cs", _F32, dim=3, device=dev)
+        raise ValueError(f"rope_cs: expected shape (n_pos, rot_dim / 2, 2), got {tuple(sh)}")
+    return _is(rope_cs, "rope_cs", torch.float32, sh, dev), sh[0], 2 * sh[1]
 
 
 def rope_scaled_table(n_pos, rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=0, device="cuda",
@@ -591,7 +618,7 @@ def rope_scaled_table(n_pos, rot_dim, base=10000.0, scaling="none", factor=1.0, 
     _opt(out, "out", _F32, shape=(n_pos, rot_dim // 2, 2))
     if out is None:
         out = _new((n_pos, rot_dim // 2, 2), torch.float32, torch.device(device), stream)
-    _run(out.device, stream, "rope_scaled_table", _ptr(out), int(n_pos), int(rot_dim), float(base),
+    _run(out.device.index, stream, "rope_scaled_table", _ptr(out), int(n_pos), int(rot_dim), float(base),
          ROPE_SCALING[scaling], float(factor), float(original_length))
     return out
 
@@ -603,19 +630,19 @@ def rope_apply(x, rope_cs, positions=None, half=False, transpose=False, out=None
     (2i, 2i+1).  ``transpose``: the gradient with respect to x of an output gradient x.  ``out``: may
     be x itself."""
     tokens, stride = _rows(x, "x")
-    dev = x.device
-    H, D = x.shape[-2:]
-    n_pos, rot = _table_rot(rope_cs, dev)
-    _opt(positions, "positions", _I32, shape=x.shape[:-2], device=dev)
+    dev, shape = x.device, x.shape
+    H, D = shape[-2:]
+    pc, n_pos, rot = _table_rot(rope_cs, dev)
+    pp = _is_opt(positions, "positions", torch.int32, shape[:-2], dev)
     if out is None:
-        out = _new(x.shape, torch.bfloat16, dev, stream)
+        out = _new(shape, torch.bfloat16, dev, stream)
         out_stride = H * D
     else:
-        if tuple(out.shape) != tuple(x.shape):
-            raise ValueError(f"out: expected shape {tuple(x.shape)}, got {tuple(out.shape)}")
         _, out_stride = _rows(out, "out", device=dev)
-    _run(dev, stream, "rope_apply", _ptr(x), _ptr(out), _ptr(rope_cs), _ptr(positions), tokens, x.shape[-3], H, D,
-         stride, out_stride, n_pos, rot, int(bool(half)), int(bool(transpose)))
+        if out.shape != shape:
+            raise ValueError(f"out: expected shape {tuple(shape)}, got {tuple(out.shape)}")
+    _run(dev.index, stream, "rope_apply", x.data_ptr(), out.data_ptr(), pc, pp, tokens, shape[-3], H, D, stride,
+         out_stride, n_pos, rot, int(bool(half)), int(bool(transpose)))
     return out
 
 
@@ -626,14 +653,15 @@ def kv_cache_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, t
     scale per row (fp32 [n_pages, Hkv, page_size])."""
     tokens, ks = _rows(k, "k")
     dev = k.device
-    n_pages, page, Hkv, D, layout, dtype = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
-    _rows(k, "k", Hkv, D)
+    (n_pages, page, Hkv, D, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    if k.shape[-2:] != (Hkv, D):
+        _rows(k, "k", Hkv, D)
     tv, vs = _rows(v, "v", Hkv, D, dev)
     if tv != tokens:
         raise ValueError(f"k holds {tokens} tokens, v {tv}")
-    _arg(slots, "slots", _I64, shape=(tokens,), device=dev)
-    _run(dev, stream, "kv_cache_append", _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-         _ptr(slots), tokens, Hkv, D, ks, vs, n_pages, page, layout, dtype)
+    sl = _is(slots, "slots", torch.int64, (tokens,), dev)
+    _run(dev.index, stream, "kv_cache_append", k.data_ptr(), v.data_ptr(), *cache, sl, tokens, Hkv, D, ks, vs, n_pages,
+         page, layout, dtype)
 
 
 def rope_kv_cache_append(q, k, v, rope_cs, positions, k_cache, v_cache, slots, k_scale=None, v_scale=None, half=False,
@@ -642,22 +670,22 @@ def rope_kv_cache_append(q, k, v, rope_cs, positions, k_cache, v_cache, slots, k
     ``positions``: int32 [tokens].  Returns the rotated q."""
     tokens, qs = _rows(q, "q")
     dev = q.device
-    n_pages, page, Hkv, D, layout, dtype = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    (n_pages, page, Hkv, D, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
     Hq = q.shape[-2]
-    _rows(q, "q", Hq, D)
+    if q.shape[-1] != D:
+        _rows(q, "q", Hq, D)
     tk, ks = _rows(k, "k", Hkv, D, dev)
     tv, vs = _rows(v, "v", Hkv, D, dev)
     if not tokens == tk == tv:
         raise ValueError(f"q, k and v hold {tokens}, {tk} and {tv} tokens")
-    n_pos, rot = _table_rot(rope_cs, dev)
-    _arg(positions, "positions", _I32, shape=(tokens,), device=dev)
-    _arg(slots, "slots", _I64, shape=(tokens,), device=dev)
-    _opt(q_out, "q_out", _BF16, shape=q.shape, device=dev)
+    pc, n_pos, rot = _table_rot(rope_cs, dev)
+    pp = _is(positions, "positions", torch.int32, (tokens,), dev)
+    sl = _is(slots, "slots", torch.int64, (tokens,), dev)
     if q_out is None:
         q_out = _new(q.shape, torch.bfloat16, dev, stream)
-    _run(dev, stream, "rope_kv_cache_append", _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(rope_cs), _ptr(positions),
-         _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(slots), tokens, Hq, Hkv, D, qs, ks, vs,
-         n_pages, page, layout, dtype, n_pos, rot, int(bool(half)))
+    po = _is(q_out, "q_out", torch.bfloat16, q.shape, dev)
+    _run(dev.index, stream, "rope_kv_cache_append", q.data_ptr(), k.data_ptr(), v.data_ptr(), po, pc, pp, *cache, sl,
+         tokens, Hq, Hkv, D, qs, ks, vs, n_pages, page, layout, dtype, n_pos, rot, int(bool(half)))
     return q_out
 
 
@@ -666,17 +694,17 @@ def kv_cache_gather(k_cache, v_cache, page_table, cu_seqlens, total, k_scale=Non
     """Packed bf16 keys and values [total, Hkv, D] of sequences in a paged cache: ``page_table`` int32
     [n_seq, max_pages], ``cu_seqlens`` int32 [n_seq + 1] (0 .. total)."""
     dev = _arg(k_cache, "k_cache", _BF16 + _CODES, dim=4).device
-    n_pages, page, Hkv, D, layout, dtype = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
-    _arg(page_table, "page_table", _I32, dim=2, device=dev)
+    (n_pages, page, Hkv, D, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    pt = _arg(page_table, "page_table", _I32, dim=2, device=dev).data_ptr()
     n_seq, max_pages = page_table.shape
-    _arg(cu_seqlens, "cu_seqlens", _I32, shape=(n_seq + 1,), device=dev)
+    cu = _is(cu_seqlens, "cu_seqlens", torch.int32, (n_seq + 1,), dev)
     total = int(total)
-    for n, t in (("k_out", k_out), ("v_out", v_out)):
-        _opt(t, n, _BF16, shape=(total, Hkv, D), device=dev)
-    k_out = _new((total, Hkv, D), torch.bfloat16, dev, stream) if k_out is None else k_out
-    v_out = _new((total, Hkv, D), torch.bfloat16, dev, stream) if v_out is None else v_out
-    _run(dev, stream, "kv_cache_gather", _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
-         _ptr(cu_seqlens), _ptr(k_out), _ptr(v_out), n_seq, total, Hkv, D, n_pages, page, max_pages, layout, dtype)
+    shape = (total, Hkv, D)
+    k_out = _new(shape, torch.bfloat16, dev, stream) if k_out is None else k_out
+    v_out = _new(shape, torch.bfloat16, dev, stream) if v_out is None else v_out
+    pk, pv = _is(k_out, "k_out", torch.bfloat16, shape, dev), _is(v_out, "v_out", torch.bfloat16, shape, dev)
+    _run(dev.index, stream, "kv_cache_gather", *cache, pt, cu, pk, pv, n_seq, total, Hkv, D, n_pages, page, max_pages,
+         layout, dtype)
     return k_out, v_out
 
 
@@ -696,30 +724,30 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, ctx_lens, k_scale=None, v
     bf16, lse fp32 [B, Hq, T] or None); rows t >= q_lens[b] are not written."""
     dev = _arg(q, "q", _BF16, dim=4).device
     B, T, Hq, D = q.shape
-    n_pages, page, Hkv, Dc, layout, dtype = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    (n_pages, page, Hkv, Dc, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
     if Dc != D:
         raise ValueError(f"q has head dimension {D}, the cache {Dc}")
-    _arg(page_table, "page_table", _I32, dim=2, device=dev)
-    if page_table.shape[0] != B:
+    pt = _arg(page_table, "page_table", _I32, dim=2, device=dev).data_ptr()
+    rows, max_pages = page_table.shape
+    if rows != B:
         raise ValueError(f"page_table: expected {B} rows, got shape {tuple(page_table.shape)}")
-    max_pages = page_table.shape[1]
-    _arg(ctx_lens, "ctx_lens", _I32, shape=(B,), device=dev)
-    _opt(q_lens, "q_lens", _I32, shape=(B,), device=dev)
-    _opt(tree_mask, "tree_mask", _I64, shape=(B, T), device=dev)
-    _opt(out, "out", _BF16, shape=q.shape, device=dev)
-    _opt(lse, "lse", _F32, shape=(B, Hq, T), device=dev)
+    pc = _is(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
+    pl = _is_opt(q_lens, "q_lens", torch.int32, (B,), dev)
+    pm = _is_opt(tree_mask, "tree_mask", torch.int64, (B, T), dev)
     if workspace is None:
         with torch.cuda.device(dev):
-            need = decode_paged_workspace_bytes(B, T, Hq, Hkv, D, page, max_pages)
-        workspace = _new((need,), torch.uint8, dev, stream) if need else None
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+            wsb = decode_paged_workspace_bytes(B, T, Hq, Hkv, D, page, max_pages)
+        workspace = _new((wsb,), torch.uint8, dev, stream) if wsb else None
+    else:
+        if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        wsb = workspace.numel() * workspace.element_size()
     if out is None:
         out = _new(q.shape, torch.bfloat16, dev, stream)
     if lse is None and want_lse:
         lse = _new((B, Hq, T), torch.float32, dev, stream)
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _run(dev, stream, "attn_decode_paged", _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(out),
-         _ptr(lse), _ptr(page_table), _ptr(ctx_lens), _ptr(q_lens), _ptr(tree_mask), _ptr(workspace) if wsb else None, wsb,
-         B, T, Hq, Hkv, D, n_pages, page, max_pages, layout, dtype, float(scale))
+    po = _is(out, "out", torch.bfloat16, q.shape, dev)
+    ps = _is_opt(lse, "lse", torch.float32, (B, Hq, T), dev)
+    _run(dev.index, stream, "attn_decode_paged", q.data_ptr(), *cache, po, ps, pt, pc, pl, pm,
+         workspace.data_ptr() if wsb else None, wsb, B, T, Hq, Hkv, D, n_pages, page, max_pages, layout, dtype, float(scale))
     return out, lse
