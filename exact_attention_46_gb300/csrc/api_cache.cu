@@ -27,6 +27,9 @@ long long extent(long long tokens, long long stride, int heads, int D) {
   return (tokens - 1) * stride + static_cast<long long>(heads) * D;
 }
 
+// The row kernels number lane groups (a token's heads in fours, at worst one) in 31 bits.
+bool rows_fit(long long tokens, long long heads) { return tokens * (heads + 3) < 0x7fffff00ll; }
+
 int check_rows(const char* name, const void* ptr, long long stride, int n_tokens, int heads, int D) {
   if (ptr == nullptr || !api_aligned16(ptr))
     return api_fail(ATTN_ERR_INVALID_ARG, "%s must be a non-null, 16-byte aligned device pointer", name);
@@ -130,6 +133,7 @@ int append(const void* q, const void* k, const void* v, void* q_out, const float
       return api_fail(ATTN_ERR_INVALID_ARG, "positions must be a non-null, 4-byte aligned device pointer");
     if ((rc = check_rope(cs, n_pos, rot, D, rope_layout)) != ATTN_OK) return rc;
   }
+  if (!rows_fit(n_tokens, (rope ? Hq : 0) + 2ll * Hkv)) return api_fail(ATTN_ERR_INVALID_ARG, "too many rows");
   const size_t cb = cache_bytes(p.cache, D), sb = scale_bytes(p.cache);
   const Range outs[5] = {{kc, cb}, {vc, cb}, {ks, sb}, {vs, sb}, {q_out, 2ull * n_tokens * (rope ? Hq : 0) * D}};
   const Range ins[6] = {{q, rope ? 2ull * extent(n_tokens, q_stride, Hq, D) : 0},
@@ -139,8 +143,6 @@ int append(const void* q, const void* k, const void* v, void* q_out, const float
                         {positions, 4ull * n_tokens},
                         {cs, 4ull * n_pos * (rope ? rot : 0)}};
   if ((rc = check_disjoint(outs, 5, ins, 6)) != ATTN_OK) return rc;
-  const long long items = static_cast<long long>(n_tokens) * ((rope ? (Hq + 3) / 4 : 0) + 2 * ((Hkv + 3) / 4));
-  if (items * (D / 8) / 256 >= 0x7fffffffll) return api_fail(ATTN_ERR_INVALID_ARG, "too many rows");
   if ((rc = api_err_words(&p.err_word)) != ATTN_OK) return rc;
   p.err_info = p.err_word + 1;
   p.q = q;
@@ -213,13 +215,12 @@ int rope_apply(const void* x, void* out, const float* rope_cs, const int* positi
   if (positions == nullptr && (seq_len < 1 || seq_len > n_pos))
     return api_fail(ATTN_ERR_INVALID_ARG, "without positions, seq_len must be in [1, n_pos] (got %d, n_pos = %d)", seq_len, n_pos);
   if (transpose != 0 && transpose != 1) return api_fail(ATTN_ERR_INVALID_ARG, "transpose must be 0 or 1");
+  if (!rows_fit(n_tokens, H)) return api_fail(ATTN_ERR_INVALID_ARG, "too many rows");
   const size_t xb = 2ull * extent(n_tokens, x_stride, H, D), ob = 2ull * extent(n_tokens, out_stride, H, D);
   const bool in_place = x == out && x_stride == out_stride;
   const Range outs[1] = {{out, ob}};
   const Range ins[3] = {{in_place ? nullptr : x, xb}, {rope_cs, 4ull * n_pos * rot_dim}, {positions, 4ull * n_tokens}};
   if ((rc = check_disjoint(outs, 1, ins, 3)) != ATTN_OK) return rc;
-  if (static_cast<long long>(n_tokens) * ((H + 3) / 4) * (D / 8) / 256 >= 0x7fffffffll)
-    return api_fail(ATTN_ERR_INVALID_ARG, "too many rows");
   RopeApplyParams p{};
   if ((rc = api_err_words(&p.err_word)) != ATTN_OK) return rc;
   p.err_info = p.err_word + 1;
@@ -265,8 +266,7 @@ int kv_cache_gather(const void* k_cache, const void* v_cache, const float* k_sca
     return api_fail(ATTN_ERR_INVALID_ARG, "page_table and cu_seqlens must be non-null, 4-byte aligned device pointers");
   if (k_out == nullptr || v_out == nullptr || !api_aligned16(k_out) || !api_aligned16(v_out))
     return api_fail(ATTN_ERR_INVALID_ARG, "k_out and v_out must be non-null, 16-byte aligned device pointers");
-  if (static_cast<long long>(total) * ((Hkv + 3) / 4) * (D / 8) / 256 >= 0x7fffffffll)
-    return api_fail(ATTN_ERR_INVALID_ARG, "too many rows");
+  if (!rows_fit(total, Hkv)) return api_fail(ATTN_ERR_INVALID_ARG, "too many rows");
   const size_t cb = cache_bytes(p.cache, D), sb = scale_bytes(p.cache), ob = 2ull * total * Hkv * D;
   const Range outs[2] = {{k_out, ob}, {v_out, ob}};
   const Range ins[6] = {{k_cache, cb}, {v_cache, cb}, {k_scale, sb}, {v_scale, sb},

@@ -103,6 +103,23 @@ def test_append_matches_oracle(T, Hq, Hkv, D, page, token_major, fp8, turn):
             assert torch.equal(scales_of(t, rest, page), scales_of(b, rest, page))
 
 
+def test_codes_are_those_of_the_fp32_quotient():
+    # unrotated rows of very different sizes: scale and codes are bit for bit amax / 448 and the E4M3
+    # rounding of x / scale in fp32 (torch's division -- by a tensor: by a number it multiplies with a
+    # rounded reciprocal -- and cast)
+    T, H, D, page = 4096, 4, 128, 64
+    x = synth.normal((T, H, D), synth.seed_for(145, 0)) * np.exp2(np.random.default_rng(9).uniform(-90, 90, (T, H, 1)))
+    k = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    (kc, vc), (ks, vs) = new_cache(T // page, H, page, D, True, False)
+    ops.kv_cache_append(k, k, kc, vc, torch.arange(T, device="cuda"), ks, vs)
+    ops.check()
+    amax = k.float().abs().amax(-1)
+    scale = amax / torch.full_like(amax, 448.0)
+    codes = (k.float() / scale[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(ks.transpose(1, 2).reshape(T, H), scale)
+    assert torch.equal(kc.transpose(1, 2).reshape(T, H, D), codes)
+
+
 def test_rows_that_are_not_finite_or_tiny():
     D, page = 64, 16
     k = torch.ones((4, 1, D), dtype=torch.bfloat16)
