@@ -161,7 +161,7 @@ int append(const void* q, const void* k, const void* v, void* q_out, const float
   return api_ok();
 }
 
-// CTAs of attn_decode_paged's key kernel on the current device: one per SM.
+// CTAs of attn_decode_paged's key kernel on the current device: one per SM, in groups of one per row tile.
 int paged_ctas() {
   static std::atomic<int> known[64];               // SM count by device: a constant of the hardware
   int dev = 0, n = 0;
@@ -175,7 +175,8 @@ int paged_ctas() {
 // A unit can be shared by CTAs only if some sequence can have more than one 128-key tile.
 bool paged_combines(int page_size, int max_pages) { return static_cast<long long>(page_size) * max_pages > 128; }
 
-// Two partial units a CTA (the one it starts in and the one it ends in): RB rows of D + 1 floats.
+// Two partial units a CTA (the one it starts in and the one it ends in): RB rows of D + 1 floats.  Where
+// there are more row tiles than CTAs there is one group and nothing is cut.
 size_t paged_workspace(int n_cta, int RB, int D) { return 8ull * n_cta * RB * (static_cast<size_t>(D) + 1); }
 
 }  // namespace
@@ -326,9 +327,8 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
     return api_fail(ATTN_ERR_UNSUPPORTED, "(Hq / Hkv) * T = %lld query rows per key/value head, at most 65535",
                     G * static_cast<long long>(T));
   const int RB = paged_rows(G * T), row_tiles = (G * T + RB - 1) / RB;
-  if (static_cast<long long>(B) * Hkv * row_tiles > 0x7fffffffll) return api_fail(ATTN_ERR_INVALID_ARG, "too many work units");
-  const int n_cta = paged_ctas();
-  const size_t need = paged_combines(page_size, max_pages) ? paged_workspace(n_cta, RB, D) : 0;
+  const int sms = paged_ctas(), group = row_tiles < sms ? row_tiles : sms, n_cta = sms / group;
+  const size_t need = paged_combines(page_size, max_pages) ? paged_workspace(sms, RB, D) : 0;
   if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need || !api_aligned16(workspace))
       return api_fail(ATTN_ERR_INVALID_ARG, "a 16-byte aligned workspace of %zu bytes is needed "
@@ -356,6 +356,10 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
   p.tree_mask = tree_mask;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  p.v_cache = v_cache;
+  p.page_stride = c.page_stride;
+  p.head_stride = c.head_stride;
+  p.tok_stride = c.tok_stride;
   p.B = B;
   p.T = T;
   p.Hq = Hq;
@@ -367,8 +371,9 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
   p.max_pages = max_pages;
   p.row_tiles = row_tiles;
   p.n_cta = n_cta;
+  p.group_ctas = group;
   p.ws_o = static_cast<float*>(workspace);
-  p.ws_l = need > 0 ? p.ws_o + 2ll * p.n_cta * RB * D : nullptr;
+  p.ws_l = need > 0 ? p.ws_o + 2ll * sms * RB * D : nullptr;
   const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));
   p.c_log2 = sc * 1.4426950408889634f;
   p.spin_limit = api_spin_limit();

@@ -1,5 +1,6 @@
 // attn_paged.cu -- attention of one or a few (drafted) query tokens per sequence over a paged
-// key/value cache, for sm_103a.  The hada.io FA3 summary ("Weitere Optimierungen und künftige
+// key/value cache, up to 32 query rows (heads of a group x tokens) per key/value head, for sm_103a;
+// attn_tree.cu takes more.  The hada.io FA3 summary ("Weitere Optimierungen und künftige
 // Integration") names LLM inference as future work and defines nothing; the readings are below.
 //
 // Sequence b has ctx_lens[b] cached keys and after them the q_lens[b] drafted tokens' own keys,
@@ -12,8 +13,8 @@
 // The work is one pass over K and V: 2 L D bytes (E4M3) or 4 L D (bf16) per key/value head, for
 // G * T <= 32 query rows far below the tensor pipe's rate, so HBM bounds it and the kernel is built
 // to keep loads in flight whatever the lengths are:
-//   * the unit is (sequence, key/value head, tile of RB packed rows r = t * G + g); its keys are cut
-//     into 128-key tiles and the tiles of all units form one list.  CTA i of N (one per SM) takes
+//   * the unit is (sequence, key/value head) with its RB packed rows r = t * G + g; its keys are cut into
+//     128-key tiles and the tiles of all units form one list.  CTA i of N (one per SM) takes
 //     tiles [i W / N, (i + 1) W / N) of the W, so every SM streams the same number of bytes for
 //     any mix of lengths, and the lengths stay on the device.  A unit that several CTAs share
 //     leaves one partial (o, lse) per CTA in the workspace; a second, dependent kernel merges them
@@ -41,17 +42,16 @@
 #include <type_traits>
 
 #include "cache.h"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace ea46 {
 
 namespace {
 
-constexpr float LN2_P = 0.69314718055994530942f;
 constexpr int NWARP = 8;                        // consumer warps
 constexpr int NPROD = 4;                        // producer warps: (key, value) x (even, odd copies)
 constexpr int NTHREADS = 32 * (NWARP + NPROD);
-enum : int { WHERE_PAGED_LOAD = 51, WHERE_PAGED_USE = 52, WHERE_PAGED_LENS = 53, WHERE_PAGED_PAGE = 54 };
 
 // NRB: 8-row blocks of a warp (1, 2).  WIDE: a warp group per 16 of 32 rows; otherwise the two
 // groups take the same rows and turns by tile.
@@ -139,100 +139,6 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
       : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
-// 16-byte asynchronous copy global -> shared, and an arrival on `bar` when this thread's copies so
-// far have landed (counted in the barrier's initial count).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-__device__ __forceinline__ void wait_drain_paged(uint32_t bar, uint32_t parity, long long limit) {
-  if (mbar_try_wait(bar, parity)) return;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > limit) return;
-}
-
-// Prefix sums of the sequences' key tiles into pre[0 .. B]; returns 0 if any length is out of
-// range.  Called by all `n` threads (n >= 32 a multiple of 32, n <= 1024).
-__device__ __forceinline__ bool tile_prefix(const PagedParams& p, int* pre, int* scratch, int n) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.B + n - 1) / n, b0 = tid * per, b1 = min(p.B, b0 + per);
-  bool ok = true;
-  int sum = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int ctx = __ldg(p.ctx_lens + b), ql = p.q_lens != nullptr ? __ldg(p.q_lens + b) : p.T;
-    const bool fine = ctx >= 0 && ql >= 0 && ql <= p.T &&
-                      static_cast<long long>(ctx) + ql <= static_cast<long long>(p.max_pages) * p.page_size;
-    ok = ok && fine;
-    const int tiles = fine && ql > 0 ? (ctx + ql + 127) >> 7 : 0;
-    pre[b + 1] = tiles;                       // own entries only, until the scan below
-    sum += tiles;
-  }
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) scratch[warp] = incl;
-  ok = __syncthreads_and(ok);
-  int off = incl - sum;
-  for (int w = 0; w < warp; ++w) off += scratch[w];
-  for (int b = b0; b < b1; ++b) {
-    off += pre[b + 1];
-    pre[b + 1] = off;
-  }
-  if (tid == 0) pre[0] = 0;
-  __syncthreads();
-  return ok;
-}
-
-// The piece of the tile list that starts at x and ends at x1 or with its unit.
-struct Segment {
-  int b, hkv, rt;       // sequence, key/value head, row tile
-  int t0, t1, n;        // tiles [t0, t1) of the unit's n
-};
-
-// x / y for y > 0, in 32 bits where both fit (the 64-bit division is a few hundred cycles).
-__device__ __forceinline__ long long quotient(long long x, long long y) {
-  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-  return x / y;
-}
-
-// Token of packed row r: r / G by multiplication (r, G < 2^16).
-__device__ __forceinline__ int token_of(const PagedParams& p, int r) {
-  return p.g_magic == 0 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.g_magic));
-}
-
-__device__ __forceinline__ Segment find_segment(const PagedParams& p, const int* pre, long long x, long long x1) {
-  const long long hr = static_cast<long long>(p.Hkv) * p.row_tiles;
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] * hr <= x) lo = mid; else hi = mid;
-  }
-  // x lies in sequence lo: empty ones before it have pre[lo + 1] == pre[lo]
-  Segment s;
-  s.b = lo;
-  s.n = pre[lo + 1] - pre[lo];
-  const long long y = x - pre[lo] * hr;
-  const int u = static_cast<int>(quotient(y, s.n));
-  s.hkv = p.row_tiles == 1 ? u : u / p.row_tiles;
-  s.rt = u - s.hkv * p.row_tiles;
-  s.t0 = static_cast<int>(y - static_cast<long long>(u) * s.n);
-  const long long left = x1 - x;
-  s.t1 = left < s.n - s.t0 ? s.t0 + static_cast<int>(left) : s.n;
-  return s;
-}
-
-__device__ __forceinline__ long long cta_start(long long i, long long W, long long N) { return quotient(i * W, N); }
-
 template <int D, bool FP8, int NRB, bool WIDE>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -265,7 +171,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (threadIdx.x == 0 && blockIdx.x == 0 && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_LENS);
     return;
   }
-  const long long W = static_cast<long long>(pre[p.B]) * p.Hkv * p.row_tiles;
+  const long long W = static_cast<long long>(pre[p.B]) * p.Hkv;
   const long long N = W < p.n_cta ? W : p.n_cta;
   if (static_cast<long long>(blockIdx.x) >= N) return;
   const long long x0 = cta_start(blockIdx.x, W, N), x1 = cta_start(blockIdx.x + 1ll, W, N);
@@ -287,7 +193,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int panel = C::NPANEL == 2 ? odd : 0;
     const uint64_t pol = l2_policy_evict_first();
     int it = 0;
-    for (long long x = x0; x < x1;) {
+    bool dead = false;                             // a wait gave up (the same in every lane)
+    for (long long x = x0; x < x1 && !dead;) {
       const Segment s = find_segment(p, pre, x, x1);
       const int L = __ldg(p.ctx_lens + s.b) + (p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T);
       const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
@@ -299,7 +206,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       };
       const int batch = 32 >> pt_log;              // tiles of a batch
       int next = look_up(s.t0);
-      for (int j0 = s.t0; j0 < s.t1; j0 += batch) {
+      for (int j0 = s.t0; j0 < s.t1 && !dead; j0 += batch) {
         const int page = next;
         next = look_up(j0 + batch);
         const int key = 128 * j0 + (lane << br_log);
@@ -310,7 +217,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int row = key & (p.page_size - 1);
         for (int i = 0; i < batch && j0 + i < s.t1; ++i, ++it) {
           const int slot = it % NSTAGE;
-          if (!warp_wait(BAR_EMPTY(slot), ((it / NSTAGE) & 1) ^ 1u, ctl, WHERE_PAGED_LOAD)) break;
+          dead = !warp_wait(BAR_EMPTY(slot), ((it / NSTAGE) & 1) ^ 1u, ctl, WHERE_PAGED_LOAD);
+          if (dead) break;
           const unsigned mine = (boxes >> (i << pt_log)) & ((1u << per_tile) - 1) & my_boxes;
           if (lane == 0) mbar_arrive_expect_tx(BAR_FULL(slot), (__popc(mine) << br_log) * C::PANEL_ROW);
           __syncwarp();
@@ -330,12 +238,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             cp_async_arrive(BAR_FULL(slot));
           }
         }
-        if (*abort_flag) break;
       }
-      if (*abort_flag) break;
       x += s.t1 - s.t0;
     }
-    if (*abort_flag) {
+    if (dead) {
       cp_async_wait_all();
       if (lane == 0)
         for (int i = it > NSTAGE ? it - NSTAGE : 0; i < it; ++i)
@@ -379,7 +285,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int i = 0; i < QN; ++i) {
       const int e = static_cast<int>(threadIdx.x) + i * 32 * NWARP;
       const int l = e & 31, ks = (e >> 5) % C::KS, rb = (e >> 5) / C::KS;
-      const int pr = sg.rt * RB + 8 * rb + (l >> 2), t = token_of(p, pr);
+      const int pr = 8 * rb + (l >> 2), t = token_of(p, pr);
       qraw[i] = make_uint2(0u, 0u);
       if (rb < RB / 8 && t < p.T) {                // rows past q_len are computed and not written
         const __nv_bfloat16* src = qb + (static_cast<long long>(t) * p.Hq + pr - t * p.G) * D;
@@ -395,7 +301,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
     my_bits = 0;
     if (threadIdx.x < RB) {
-      const int t = token_of(p, sg.rt * RB + static_cast<int>(threadIdx.x));
+      const int t = token_of(p, static_cast<int>(threadIdx.x));
       if (t < p.T)
         my_bits = p.tree_mask != nullptr ? __ldg(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
                                          : (t >= 63 ? ~0ull : (2ull << t) - 1);
@@ -527,7 +433,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
         // ---- scales of this thread's four keys ----
-        float ksc[2][2], vsc[2][2];
+        [[maybe_unused]] float ksc[2][2], vsc[2][2];
         if constexpr (FP8) {
           const float* sc = reinterpret_cast<const float*>(base + slot * C::STAGE_BYTES + 2 * C::TILE_BYTES) + kw;
           float top = 0.f;
@@ -806,10 +712,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       float M, l;
       whole_row(r, M, l);
       const float lse2 = l == 0.f ? -INFINITY : M + __log2f(l);
-      const int pr = dn.rt * RB + r, t = token_of(p, pr);
+      const int t = token_of(p, r);
       if (!whole) p.ws_l[ws_slot * RB + r] = lse2;
       else if (t < ql_dn && p.lse != nullptr)
-        p.lse[(static_cast<long long>(dn.b) * p.Hq + dn.hkv * p.G + pr - t * p.G) * p.T + t] = lse2 * LN2_P;
+        p.lse[(static_cast<long long>(dn.b) * p.Hq + dn.hkv * p.G + r - t * p.G) * p.T + t] = lse2 * LN2_P;
     }
     // 32 columns at a time: column 16 m + 8 y + g of the buffer is row g + 8 y of O^T's block m
 #pragma unroll
@@ -849,11 +755,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           a += src[i0];
           b += src[i1];
         }
-        const int pr = dn.rt * RB + r, t = token_of(p, pr);
+        const int t = token_of(p, r);
         if (t < ql_dn) {
           if (whole)
             *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) +
-                                         ((static_cast<long long>(dn.b) * p.T + t) * p.Hq + dn.hkv * p.G + pr - t * p.G) * D + d) =
+                                         ((static_cast<long long>(dn.b) * p.T + t) * p.Hq + dn.hkv * p.G + r - t * p.G) * D + d) =
                 pack_bf16x2(a, b);
           else
             *reinterpret_cast<float2*>(p.ws_o + (ws_slot * RB + r) * D + d) = make_float2(a, b);
@@ -864,8 +770,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-// Merge of the units that several CTAs share.  Block i looks at the start of CTA i + 1's tiles: where
-// that is the first cut inside a unit, the block merges the unit -- N - 1 blocks whatever the batch.
+// Merge of the units that several groups share.  A block looks at the start of group i + 1's tiles: where
+// that is the first cut inside a unit, it merges one row tile of the unit -- N - 1 blocks a row tile,
+// whatever the batch.
 // Its warps take the rows; with fewer rows than warps several warps share a row's parts.
 template <int D, int RB>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p) {
@@ -875,9 +782,9 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
   __shared__ float part[NW][D + 2];
   const bool ok = tile_prefix(p, pre, scratch, 32 * NW);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long hr = static_cast<long long>(p.Hkv) * p.row_tiles;
-  const long long W = ok ? pre[p.B] * hr : 0, N = W < p.n_cta ? W : p.n_cta;
-  const long long i = blockIdx.x + 1ll;
+  const long long W = ok ? static_cast<long long>(pre[p.B]) * p.Hkv : 0, N = W < p.n_cta ? W : p.n_cta;
+  const long long i = blockIdx.x / p.row_tiles + 1ll;
+  const int rt = static_cast<int>(blockIdx.x % p.row_tiles);
   bool mine = i < N;
   Segment s{};
   long long c1 = 0;
@@ -885,15 +792,15 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
   if (mine) {
     const long long x = cta_start(i, W, N);
     s = find_segment(p, pre, x, W);
-    // the CTA that holds list position y is the last c with c W / N <= y
+    // the group that holds list position y is the last c with c W / N <= y
     mine = s.t0 > 0 && quotient((x - s.t0 + 1) * N - 1, W) == i - 1;
     c1 = quotient((x - s.t0 + s.n) * N - 1, W);
     ql = p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T;
   }
   grid_dependency_wait();       // in every block: this grid's end stands for the key kernel's too
   if (!mine) return;
-  const int c0 = static_cast<int>(i - 1), n = static_cast<int>(c1) - c0 + 1;      // parts: CTAs c0 .. c1
-  const int left = ql * p.G - s.rt * RB, rows = left < RB ? left : RB;
+  const int c0 = static_cast<int>(i - 1), n = static_cast<int>(c1) - c0 + 1;      // parts: groups c0 .. c1
+  const int left = ql * p.G - rt * RB, rows = left < RB ? left : RB;
   const int share_log = rows >= 8 ? 0 : (rows > 4 ? 0 : (rows > 2 ? 1 : (rows > 1 ? 2 : 3)));   // warps of a row
   const int share = 1 << share_log;
   for (int r0 = 0; r0 < rows; r0 += NW >> share_log) {
@@ -903,7 +810,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     // c0's part is its last unit's (slot 1), the others' their first's (slot 0)
-    auto slot = [&](int c) { return 2ll * (c0 + c) + (c == 0 ? 1 : 0); };
+    auto slot = [&](int c) { return 2ll * ((c0 + c) * static_cast<long long>(p.row_tiles) + rt) + (c == 0 ? 1 : 0); };
     if (live) {
       for (int c = lane; c < n; c += 32) mx = fmaxf(mx, __ldcg(p.ws_l + slot(c) * RB + r));
 #pragma unroll
@@ -952,7 +859,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
         }
     }
     if (live && sub == 0) {
-      const int pr = s.rt * RB + r, t = token_of(p, pr);
+      const int pr = rt * RB + r, t = token_of(p, pr);
       const float inv = sum == 0.f ? 1.f : 1.f / sum;          // no key at all: the parts' zeros
       const long long h = static_cast<long long>(s.hkv) * p.G + pr - t * p.G;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<long long>(s.b) * p.T + t) * p.Hq + h) * D + lane * E;
@@ -962,6 +869,22 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
         p.lse[(static_cast<long long>(s.b) * p.Hq + h) * p.T + t] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * LN2_P;
     }
   }
+}
+
+// The merge starts while the key kernel's last CTAs finish and waits for them on the device.
+template <int D, int RB>
+cudaError_t launch_paged_combine(const PagedParams& p, cudaStream_t st) {
+  if (p.n_cta < 2) return cudaSuccess;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_cta - 1) * p.row_tiles);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, RB>, p);
 }
 
 template <int D, bool FP8, int NRB, bool WIDE>
@@ -978,18 +901,8 @@ cudaError_t launch_paged_d(const CUtensorMap& tk, const CUtensorMap& tv, const P
     configured.fetch_or(bit);
   }
   attn_paged_kernel<D, FP8, NRB, WIDE><<<p.n_cta, NTHREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess || !combine || p.n_cta < 2) return e;
-  // the merge starts while the last CTAs finish and waits for them on the device
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.n_cta - 1);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, C::RB>, p);
+  if ((e = cudaGetLastError()) != cudaSuccess || !combine) return e;
+  return launch_paged_combine<D, C::RB>(p, st);
 }
 
 template <int D, bool FP8>
@@ -1002,8 +915,13 @@ cudaError_t launch_paged_m(const CUtensorMap& tk, const CUtensorMap& tv, const P
 
 }  // namespace
 
+cudaError_t launch_tree_combine(const PagedParams& p, int D, cudaStream_t st) {
+  return D == 64 ? launch_paged_combine<64, PAGED_TREE_ROWS>(p, st) : launch_paged_combine<128, PAGED_TREE_ROWS>(p, st);
+}
+
 cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
                               bool combine, cudaStream_t st) {
+  if (paged_rows(p.G * p.T) == PAGED_TREE_ROWS) return launch_attn_tree(tk, tv, p, D, fp8, combine, st);
   if (D == 64) return fp8 ? launch_paged_m<64, true>(tk, tv, p, combine, st) : launch_paged_m<64, false>(tk, tv, p, combine, st);
   return fp8 ? launch_paged_m<128, true>(tk, tv, p, combine, st) : launch_paged_m<128, false>(tk, tv, p, combine, st);
 }

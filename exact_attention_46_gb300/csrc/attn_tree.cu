@@ -1,0 +1,702 @@
+// attn_tree.cu -- attention of a drafted tree (or many heads) over a paged key/value cache: more than 32
+// query rows (heads of a group x drafted tokens) per key/value head, for sm_103a.  What it
+// computes, the readings and the list of key tiles are attn_paged.cu's and paged.cuh's.
+//
+// With 33 or more rows the 128-row tile of tcgen05 is used well: S = Q K^T and O += P V run on it with
+// S, P and O in Tensor Memory, one softmax thread per row.  128 rows take about 1100 cycles of the
+// tensor pipe and about as many of the exp2 units per 128-key tile of D = 128 in bf16, against the 2800
+// the tile takes from HBM at an SM's share of it, so one row tile is bound by HBM and several by
+// compute; the CTAs of a group take one row tile each and the same keys, which all but the first find
+// in L2.
+//   * warps 0..3 softmax (thread = row), 4 issues the MMAs, 5 and 6 load K and V tiles by TMA (one box
+//     per page and swizzle panel) through a ring each, 7 the E4M3 scales;
+//   * S and P are double-buffered: S(i + 1) is issued before PV(i).  The running maximum is lazy (O is
+//     rescaled in Tensor Memory only when a maximum moves by more than 2^TAU);
+//   * the next unit's queries are written to shared memory before the last unit's epilogue, so its
+//     first S is computed meanwhile;
+//   * E4M3: the products run on the codes themselves.  A query row, scaled by a power of two into
+//     E4M3's range, is the exact sum of two E4M3 terms (bf16 has eight significant bits, each term
+//     four; below 2^-10 of the row's largest element the second loses bits, 2^-18 of the largest at
+//     most), and a numerator times its value's scale is rounded to the sum of two: 2^-8 of it, as bf16
+//     would be, because one E4M3 term (2^-4) is too coarse and the tensor core takes no mixed types.
+//     Each term is one more MMA over the same tile;
+//   * hidden keys: logits replaced by -inf before the maximum.  In tiles with drafted keys or the end of
+//     the sequence the value rows past the end are zeroed in shared memory, and so is what is not
+//     finite in a drafted row; the rows that see it get it in the epilogue (E4M3: a scale that is
+//     not finite makes their numerators NaN).
+// Every mbarrier wait is bounded.
+#include <atomic>
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "cache.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace ea46 {
+
+namespace {
+
+template <int D, bool FP8>
+struct TreeCfg {
+  static constexpr int ESZ = FP8 ? 1 : 2;
+  static constexpr int ROW_BYTES = D * ESZ;
+  static constexpr int PANEL_ROW = ROW_BYTES >= 128 ? 128 : ROW_BYTES;
+  static constexpr int NPANEL = ROW_BYTES / PANEL_ROW;
+  static constexpr int PANEL_BYTES = 128 * PANEL_ROW;
+  static constexpr int TILE_BYTES = 128 * ROW_BYTES;
+  static constexpr int NQ = FP8 ? 2 : 1;                      // query tiles: terms of the queries
+  // K and V tiles in flight
+  static constexpr int NK = TILE_BYTES == 32768 ? 3 : (TILE_BYTES == 16384 ? 5 : 8);
+  static constexpr int NV = TILE_BYTES == 32768 ? 2 : (TILE_BYTES == 16384 ? 5 : 8);
+  static constexpr int NSC = FP8 ? 4 : 0;                     // stages of 128 key and 128 value scales
+  static constexpr uint32_t SBO = 8 * PANEL_ROW;
+  static constexpr uint32_t LAYOUT = PANEL_ROW == 128 ? 2u : 4u;
+  static constexpr int KSTEPS_QK = ROW_BYTES / 32;
+  static constexpr int STEPS_PER_PANEL = PANEL_ROW / 32;
+  static constexpr int UMMA_K = FP8 ? 32 : 16;
+  static constexpr int KSTEPS_PV = 128 / UMMA_K;
+  static constexpr uint32_t FMT = FP8 ? 0u : 1u;
+  static constexpr uint32_t IDESC_QK = instr_desc(FMT, 0, 128, 128);
+  static constexpr uint32_t IDESC_PV = instr_desc(FMT, 1, 128, D);
+  // Tensor Memory: S buffers at columns 0 and 128, O at 256, two P buffers of 64 columns after O (E4M3: 32
+  // for each term)
+  static constexpr uint32_t O_COL = 256, P_COL = 256 + D;
+  static constexpr int K_OFF = NQ * TILE_BYTES, V_OFF = K_OFF + NK * TILE_BYTES;
+  static constexpr int SC_OFF = V_OFF + NV * TILE_BYTES;
+  static constexpr int PRE_OFF = SC_OFF + NSC * 1024;
+  static constexpr int FLAG_OFF = PRE_OFF + (PAGED_MAX_BATCH + 2) * 4;      // vodd [2] x 8, scratch, abort, tmem
+  static constexpr int BAR_OFF = FLAG_OFF + 64;
+  static constexpr int NBAR = 8 + 2 * (NK + NV + NSC);
+  static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NBAR * 8;
+  static_assert(FLAG_OFF % 8 == 0 && BAR_OFF % 8 == 0, "alignment");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(P_COL + 128 <= 512, "Tensor Memory budget");
+};
+
+constexpr int TREE_THREADS = 256;
+// Lazy rescale threshold (log2).  Numerators reach 2^TAU; E4M3's two terms then span [2^-10, 2^8] around
+// numerators scaled by 2^7.
+constexpr float TAU_BF16 = 8.0f, TAU_E4M3 = 1.0f;
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// x (two fp16) as two E4M3 terms: hi = E4M3(x), lo = E4M3(x - hi); the pairs in the low 16 bits.
+__device__ __forceinline__ void e4m3_terms(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, d;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 b, h;\n\t"
+      "sub.rn.f16x2 d, %2, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\t"
+      "cvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
+      : "=r"(hi), "=r"(lo) : "r"(x));
+}
+
+__device__ __forceinline__ void e4m3_terms4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+  uint32_t h0, l0, h1, l1;
+  e4m3_terms(f16x2(a, b), h0, l0);
+  e4m3_terms(f16x2(c, d), h1, l1);
+  hi = __byte_perm(h0, h1, 0x5410);
+  lo = __byte_perm(l0, l1, 0x5410);
+}
+
+__device__ __forceinline__ bool finite_f(float x) { return fabsf(x) < INFINITY; }
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(TREE_THREADS, 1)
+    attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const PagedParams p) {
+  using C = TreeCfg<D, FP8>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_u32 - raw_u32);
+  const uint32_t sQ = base_u32, sK = base_u32 + C::K_OFF, sV = base_u32 + C::V_OFF;
+  int* pre = reinterpret_cast<int*>(base + C::PRE_OFF);
+  unsigned long long* vodd_sh = reinterpret_cast<unsigned long long*>(base + C::FLAG_OFF);   // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::FLAG_OFF + 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::FLAG_OFF + 20);
+  int* scratch = reinterpret_cast<int*>(base + C::FLAG_OFF + 24);                            // [8]
+  const uint32_t bar0 = base_u32 + C::BAR_OFF;
+  const uint32_t BAR_Q = bar0, BAR_O = bar0 + 8, BAR_DONE = bar0 + 16, BAR_PV = bar0 + 24;
+  auto BAR_S = [&](int b) { return bar0 + 32 + 8u * b; };
+  auto BAR_P = [&](int b) { return bar0 + 48 + 8u * b; };
+  auto FULLK = [&](int s) { return bar0 + 64 + 8u * s; };
+  auto EMPTYK = [&](int s) { return bar0 + 64 + 8u * (C::NK + s); };
+  auto FULLV = [&](int s) { return bar0 + 64 + 8u * (2 * C::NK + s); };
+  auto EMPTYV = [&](int s) { return bar0 + 64 + 8u * (2 * C::NK + C::NV + s); };
+  auto FULLS = [&](int s) { return bar0 + 64 + 8u * (2 * (C::NK + C::NV) + s); };
+  auto EMPTYS = [&](int s) { return bar0 + 64 + 8u * (2 * (C::NK + C::NV) + C::NSC + s); };
+
+  const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
+  if (threadIdx.x == 0) {
+    mbar_init(BAR_Q, 4);
+    mbar_init(BAR_O, 1);
+    mbar_init(BAR_DONE, 1);
+    mbar_init(BAR_PV, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(BAR_S(b), 1);
+      mbar_init(BAR_P(b), 4);
+    }
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(FULLK(s), 1);
+      mbar_init(EMPTYK(s), 1);
+    }
+    for (int s = 0; s < C::NV; ++s) {
+      mbar_init(FULLV(s), 1);
+      mbar_init(EMPTYV(s), 1);
+    }
+    for (int s = 0; s < C::NSC; ++s) {
+      mbar_init(FULLS(s), 32);
+      mbar_init(EMPTYS(s), 4);
+    }
+    *abort_flag = 0;
+    vodd_sh[0] = vodd_sh[1] = 0;
+    fence_barrier_init();
+  }
+  grid_launch_dependents();
+  const bool fine = tile_prefix(p, pre, scratch, TREE_THREADS);
+  if (!fine) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_LENS);
+    return;
+  }
+  const long long W = static_cast<long long>(pre[p.B]) * p.Hkv;
+  const long long N = W < p.n_cta ? W : p.n_cta;
+  const int group = blockIdx.x / p.group_ctas, rt0 = blockIdx.x % p.group_ctas;
+  if (group >= N) return;
+  const long long x0 = cta_start(group, W, N), x1 = cta_start(group + 1ll, W, N);
+  if (warp == 4) tmem_alloc(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{p.spin_limit, abort_flag, p.err_word, p.err_info};
+
+  if (warp >= 5) {
+    // ---- loads: K (warp 5), V (6), E4M3 scales (7).  Box i of a segment's list of boxes is br rows of
+    // one page; lane i % 32 looks its page up, one batch of 32 boxes ahead, and issues its copies ----
+    if (FP8 || warp < 7) {
+      const bool is_k = warp == 5, is_s = warp == 7;
+      const CUtensorMap* tm = is_k ? &tmK : &tmV;
+      const int ps_log = 31 - __clz(p.page_size), br_log = ps_log < 7 ? ps_log : 7;
+      const int pt_log = 7 - br_log, per_tile = 1 << pt_log, batch = 32 >> pt_log;
+      const int stages = is_s ? C::NSC : (is_k ? C::NK : C::NV);
+      const uint64_t pol = p.row_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+      int it = 0, slot = 0;
+      uint32_t par = 1;
+      bool dead = false;                           // a wait gave up (the same in every lane)
+      for (int rt = rt0; rt < p.row_tiles && !dead; rt += p.group_ctas)
+        for (long long x = x0; x < x1 && !dead;) {
+          const Segment s = find_segment(p, pre, x, x1);
+          const int L = __ldg(p.ctx_lens + s.b) + (p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T);
+          const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
+          auto look_up = [&](int j) {
+            const int at = (128 * j + (lane << br_log)) >> ps_log;
+            return j < s.t1 && at < p.max_pages ? __ldg(table + at) : -1;
+          };
+          int next = look_up(s.t0);
+          for (int j0 = s.t0; j0 < s.t1 && !dead; j0 += batch) {
+            const int page = next;
+            next = look_up(j0 + batch);
+            const int key = 128 * j0 + (lane << br_log);
+            const bool wanted = key < L && j0 + (lane >> pt_log) < s.t1;
+            const bool good = wanted && page >= 0 && page < p.n_pages;
+            if (is_k && wanted && !good && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_PAGE);
+            const unsigned boxes = __ballot_sync(0xffffffffu, good);
+            const int row = key & (p.page_size - 1);
+            for (int i = 0; i < batch && j0 + i < s.t1; ++i, ++it) {
+              dead = !warp_wait(is_s ? EMPTYS(slot) : (is_k ? EMPTYK(slot) : EMPTYV(slot)), par, ctl, WHERE_PAGED_LOAD);
+              if (dead) break;
+              if (!is_s) {
+                const uint32_t full = is_k ? FULLK(slot) : FULLV(slot);
+                const uint32_t dst = (is_k ? sK : sV) + slot * C::TILE_BYTES;
+                const unsigned mine = (boxes >> (i << pt_log)) & ((1u << per_tile) - 1);
+                if (lane == 0) mbar_arrive_expect_tx(full, (__popc(mine) << br_log) * C::ROW_BYTES);
+                __syncwarp();
+                const int box = lane & (per_tile - 1);
+                if ((lane >> pt_log) == i && ((mine >> box) & 1)) {
+#pragma unroll
+                  for (int pn = 0; pn < C::NPANEL; ++pn)
+                    tma_load_4d(dst + pn * C::PANEL_BYTES + (box << br_log) * C::PANEL_ROW, tm, full,
+                                pn * (C::PANEL_ROW / C::ESZ), row, s.hkv, page, pol);
+                }
+              } else if constexpr (FP8) {
+                // lane: the scales of four keys of the tile
+                const uint32_t dst = base_u32 + C::SC_OFF + 1024 * slot + 16 * lane;
+                const int src = (i << pt_log) + (lane >> (br_log - 2));
+                const int pg = __shfl_sync(0xffffffffu, page, src);
+                const int r0 = __shfl_sync(0xffffffffu, row, src) + ((4 * lane) & ((1 << br_log) - 1));
+                if ((boxes >> src) & 1) {
+                  const long long e = (static_cast<long long>(pg) * p.Hkv + s.hkv) * p.page_size + r0;
+                  cp_async16(dst, p.k_scale + e);
+                  cp_async16(dst + 512, p.v_scale + e);
+                }
+                cp_async_arrive(FULLS(slot));
+              }
+              if (++slot == stages) {
+                slot = 0;
+                par ^= 1;
+              }
+            }
+          }
+          x += s.t1 - s.t0;
+        }
+      if (dead) {
+        cp_async_wait_all();
+        if (lane == 0 && !is_s) {
+          // this warp's copies in flight: the slots issued last
+          const int n = it < stages ? it : stages;
+          for (int i = 0; i < n; ++i)
+            wait_drain_paged(is_k ? FULLK((it - 1 - i) % stages) : FULLV((it - 1 - i) % stages), ((it - 1 - i) / stages) & 1,
+                             p.spin_limit);
+        }
+      }
+    }
+  } else if (warp == 4) {
+    // ---- MMA issue ----
+    if (lane == 0) {
+      const uint64_t dq = smem_desc(sQ, 16, C::SBO, C::LAYOUT);
+      const uint64_t dk0 = smem_desc(sK, 16, C::SBO, C::LAYOUT);
+      const uint64_t dv0 = smem_desc(sV, C::PANEL_BYTES, C::SBO, C::LAYOUT);
+      bool ok = true;
+      int it = 0, seg = 0;
+      auto qk = [&](int i) -> bool {
+        const int ks = i % C::NK;
+        if (!wait_bounded(FULLK(ks), (i / C::NK) & 1, ctl, WHERE_PAGED_MMA)) return false;
+        tc_fence_after();
+        const uint64_t bk = dk0 + ((ks * C::TILE_BYTES) >> 4);
+#pragma unroll
+        for (int term = 0; term < C::NQ; ++term)
+#pragma unroll
+          for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
+            const uint32_t off = ((kk / C::STEPS_PER_PANEL) * C::PANEL_BYTES + (kk % C::STEPS_PER_PANEL) * 32) >> 4;
+            const uint64_t aq = dq + off + ((term * C::TILE_BYTES) >> 4);
+            if (FP8) mma_f8_ss(tmem + 128u * (i & 1), aq, bk + off, C::IDESC_QK, (kk > 0 || term > 0) ? 1u : 0u);
+            else     mma_f16_ss(tmem + 128u * (i & 1), aq, bk + off, C::IDESC_QK, kk > 0 ? 1u : 0u);
+          }
+        mma_commit(BAR_S(i & 1));
+        mma_commit(EMPTYK(ks));
+        return true;
+      };
+      for (int rt = rt0; ok && rt < p.row_tiles; rt += p.group_ctas)
+        for (long long x = x0; ok && x < x1; ++seg) {
+          const Segment s = find_segment(p, pre, x, x1);
+          const int n = s.t1 - s.t0;
+          if (!(ok = wait_bounded(BAR_Q, seg & 1, ctl, WHERE_PAGED_MMA))) break;
+          if (!(ok = qk(it))) break;
+          for (int j = 0; j < n; ++j, ++it) {
+            // S(it + 1) overwrites S(it - 1), which the softmax read before it handed over P(it - 1)
+            if (j + 1 < n && !(ok = qk(it + 1))) break;
+            if (!(ok = wait_bounded(BAR_P(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_MMA))) break;
+            const int vs = it % C::NV;
+            if (!(ok = wait_bounded(FULLV(vs), (it / C::NV) & 1, ctl, WHERE_PAGED_MMA))) break;
+            tc_fence_after();
+            const uint64_t bv = dv0 + ((vs * C::TILE_BYTES) >> 4);
+            const uint32_t pa = tmem + C::P_COL + 64u * (it & 1);
+#pragma unroll
+            for (int term = 0; term < C::NQ; ++term)
+#pragma unroll
+              for (int kk = 0; kk < C::KSTEPS_PV; ++kk) {
+                const uint32_t off = (kk * C::UMMA_K * C::PANEL_ROW) >> 4;
+                const uint32_t acc = (j > 0 || kk > 0 || term > 0) ? 1u : 0u;
+                if (FP8) mma_f8_ts(tmem + C::O_COL, pa + 32u * term + 8u * kk, bv + off, C::IDESC_PV, acc);
+                else     mma_f16_ts(tmem + C::O_COL, pa + 8u * kk, bv + off, C::IDESC_PV, acc);
+              }
+            mma_commit(BAR_PV);
+            mma_commit(EMPTYV(vs));
+          }
+          if (ok) mma_commit(BAR_O);
+          x += n;
+        }
+      mma_commit(BAR_DONE);
+      wait_drain_paged(BAR_DONE, 0, p.spin_limit);
+    }
+  } else {
+    // ---- softmax: thread = row of the tile ----
+    const int r = static_cast<int>(threadIdx.x);
+    const uint32_t tl = tmem + (static_cast<uint32_t>(warp) << 21);          // this warp's 32 lanes
+    Segment sg;
+    int ctx = 0, ql = 0;
+    unsigned long long bits = 0;
+    float cmul = p.c_log2;
+    bool bad = false;
+    // Lengths, mask and query row of the segment that starts at x; the row goes to shared memory.  Runs when
+    // the last segment's S = Q K^T are complete.
+    auto fetch = [&](int rt, long long x) {
+      sg = find_segment(p, pre, x, x1);
+      ctx = __ldg(p.ctx_lens + sg.b);
+      ql = p.q_lens != nullptr ? __ldg(p.q_lens + sg.b) : p.T;
+      const int pr = rt * PAGED_TREE_ROWS + r, t = token_of(p, pr);
+      const bool there = t < p.T;
+      bits = 0;
+      if (there)
+        bits = p.tree_mask != nullptr ? __ldg(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
+                                      : (t >= 63 ? ~0ull : (2ull << t) - 1);
+      if (ql < 64) bits &= (1ull << ql) - 1;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(p.q) +
+          ((static_cast<long long>(sg.b) * p.T + t) * p.Hq + sg.hkv * p.G + pr - t * p.G) * D);
+      if constexpr (!FP8) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 u = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+          st_shared_v4(sQ + (c >> 3) * C::PANEL_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4), u.x, u.y, u.z, u.w);
+        }
+      } else {
+        float m = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 u = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+        }
+        // power of two that brings the largest element into [128, 256): exact
+        int ex = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+        ex = ex < -100 ? -100 : (ex > 100 ? 100 : ex);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
+        cmul = p.c_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint4 u = there ? __ldg(src + 2 * c + y) : make_uint4(0u, 0u, 0u, 0u);
+            e4m3_terms4(__uint_as_float(u.x << 16) * up, __uint_as_float(u.x & 0xffff0000u) * up,
+                        __uint_as_float(u.y << 16) * up, __uint_as_float(u.y & 0xffff0000u) * up, hi[2 * y], lo[2 * y]);
+            e4m3_terms4(__uint_as_float(u.z << 16) * up, __uint_as_float(u.z & 0xffff0000u) * up,
+                        __uint_as_float(u.w << 16) * up, __uint_as_float(u.w & 0xffff0000u) * up, hi[2 * y + 1],
+                        lo[2 * y + 1]);
+          }
+          const uint32_t at = sQ + r * C::PANEL_ROW +
+                              ((C::PANEL_ROW == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3))) << 4);
+          st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(at + C::TILE_BYTES, lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR_Q);
+    };
+    int it = 0, seg = 0, sslot = 0;
+    uint32_t spar = 0;
+    bool first = true;
+    for (int rt = rt0; rt < p.row_tiles; rt += p.group_ctas)
+      for (long long x = x0; x < x1; ++seg) {
+        if (first) fetch(rt, x);
+        first = false;
+        const Segment dn = sg;
+        const int my_ctx = ctx, my_ql = ql, L = ctx + ql;
+        const unsigned long long my_bits = bits;
+        const float my_cmul = cmul;
+        float m_run = -INFINITY, l_run = 0.f;
+        float vref = 0.f, vup = 0.f;               // E4M3: power of two above the value scales, 2^7 / vref
+        for (int j = dn.t0; j < dn.t1; ++j, ++it) {
+          const int kb = 128 * j;
+          const bool tail = kb + 128 > my_ctx;     // drafted keys, or the end of the sequence
+          const uint32_t sb = tl + 128u * (it & 1);
+          if (!bad && !warp_wait(BAR_S(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+          if (FP8 && !bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
+          const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF + 1024 * sslot);
+          uint32_t sr[4][32];
+          if (!bad) {
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32(sb + 32u * q, sr[q]);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) reg_fence(sr[q][i]);
+          float alpha_v = 1.f;
+          bool vscale_odd = false;
+          if constexpr (FP8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 k4 = reinterpret_cast<const float4*>(sc + 32 * q)[i];
+                sr[q][4 * i] = __float_as_uint(__uint_as_float(sr[q][4 * i]) * k4.x);
+                sr[q][4 * i + 1] = __float_as_uint(__uint_as_float(sr[q][4 * i + 1]) * k4.y);
+                sr[q][4 * i + 2] = __float_as_uint(__uint_as_float(sr[q][4 * i + 2]) * k4.z);
+                sr[q][4 * i + 3] = __float_as_uint(__uint_as_float(sr[q][4 * i + 3]) * k4.w);
+              }
+            // largest finite value scale of the tile's keys
+            const float4 v4 = reinterpret_cast<const float4*>(sc + 128)[lane];
+            const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool in = kb + 4 * lane + i < L;
+              top = fmaxf(top, in && finite_f(vv[i]) ? vv[i] : 0.f);
+              vscale_odd = vscale_odd || (in && !finite_f(vv[i]));
+            }
+            vscale_odd = __any_sync(0xffffffffu, vscale_odd);
+            if (__any_sync(0xffffffffu, top > vref)) {
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const float nref = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + (top < 0x1p126f ? 0x00800000u : 0u));
+              alpha_v = vref / nref;
+              vref = nref;
+              vup = 128.f / nref;
+            }
+          }
+          if (tail) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              // 32 columns' visibility: the context, then this row's drafts (bits past q_len are clear)
+              const int rel = kb + 32 * q - my_ctx;
+              const uint32_t vis = rel >= 0    ? (rel < 64 ? static_cast<uint32_t>(my_bits >> rel) : 0u)
+                                   : rel > -32 ? (static_cast<uint32_t>(my_bits << -rel) | ((1u << -rel) - 1))
+                                               : ~0u;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((vis >> i) & 1)) sr[q][i] = __float_as_uint(-INFINITY);
+            }
+          }
+          float mt = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) mt = max3(mt, __uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
+          mt *= my_cmul;
+          bool rescale = alpha_v != 1.f;
+          float alpha = alpha_v;
+          if (mt > m_run + (FP8 ? TAU_E4M3 : TAU_BF16) || (m_run == -INFINITY && mt != -INFINITY)) {
+            const float f = m_run == -INFINITY ? 0.f : ex2(m_run - mt);
+            alpha *= f;
+            l_run *= f;
+            m_run = mt;
+            rescale = true;
+          }
+          const float off = m_run == -INFINITY ? 0.f : m_run;
+          const uint32_t pb = tl + C::P_COL + 64u * (it & 1);
+          const uint64_t cm2 = f2_pack(my_cmul, my_cmul), of2 = f2_pack(-off, -off);
+          uint64_t sum = f2_pack(0.f, 0.f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (!FP8) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float a, b;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[q][2 * i]), __uint_as_float(sr[q][2 * i + 1])), cm2, of2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum = f2_add(sum, f2_pack(a, b));
+                pk[i] = pack_bf16x2(a, b);
+              }
+              if (!bad) tmem_st16(pb + 16u * q, pk);
+            } else {
+              uint32_t hi[8], lo[8];
+              const uint64_t up2 = f2_pack(vup, vup);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + 32 * q)[i];
+                float e[4], y[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[q][4 * i + 2 * h]), __uint_as_float(sr[q][4 * i + 2 * h + 1])),
+                                   cm2, of2), e[2 * h], e[2 * h + 1]);
+                  e[2 * h] = ex2(e[2 * h]);
+                  e[2 * h + 1] = ex2(e[2 * h + 1]);
+                  const uint64_t e2 = f2_pack(e[2 * h], e[2 * h + 1]);
+                  sum = f2_add(sum, e2);
+                  f2_unpack(f2_mul(f2_mul(e2, up2), h == 0 ? f2_pack(v4.x, v4.y) : f2_pack(v4.z, v4.w)), y[2 * h], y[2 * h + 1]);
+                }
+                if (tail || vscale_odd) {          // hidden: 0 whatever the scale; seen and not finite: NaN
+                  const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                  for (int h = 0; h < 4; ++h) y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] : __int_as_float(0x7fffffff));
+                }
+                e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
+              }
+              if (!bad) {
+                tmem_st8(pb + 8u * q, hi);
+                tmem_st8(pb + 32u + 8u * q, lo);
+              }
+            }
+          }
+          {
+            float s0, s1;
+            f2_unpack(sum, s0, s1);
+            l_run += s0 + s1;
+          }
+          if (!bad && j > dn.t0 && __any_sync(0xffffffffu, rescale)) {
+            // O must hold PV(it - 1) complete; PV(it) waits for this warp's arrival below
+            if (!warp_wait(BAR_PV, (it - 1) & 1, ctl, WHERE_PAGED_USE)) {
+              bad = true;
+            } else {
+              tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tmem_ld32(tl + C::O_COL + 32u * q, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  reg_fence(o[i]);
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * (rescale ? alpha : 1.f));
+                }
+                tmem_st32(tl + C::O_COL + 32u * q, o);
+              }
+            }
+          }
+          if (tail) {
+            // thread = key row of the value tile: what must not meet a zero numerator is taken out
+            if (!bad && !warp_wait(FULLV(it % C::NV), (it / C::NV) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+            const int key = kb + r;
+            if (!bad && key >= my_ctx) {
+              uint8_t* row = base + C::V_OFF + (it % C::NV) * C::TILE_BYTES + r * C::PANEL_ROW;
+              bool clear = key >= L;
+              if (FP8 && !clear) clear = !finite_f(sc[128 + r]);
+              bool odd = false;
+#pragma unroll 1
+              for (int c = 0; c < C::ROW_BYTES / 16; ++c) {
+                uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * C::PANEL_BYTES + (((c & 7) ^ (r & 3)) << 4));
+                if (clear) {
+                  *at = make_uint4(0u, 0u, 0u, 0u);
+                } else if (!FP8) {
+                  uint4 u = *at;
+                  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+                  bool hit = false;
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    if ((w[i] & 0x7f80u) == 0x7f80u) { w[i] &= 0xffff0000u; hit = true; }
+                    if ((w[i] & 0x7f800000u) == 0x7f800000u) { w[i] &= 0xffffu; hit = true; }
+                  }
+                  if (hit) *at = u;
+                  odd = odd || hit;
+                }
+              }
+              if (odd) atomicOr(vodd_sh + (seg & 1), 1ull << (key - my_ctx));
+            }
+            fence_proxy_async_smem();
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(BAR_P(it & 1));
+            if (FP8) mbar_arrive(EMPTYS(sslot));
+          }
+          if (FP8 && ++sslot == C::NSC) {
+            sslot = 0;
+            spar ^= 1;
+          }
+        }
+        // ---- end of the segment: what the value rows held that was not finite, the next segment's queries,
+        // then the output ----
+        named_bar_sync(1, 128);
+        const unsigned long long vodd = vodd_sh[seg & 1] & my_bits;
+        if (r == 0) vodd_sh[(seg & 1) ^ 1] = 0;    // read by all before this barrier; next written after BAR_Q
+        x += dn.t1 - dn.t0;
+        {
+          const int rn = rt + p.group_ctas;
+          if (x < x1) fetch(rt, x);
+          else if (rn < p.row_tiles) fetch(rn, x0);
+        }
+        if (!bad && !warp_wait(BAR_O, seg & 1, ctl, WHERE_PAGED_USE)) bad = true;
+        if (!bad) {
+          tc_fence_after();
+          const int pr = rt * PAGED_TREE_ROWS + r, t = token_of(p, pr);
+          const bool valid = t < my_ql;
+          const bool whole = dn.t0 == 0 && dn.t1 == dn.n;
+          const long long ws_slot = 2ll * (group * static_cast<long long>(p.row_tiles) + rt) + (dn.t0 > 0 ? 0 : 1);
+          float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+          if (FP8) inv *= vref * 0x1p-7f;
+          const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
+          const long long head = static_cast<long long>(dn.hkv) * p.G + pr - t * p.G;
+          __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.o) +
+                                ((static_cast<long long>(dn.b) * p.T + t) * p.Hq + head) * D;
+          float* wrow = p.ws_o + (ws_slot * PAGED_TREE_ROWS + r) * D;
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tl + C::O_COL + 32u * q, o);
+            tmem_wait_ld();
+            float f[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              reg_fence(o[i]);
+              f[i] = __uint_as_float(o[i]) * inv;
+            }
+            if (valid && !FP8 && vodd != 0) {
+              // infinities and NaN of drafted value rows that this row sees
+              for (unsigned long long left = vodd; left != 0; left &= left - 1) {
+                const int key = my_ctx + __ffsll(left) - 1;
+                if (key < 128 * dn.t0 || key >= 128 * dn.t1) continue;
+                const int page = __ldg(p.page_table + static_cast<long long>(dn.b) * p.max_pages + key / p.page_size);
+                if (page < 0 || page >= p.n_pages) continue;
+                const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_cache) + page * p.page_stride +
+                                         dn.hkv * p.head_stride + (key % p.page_size) * p.tok_stride + 32 * q;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float e = __bfloat162float(v[i]);
+                  if (!finite_f(e)) f[i] += e;
+                }
+              }
+            }
+            if (valid && whole) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(orow + 32 * q + 8 * i) =
+                    make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                               pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+            } else if (valid) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(wrow + 32 * q + 4 * i) =
+                    make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+            }
+            __syncwarp();
+          }
+          if (!whole) p.ws_l[ws_slot * PAGED_TREE_ROWS + r] = lse2;
+          else if (valid && p.lse != nullptr) p.lse[(static_cast<long long>(dn.b) * p.Hq + head) * p.T + t] = lse2 * LN2_P;
+          tc_fence_before();                       // these reads of O before the next P's arrival
+        }
+      }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool FP8>
+cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, bool combine, cudaStream_t st) {
+  using C = TreeCfg<D, FP8>;
+  static std::atomic<unsigned long long> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if ((configured.load() & bit) == 0) {
+    e = cudaFuncSetAttribute(attn_tree_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  attn_tree_kernel<D, FP8><<<p.n_cta * p.group_ctas, TREE_THREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess || !combine) return e;
+  return launch_tree_combine(p, D, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tree(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
+                             bool combine, cudaStream_t st) {
+  if (D == 64) return fp8 ? launch_tree_d<64, true>(tk, tv, p, combine, st) : launch_tree_d<64, false>(tk, tv, p, combine, st);
+  return fp8 ? launch_tree_d<128, true>(tk, tv, p, combine, st) : launch_tree_d<128, false>(tk, tv, p, combine, st);
+}
+
+}  // namespace ea46

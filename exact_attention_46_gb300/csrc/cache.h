@@ -84,13 +84,16 @@ struct PagedParams {
   const unsigned long long* tree_mask;              // [B, T] or nullptr: chain
   const float* k_scale; // E4M3: [n_pages, Hkv, page_size]
   const float* v_scale;
+  const void* v_cache;  // bf16: read element by element for drafted rows that are not finite
+  long long page_stride, head_stride, tok_stride;   // elements
   float* ws_o;          // [slots][RB][D] partial outputs
   float* ws_l;          // [slots][RB] partial lse, log2 units
   int B, T, Hq, Hkv, G;
   uint32_t g_magic;     // ceil(2^32 / G), 0 for G = 1
   int n_pages, page_size, max_pages;
   int row_tiles;        // ceil(G * T / RB)
-  int n_cta;            // CTAs of the key kernel
+  int n_cta;            // groups of CTAs that share the key tiles out; a group has one CTA per row tile,
+  int group_ctas;       // at most group_ctas
   float c_log2;         // softmax scale * log2(e)
   long long spin_limit;
   int* err_word;
@@ -101,12 +104,17 @@ constexpr int PAGED_MAX_BATCH = 1024;
 constexpr int PAGED_MAX_DRAFT = 64;
 
 // Query rows per work unit for R = G * T packed rows.
-constexpr int paged_rows(int R) { return R <= 8 ? 8 : (R <= 16 ? 16 : 32); }
+constexpr int PAGED_TREE_ROWS = 128;
+constexpr int paged_rows(int R) { return R <= 8 ? 8 : (R <= 16 ? 16 : (R <= 32 ? 32 : PAGED_TREE_ROWS)); }
 
 // tk, tv: the cache as (D, page_size, Hkv, n_pages) with a box of one swizzle panel x
 // min(page_size, 128) rows.
 cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
                               bool combine, cudaStream_t st);
+
+cudaError_t launch_attn_tree(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
+                             bool combine, cudaStream_t st);
+cudaError_t launch_tree_combine(const PagedParams& p, int D, cudaStream_t st);
 
 // Shared pieces of the C-ABI layer (api.cu).
 int api_fail(int code, const char* fmt, ...);

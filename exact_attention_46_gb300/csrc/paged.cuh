@@ -1,0 +1,114 @@
+// paged.cuh -- what the kernels of attention over a paged cache share: the list of key tiles and how
+// it is cut over the CTAs, and the asynchronous copies outside TMA.
+//
+// A unit is (sequence, key/value head); its keys are cut into 128-key tiles.  The tiles of all units, in
+// the order sequence, key/value head, key, form one list of W; group i of N takes [i W / N,
+// (i + 1) W / N).  A group is one CTA, or one per tile of packed query rows where there are several:
+// its CTAs go through the same keys at the same time, so all but the first find them in L2.
+// Everything is computed from the lengths on the device.
+#pragma once
+
+#include <cstdint>
+
+#include "cache.h"
+#include "ptx.cuh"
+
+namespace ea46 {
+
+constexpr float LN2_P = 0.69314718055994530942f;
+enum : int { WHERE_PAGED_LOAD = 51, WHERE_PAGED_USE = 52, WHERE_PAGED_LENS = 53, WHERE_PAGED_PAGE = 54,
+             WHERE_PAGED_MMA = 55 };
+
+// 16-byte asynchronous copy global -> shared, and an arrival on `bar` when this thread's copies so
+// far have landed (counted in the barrier's initial count).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void wait_drain_paged(uint32_t bar, uint32_t parity, long long limit) {
+  if (mbar_try_wait(bar, parity)) return;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > limit) return;
+}
+
+// Prefix sums of the sequences' key tiles into pre[0 .. B]; returns 0 if any length is out of
+// range.  Called by all `n` threads (n >= 32 a multiple of 32, n <= 1024).
+__device__ __forceinline__ bool tile_prefix(const PagedParams& p, int* pre, int* scratch, int n) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + n - 1) / n, b0 = tid * per, b1 = min(p.B, b0 + per);
+  bool ok = true;
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int ctx = __ldg(p.ctx_lens + b), ql = p.q_lens != nullptr ? __ldg(p.q_lens + b) : p.T;
+    const bool fine = ctx >= 0 && ql >= 0 && ql <= p.T &&
+                      static_cast<long long>(ctx) + ql <= static_cast<long long>(p.max_pages) * p.page_size;
+    ok = ok && fine;
+    const int tiles = fine && ql > 0 ? (ctx + ql + 127) >> 7 : 0;
+    pre[b + 1] = tiles;                       // own entries only, until the scan below
+    sum += tiles;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  ok = __syncthreads_and(ok);
+  int off = incl - sum;
+  for (int w = 0; w < warp; ++w) off += scratch[w];
+  for (int b = b0; b < b1; ++b) {
+    off += pre[b + 1];
+    pre[b + 1] = off;
+  }
+  if (tid == 0) pre[0] = 0;
+  __syncthreads();
+  return ok;
+}
+
+// The piece of the tile list that starts at x and ends at x1 or with its unit.
+struct Segment {
+  int b, hkv;           // sequence, key/value head
+  int t0, t1, n;        // tiles [t0, t1) of the unit's n
+};
+
+// x / y for y > 0, in 32 bits where both fit (the 64-bit division is a few hundred cycles).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
+// Token of packed row r: r / G by multiplication (r, G < 2^16).
+__device__ __forceinline__ int token_of(const PagedParams& p, int r) {
+  return p.g_magic == 0 ? r : static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.g_magic));
+}
+
+__device__ __forceinline__ Segment find_segment(const PagedParams& p, const int* pre, long long x, long long x1) {
+  const long long hr = p.Hkv;
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] * hr <= x) lo = mid; else hi = mid;
+  }
+  // x lies in sequence lo: empty ones before it have pre[lo + 1] == pre[lo]
+  Segment s;
+  s.b = lo;
+  s.n = pre[lo + 1] - pre[lo];
+  const long long y = x - pre[lo] * hr;
+  s.hkv = static_cast<int>(quotient(y, s.n));
+  s.t0 = static_cast<int>(y - static_cast<long long>(s.hkv) * s.n);
+  const long long left = x1 - x;
+  s.t1 = left < s.n - s.t0 ? s.t0 + static_cast<int>(left) : s.n;
+  return s;
+}
+
+__device__ __forceinline__ long long cta_start(long long i, long long W, long long N) { return quotient(i * W, N); }
+
+}  // namespace ea46

@@ -10,6 +10,16 @@ roundings: with X = max_j scale sum_d |q_d k_jd| over the seen keys and A = sum_
 * the output rounds to bf16: 2^-8 of it.
 So |err| <= 2^-8 |o| + (r + 2 dx + 2^-18) A (+ L 2^-26 448 max scale), r = 2^-8 or 2^-11, and
 |lse err| <= dx + 2^-18 (1 + |lse|).
+Over an E4M3 cache with more than 32 rows (group x drafts) the products run on E4M3 terms:
+* a query row, scaled so that its largest element lies in [128, 256), is the sum of two terms.  An
+  element of eight significant bits leaves a remainder of four after the first term, which the
+  second holds exactly unless it lies below E4M3's smallest step 2^-9: that is off by at most half
+  a step, 2^-10, so by 2^-17 of the row's largest element (and only in elements below 2^-9 of
+  it).  A logit moves by at most 2^-17 scale max|q| sum_d |k_jd| more;
+* a numerator times its value's scale over 2^-7 vref (vref a power of two, at most twice the largest
+  scale) is rounded to fp16 (2^-11) and to two terms: 2^-4 * 2^-4 = 2^-8 of it, or half a step, 2^-10,
+  where that is more: 2^-17 vref of the value's code, per key, over a sum of at least 1.  So
+  r = 2^-8 + 2^-11 and the last term becomes 2^-16 max scale sum_j |code_jd|.
 What no row may see -- free rows of used pages, free pages, entries behind the page table's end -- holds
 NaN.
 """
@@ -93,7 +103,8 @@ class Problem:
     def check(self, o, lse, scale=None):
         scale = 1 / np.sqrt(self.D) if scale is None else scale
         o, lse = to64(o), to64(lse)
-        r = 2.0 ** -11 if self.fp8 else 2.0 ** -8
+        terms = self.fp8 and self.T * self.Hq // self.Hkv > 32
+        r = 2.0 ** -8 + 2.0 ** -11 if terms else (2.0 ** -11 if self.fp8 else 2.0 ** -8)
         for b in range(self.B):
             n = self.ql[b]
             if n == 0:
@@ -102,6 +113,8 @@ class Problem:
             ref, ref_lse, A, X = paged.tree_attention(to64(self.q[b, :n]), k, v, self.ctx[b],
                                                       None if self.mask is None else self.mask[b], scale)
             dx = (self.D + 16) * 2.0 ** -24 * X
+            if terms:
+                dx = dx + 2.0 ** -17 * scale * np.abs(to64(self.q[b, :n])).max(-1).T * np.abs(k).sum(-1).max()
             empty = np.isneginf(ref_lse)
             assert np.array_equal(np.isneginf(lse[b, :, :n]), empty)
             gap = np.abs(np.where(empty, 0, lse[b, :, :n]) - np.where(empty, 0, ref_lse))
@@ -111,6 +124,9 @@ class Problem:
                 j = np.arange(self.L[b])
                 s = self.scale[1].cpu().numpy().transpose(0, 2, 1)[self.table[b, j // self.page], j % self.page]
                 floor = self.L[b] * 2.0 ** -26 * 448 * float(s.max())
+                if terms:
+                    codes = np.abs(v / s.astype(np.float64)[..., None]).sum(0)              # [Hkv, D]
+                    floor = floor + 2.0 ** -16 * float(s.max()) * np.repeat(codes, self.Hq // self.Hkv, 0)[None]
             tol = 2.0 ** -8 * np.abs(ref) + (r + 2 * dx.T[..., None] + 2.0 ** -18) * A + floor
             err = np.abs(o[b, :n] - ref)
             assert np.all(err <= tol), (b, float((err - tol).max()))
