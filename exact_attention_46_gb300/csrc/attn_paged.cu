@@ -771,9 +771,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 }
 
 // Merge of the units that several groups share.  A block looks at the start of group i + 1's tiles: where
-// that is the first cut inside a unit, it merges one row tile of the unit -- N - 1 blocks a row tile,
-// whatever the batch.
-// Its warps take the rows; with fewer rows than warps several warps share a row's parts.
+// that is the first cut inside a unit, it merges eight rows of one row tile of the unit, a warp each --
+// (N - 1) RB / 8 blocks a row tile, whatever the batch.  With fewer rows than warps several warps share
+// a row's parts.
 template <int D, int RB>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p) {
   constexpr int NW = 8, E = D / 32;
@@ -800,12 +800,13 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
   grid_dependency_wait();       // in every block: this grid's end stands for the key kernel's too
   if (!mine) return;
   const int c0 = static_cast<int>(i - 1), n = static_cast<int>(c1) - c0 + 1;      // parts: groups c0 .. c1
-  const int left = ql * p.G - rt * RB, rows = left < RB ? left : RB;
-  const int share_log = rows >= 8 ? 0 : (rows > 4 ? 0 : (rows > 2 ? 1 : (rows > 1 ? 2 : 3)));   // warps of a row
+  const int first = 8 * blockIdx.y, left = ql * p.G - rt * RB - first, rows = left < NW ? left : NW;
+  if (rows <= 0) return;
+  const int share_log = rows > 4 ? 0 : (rows > 2 ? 1 : (rows > 1 ? 2 : 3));        // warps of a row
   const int share = 1 << share_log;
-  for (int r0 = 0; r0 < rows; r0 += NW >> share_log) {
-    const int r = r0 + (warp >> share_log), sub = warp & (share - 1);
-    const bool live = r < rows;
+  {
+    const int r = first + (warp >> share_log), sub = warp & (share - 1);
+    const bool live = r - first < rows;
     float mx = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -876,7 +877,7 @@ template <int D, int RB>
 cudaError_t launch_paged_combine(const PagedParams& p, cudaStream_t st) {
   if (p.n_cta < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_cta - 1) * p.row_tiles);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_cta - 1) * p.row_tiles, RB / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];

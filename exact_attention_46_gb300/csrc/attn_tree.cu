@@ -49,6 +49,7 @@ struct TreeCfg {
   // K and V tiles in flight
   static constexpr int NK = TILE_BYTES == 32768 ? 3 : (TILE_BYTES == 16384 ? 5 : 8);
   static constexpr int NV = TILE_BYTES == 32768 ? 2 : (TILE_BYTES == 16384 ? 5 : 8);
+  static constexpr int CH = FP8 ? 32 : 64;                    // columns of S a softmax thread holds at once
   static constexpr int NSC = FP8 ? 4 : 0;                     // stages of 128 key and 128 value scales
   static constexpr uint32_t SBO = 8 * PANEL_ROW;
   static constexpr uint32_t LAYOUT = PANEL_ROW == 128 ? 2u : 4u;
@@ -403,30 +404,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
           if (!bad && !warp_wait(BAR_S(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
           if (FP8 && !bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
           const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF + 1024 * sslot);
-          uint32_t sr[4][32];
-          if (!bad) {
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(sb + 32u * q, sr[q]);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) reg_fence(sr[q][i]);
+          if (!bad) tc_fence_after();
           float alpha_v = 1.f;
           bool vscale_odd = false;
           if constexpr (FP8) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 k4 = reinterpret_cast<const float4*>(sc + 32 * q)[i];
-                sr[q][4 * i] = __float_as_uint(__uint_as_float(sr[q][4 * i]) * k4.x);
-                sr[q][4 * i + 1] = __float_as_uint(__uint_as_float(sr[q][4 * i + 1]) * k4.y);
-                sr[q][4 * i + 2] = __float_as_uint(__uint_as_float(sr[q][4 * i + 2]) * k4.z);
-                sr[q][4 * i + 3] = __float_as_uint(__uint_as_float(sr[q][4 * i + 3]) * k4.w);
-              }
             // largest finite value scale of the tile's keys
             const float4 v4 = reinterpret_cast<const float4*>(sc + 128)[lane];
             const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
@@ -447,24 +428,56 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
               vup = 128.f / nref;
             }
           }
-          if (tail) {
+          // CH columns of S, scaled by the keys' scales, hidden ones -inf
+          auto load_s = [&](int c0, uint32_t (&s)[C::CH / 32][32]) {
+            if (!bad) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              // 32 columns' visibility: the context, then this row's drafts (bits past q_len are clear)
-              const int rel = kb + 32 * q - my_ctx;
-              const uint32_t vis = rel >= 0    ? (rel < 64 ? static_cast<uint32_t>(my_bits >> rel) : 0u)
-                                   : rel > -32 ? (static_cast<uint32_t>(my_bits << -rel) | ((1u << -rel) - 1))
-                                               : ~0u;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((vis >> i) & 1)) sr[q][i] = __float_as_uint(-INFINITY);
+              for (int q = 0; q < C::CH / 32; ++q) tmem_ld32(sb + c0 + 32u * q, s[q]);
+              tmem_wait_ld();
             }
-          }
+#pragma unroll
+            for (int q = 0; q < C::CH / 32; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) reg_fence(s[q][i]);
+            if constexpr (FP8) {
+#pragma unroll
+              for (int q = 0; q < C::CH / 32; ++q)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 k4 = reinterpret_cast<const float4*>(sc + c0 + 32 * q)[i];
+                  float y[4];
+                  f2_unpack(f2_mul(f2_pack(__uint_as_float(s[q][4 * i]), __uint_as_float(s[q][4 * i + 1])),
+                                   f2_pack(k4.x, k4.y)), y[0], y[1]);
+                  f2_unpack(f2_mul(f2_pack(__uint_as_float(s[q][4 * i + 2]), __uint_as_float(s[q][4 * i + 3])),
+                                   f2_pack(k4.z, k4.w)), y[2], y[3]);
+#pragma unroll
+                  for (int h = 0; h < 4; ++h) s[q][4 * i + h] = __float_as_uint(y[h]);
+                }
+            }
+            if (tail) {
+#pragma unroll
+              for (int q = 0; q < C::CH / 32; ++q) {
+                // 32 columns' visibility: the context, then this row's drafts (bits past q_len are clear)
+                const int rel = kb + c0 + 32 * q - my_ctx;
+                const uint32_t vis = rel >= 0    ? (rel < 64 ? static_cast<uint32_t>(my_bits >> rel) : 0u)
+                                     : rel > -32 ? (static_cast<uint32_t>(my_bits << -rel) | ((1u << -rel) - 1))
+                                                 : ~0u;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!((vis >> i) & 1)) s[q][i] = __float_as_uint(-INFINITY);
+              }
+            }
+          };
           float mt = -INFINITY;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += C::CH) {
+            uint32_t s[C::CH / 32][32];
+            load_s(c0, s);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < C::CH / 32; ++q)
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) mt = max3(mt, __uint_as_float(sr[q][i]), __uint_as_float(sr[q][i + 1]));
+              for (int i = 0; i < 32; i += 2) mt = max3(mt, __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
+          }
           mt *= my_cmul;
           bool rescale = alpha_v != 1.f;
           float alpha = alpha_v;
@@ -479,47 +492,53 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
           const uint32_t pb = tl + C::P_COL + 64u * (it & 1);
           const uint64_t cm2 = f2_pack(my_cmul, my_cmul), of2 = f2_pack(-off, -off);
           uint64_t sum = f2_pack(0.f, 0.f);
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += C::CH) {
+            uint32_t s[C::CH / 32][32];
+            load_s(c0, s);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (!FP8) {
-              uint32_t pk[16];
+            for (int q = 0; q < C::CH / 32; ++q) {
+              if constexpr (!FP8) {
+                uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float a, b;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[q][2 * i]), __uint_as_float(sr[q][2 * i + 1])), cm2, of2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-                sum = f2_add(sum, f2_pack(a, b));
-                pk[i] = pack_bf16x2(a, b);
-              }
-              if (!bad) tmem_st16(pb + 16u * q, pk);
-            } else {
-              uint32_t hi[8], lo[8];
-              const uint64_t up2 = f2_pack(vup, vup);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + 32 * q)[i];
-                float e[4], y[4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[q][4 * i + 2 * h]), __uint_as_float(sr[q][4 * i + 2 * h + 1])),
-                                   cm2, of2), e[2 * h], e[2 * h + 1]);
-                  e[2 * h] = ex2(e[2 * h]);
-                  e[2 * h + 1] = ex2(e[2 * h + 1]);
-                  const uint64_t e2 = f2_pack(e[2 * h], e[2 * h + 1]);
-                  sum = f2_add(sum, e2);
-                  f2_unpack(f2_mul(f2_mul(e2, up2), h == 0 ? f2_pack(v4.x, v4.y) : f2_pack(v4.z, v4.w)), y[2 * h], y[2 * h + 1]);
+                for (int i = 0; i < 16; ++i) {
+                  float a, b;
+                  f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), cm2, of2), a, b);
+                  a = ex2(a);
+                  b = ex2(b);
+                  sum = f2_add(sum, f2_pack(a, b));
+                  pk[i] = pack_bf16x2(a, b);
                 }
-                if (tail || vscale_odd) {          // hidden: 0 whatever the scale; seen and not finite: NaN
-                  const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+                if (!bad) tmem_st16(pb + c0 / 2 + 16u * q, pk);
+              } else {
+                uint32_t hi[8], lo[8];
+                const uint64_t up2 = f2_pack(vup, vup);
 #pragma unroll
-                  for (int h = 0; h < 4; ++h) y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] : __int_as_float(0x7fffffff));
+                for (int i = 0; i < 8; ++i) {
+                  const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + c0 + 32 * q)[i];
+                  float e[4], y[4];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][4 * i + 2 * h]), __uint_as_float(s[q][4 * i + 2 * h + 1])),
+                                     cm2, of2), e[2 * h], e[2 * h + 1]);
+                    e[2 * h] = ex2(e[2 * h]);
+                    e[2 * h + 1] = ex2(e[2 * h + 1]);
+                    const uint64_t e2 = f2_pack(e[2 * h], e[2 * h + 1]);
+                    sum = f2_add(sum, e2);
+                    f2_unpack(f2_mul(f2_mul(e2, up2), h == 0 ? f2_pack(v4.x, v4.y) : f2_pack(v4.z, v4.w)), y[2 * h],
+                              y[2 * h + 1]);
+                  }
+                  if (tail || vscale_odd) {        // hidden: 0 whatever the scale; seen and not finite: NaN
+                    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] : __int_as_float(0x7fffffff));
+                  }
+                  e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
                 }
-                e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
-              }
-              if (!bad) {
-                tmem_st8(pb + 8u * q, hi);
-                tmem_st8(pb + 32u + 8u * q, lo);
+                if (!bad) {
+                  tmem_st8(pb + c0 / 4 + 8u * q, hi);
+                  tmem_st8(pb + 32u + c0 / 4 + 8u * q, lo);
+                }
               }
             }
           }
