@@ -175,9 +175,10 @@ int paged_ctas() {
 // A unit can be shared by CTAs only if some sequence can have more than one 128-key tile.
 bool paged_combines(int page_size, int max_pages) { return static_cast<long long>(page_size) * max_pages > 128; }
 
-// Two partial units a CTA (the one it starts in and the one it ends in): RB rows of D + 1 floats.  Where
+// Two partial units a CTA (the one it starts in and the one it ends in): RB rows of D + 1 floats; and a
+// CTA's cut (16 bytes).  Where
 // there are more row tiles than CTAs there is one group and nothing is cut.
-size_t paged_workspace(int n_cta, int RB, int D) { return 8ull * n_cta * RB * (static_cast<size_t>(D) + 1); }
+size_t paged_workspace(int n_cta, int RB, int D) { return 8ull * n_cta * RB * (static_cast<size_t>(D) + 1) + 16ull * n_cta; }
 
 }  // namespace
 
@@ -374,6 +375,7 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
   p.group_ctas = group;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_l = need > 0 ? p.ws_o + 2ll * sms * RB * D : nullptr;
+  p.cuts = need > 0 ? reinterpret_cast<int4*>(p.ws_l + 2ll * sms * RB) : nullptr;
   const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(static_cast<float>(D));
   p.c_log2 = sc * 1.4426950408889634f;
   p.spin_limit = api_spin_limit();

@@ -169,11 +169,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   grid_launch_dependents();
   if (!tile_prefix(p, pre, scratch, NTHREADS)) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_LENS);
+    if (threadIdx.x == 0) write_cut(p, pre, blockIdx.x, 0, 0);
     return;
   }
   const long long W = static_cast<long long>(pre[p.B]) * p.Hkv;
   const long long N = W < p.n_cta ? W : p.n_cta;
-  if (static_cast<long long>(blockIdx.x) >= N) return;
+  if (static_cast<long long>(blockIdx.x) >= N) {
+    if (threadIdx.x == 0) write_cut(p, pre, blockIdx.x, W, N);
+    return;
+  }
   const long long x0 = cta_start(blockIdx.x, W, N), x1 = cta_start(blockIdx.x + 1ll, W, N);
   const WaitCtl ctl{p.spin_limit, abort_flag, p.err_word, p.err_info};
 
@@ -241,6 +245,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       x += s.t1 - s.t0;
     }
+    if (pw == 0 && lane == 0) write_cut(p, pre, blockIdx.x, W, N);   // the loads are all on their way
     if (dead) {
       cp_async_wait_all();
       if (lane == 0)
@@ -770,42 +775,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-// Merge of the units that several groups share.  A block looks at the start of group i + 1's tiles: where
-// that is the first cut inside a unit, it merges eight rows of one row tile of the unit, a warp each --
-// (N - 1) RB / 8 blocks a row tile, whatever the batch.  With fewer rows than warps several warps share
-// a row's parts.
+// Rows of a merge block.  Few rows a unit: the parts of a row are read by several warps at once.
+template <int RB>
+constexpr int COMBINE_ROWS = RB == PAGED_TREE_ROWS ? 8 : RB / 8;
+
+// Merge of the units that several groups share.  A block takes ROWS rows of one row tile of the unit that
+// group i + 1's start cuts first, if it cuts one; eight warps, 8 / ROWS for the parts of a row.
 template <int D, int RB>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p) {
-  constexpr int NW = 8, E = D / 32;
-  __shared__ int pre[PAGED_MAX_BATCH + 1];
-  __shared__ int scratch[NW];
+  constexpr int NW = 8, E = D / 32, ROWS = COMBINE_ROWS<RB>, share = NW / ROWS;
   __shared__ float part[NW][D + 2];
-  const bool ok = tile_prefix(p, pre, scratch, 32 * NW);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long W = ok ? static_cast<long long>(pre[p.B]) * p.Hkv : 0, N = W < p.n_cta ? W : p.n_cta;
-  const long long i = blockIdx.x / p.row_tiles + 1ll;
-  const int rt = static_cast<int>(blockIdx.x % p.row_tiles);
-  bool mine = i < N;
-  Segment s{};
-  long long c1 = 0;
-  int ql = 0;
-  if (mine) {
-    const long long x = cta_start(i, W, N);
-    s = find_segment(p, pre, x, W);
-    // the group that holds list position y is the last c with c W / N <= y
-    mine = s.t0 > 0 && quotient((x - s.t0 + 1) * N - 1, W) == i - 1;
-    c1 = quotient((x - s.t0 + s.n) * N - 1, W);
-    ql = p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T;
-  }
+  const int c0 = static_cast<int>(blockIdx.x / p.row_tiles), rt = static_cast<int>(blockIdx.x % p.row_tiles);
   grid_dependency_wait();       // in every block: this grid's end stands for the key kernel's too
-  if (!mine) return;
-  const int c0 = static_cast<int>(i - 1), n = static_cast<int>(c1) - c0 + 1;      // parts: groups c0 .. c1
-  const int first = 8 * blockIdx.y, left = ql * p.G - rt * RB - first, rows = left < NW ? left : NW;
-  if (rows <= 0) return;
-  const int share_log = rows > 4 ? 0 : (rows > 2 ? 1 : (rows > 1 ? 2 : 3));        // warps of a row
-  const int share = 1 << share_log;
+  const int4 cut = __ldcg(p.cuts + c0 + 1);
+  const int n = cut.x;                                          // parts: groups c0 .. c0 + n - 1
+  const int first = ROWS * blockIdx.y, rows = cut.w * p.G - rt * RB - first;
+  if (n == 0 || rows <= 0) return;
   {
-    const int r = first + (warp >> share_log), sub = warp & (share - 1);
+    const int r = first + warp / share, sub = warp % share;
     const bool live = r - first < rows;
     float mx = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
@@ -862,12 +850,12 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
     if (live && sub == 0) {
       const int pr = rt * RB + r, t = token_of(p, pr);
       const float inv = sum == 0.f ? 1.f : 1.f / sum;          // no key at all: the parts' zeros
-      const long long h = static_cast<long long>(s.hkv) * p.G + pr - t * p.G;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<long long>(s.b) * p.T + t) * p.Hq + h) * D + lane * E;
+      const long long h = static_cast<long long>(cut.z) * p.G + pr - t * p.G;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<long long>(cut.y) * p.T + t) * p.Hq + h) * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
       if (lane == 0 && p.lse != nullptr)
-        p.lse[(static_cast<long long>(s.b) * p.Hq + h) * p.T + t] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * LN2_P;
+        p.lse[(static_cast<long long>(cut.y) * p.Hq + h) * p.T + t] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * LN2_P;
     }
   }
 }
@@ -877,7 +865,7 @@ template <int D, int RB>
 cudaError_t launch_paged_combine(const PagedParams& p, cudaStream_t st) {
   if (p.n_cta < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_cta - 1) * p.row_tiles, RB / 8);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_cta - 1) * p.row_tiles, RB / COMBINE_ROWS<RB>);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];

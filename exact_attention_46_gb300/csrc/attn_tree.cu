@@ -3,13 +3,15 @@
 // computes, the readings and the list of key tiles are attn_paged.cu's and paged.cuh's.
 //
 // With 33 or more rows the 128-row tile of tcgen05 is used well: S = Q K^T and O += P V run on it with
-// S, P and O in Tensor Memory, one softmax thread per row.  128 rows take about 1100 cycles of the
+// S, P and O in Tensor Memory.  128 rows take about 1100 cycles of the
 // tensor pipe and about as many of the exp2 units per 128-key tile of D = 128 in bf16, against the 2800
 // the tile takes from HBM at an SM's share of it, so one row tile is bound by HBM and several by
 // compute; the CTAs of a group take one row tile each and the same keys, which all but the first find
 // in L2.
-//   * warps 0..3 softmax (thread = row), 4 issues the MMAs, 5 and 6 load K and V tiles by TMA (one box
-//     per page and swizzle panel) through a ring each, 7 the E4M3 scales;
+//   * warps 0..7 softmax (thread = row and half of the tile's keys; the two warps of a quarter of Tensor
+//     Memory exchange their maxima, and hide each other's latencies), 8 issues the MMAs, 9 and 10
+//     load K and V tiles by TMA (one box per page and swizzle panel) through a ring each, 11 the
+//     E4M3 scales;
 //   * S and P are double-buffered: S(i + 1) is issued before PV(i).  The running maximum is lazy (O is
 //     rescaled in Tensor Memory only when a maximum moves by more than 2^TAU);
 //   * the next unit's queries are written to shared memory before the last unit's epilogue, so its
@@ -49,7 +51,6 @@ struct TreeCfg {
   // K and V tiles in flight
   static constexpr int NK = TILE_BYTES == 32768 ? 3 : (TILE_BYTES == 16384 ? 5 : 8);
   static constexpr int NV = TILE_BYTES == 32768 ? 2 : (TILE_BYTES == 16384 ? 5 : 8);
-  static constexpr int CH = FP8 ? 32 : 64;                    // columns of S a softmax thread holds at once
   static constexpr int NSC = FP8 ? 4 : 0;                     // stages of 128 key and 128 value scales
   static constexpr uint32_t SBO = 8 * PANEL_ROW;
   static constexpr uint32_t LAYOUT = PANEL_ROW == 128 ? 2u : 4u;
@@ -66,8 +67,9 @@ struct TreeCfg {
   static constexpr int K_OFF = NQ * TILE_BYTES, V_OFF = K_OFF + NK * TILE_BYTES;
   static constexpr int SC_OFF = V_OFF + NV * TILE_BYTES;
   static constexpr int PRE_OFF = SC_OFF + NSC * 1024;
-  static constexpr int FLAG_OFF = PRE_OFF + (PAGED_MAX_BATCH + 2) * 4;      // vodd [2] x 8, scratch, abort, tmem
-  static constexpr int BAR_OFF = FLAG_OFF + 64;
+  static constexpr int RED_OFF = PRE_OFF + (PAGED_MAX_BATCH + 2) * 4;       // [3][2][128] floats: maxima (twice), sums
+  static constexpr int FLAG_OFF = RED_OFF + 3 * 2 * 128 * 4;                // vodd [2] x 8, tmem, abort, scratch
+  static constexpr int BAR_OFF = FLAG_OFF + 96;
   static constexpr int NBAR = 8 + 2 * (NK + NV + NSC);
   static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NBAR * 8;
   static_assert(FLAG_OFF % 8 == 0 && BAR_OFF % 8 == 0, "alignment");
@@ -75,7 +77,8 @@ struct TreeCfg {
   static_assert(P_COL + 128 <= 512, "Tensor Memory budget");
 };
 
-constexpr int TREE_THREADS = 256;
+constexpr int TREE_THREADS = 384;
+constexpr int MMA_WARP = 8, K_WARP = 9, S_WARP = 11;
 // Lazy rescale threshold (log2).  Numerators reach 2^TAU; E4M3's two terms then span [2^-10, 2^8] around
 // numerators scaled by 2^7.
 constexpr float TAU_BF16 = 8.0f, TAU_E4M3 = 1.0f;
@@ -121,7 +124,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
   unsigned long long* vodd_sh = reinterpret_cast<unsigned long long*>(base + C::FLAG_OFF);   // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::FLAG_OFF + 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::FLAG_OFF + 20);
-  int* scratch = reinterpret_cast<int*>(base + C::FLAG_OFF + 24);                            // [8]
+  int* scratch = reinterpret_cast<int*>(base + C::FLAG_OFF + 24);                            // [12]
+  float* red = reinterpret_cast<float*>(base + C::RED_OFF);                                  // [3][2][128]
   const uint32_t bar0 = base_u32 + C::BAR_OFF;
   const uint32_t BAR_Q = bar0, BAR_O = bar0 + 8, BAR_DONE = bar0 + 16, BAR_PV = bar0 + 24;
   auto BAR_S = [&](int b) { return bar0 + 32 + 8u * b; };
@@ -135,13 +139,13 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 
   const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
   if (threadIdx.x == 0) {
-    mbar_init(BAR_Q, 4);
+    mbar_init(BAR_Q, 8);
     mbar_init(BAR_O, 1);
     mbar_init(BAR_DONE, 1);
     mbar_init(BAR_PV, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(BAR_S(b), 1);
-      mbar_init(BAR_P(b), 4);
+      mbar_init(BAR_P(b), 8);
     }
     for (int s = 0; s < C::NK; ++s) {
       mbar_init(FULLK(s), 1);
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     }
     for (int s = 0; s < C::NSC; ++s) {
       mbar_init(FULLS(s), 32);
-      mbar_init(EMPTYS(s), 4);
+      mbar_init(EMPTYS(s), 8);
     }
     *abort_flag = 0;
     vodd_sh[0] = vodd_sh[1] = 0;
@@ -163,25 +167,29 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
   const bool fine = tile_prefix(p, pre, scratch, TREE_THREADS);
   if (!fine) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_LENS);
+    if (threadIdx.x == 0 && blockIdx.x % p.group_ctas == 0) write_cut(p, pre, blockIdx.x / p.group_ctas, 0, 0);
     return;
   }
   const long long W = static_cast<long long>(pre[p.B]) * p.Hkv;
   const long long N = W < p.n_cta ? W : p.n_cta;
   const int group = blockIdx.x / p.group_ctas, rt0 = blockIdx.x % p.group_ctas;
-  if (group >= N) return;
+  if (group >= N) {
+    if (threadIdx.x == 0 && rt0 == 0) write_cut(p, pre, group, W, N);
+    return;
+  }
   const long long x0 = cta_start(group, W, N), x1 = cta_start(group + 1ll, W, N);
-  if (warp == 4) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{p.spin_limit, abort_flag, p.err_word, p.err_info};
 
-  if (warp >= 5) {
-    // ---- loads: K (warp 5), V (6), E4M3 scales (7).  Box i of a segment's list of boxes is br rows of
+  if (warp >= K_WARP) {
+    // ---- loads: K, V, E4M3 scales, a warp each.  Box i of a segment's list of boxes is br rows of
     // one page; lane i % 32 looks its page up, one batch of 32 boxes ahead, and issues its copies ----
-    if (FP8 || warp < 7) {
-      const bool is_k = warp == 5, is_s = warp == 7;
+    if (FP8 || warp < S_WARP) {
+      const bool is_k = warp == K_WARP, is_s = warp == S_WARP;
       const CUtensorMap* tm = is_k ? &tmK : &tmV;
       const int ps_log = 31 - __clz(p.page_size), br_log = ps_log < 7 ? ps_log : 7;
       const int pt_log = 7 - br_log, per_tile = 1 << pt_log, batch = 32 >> pt_log;
@@ -246,6 +254,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
           }
           x += s.t1 - s.t0;
         }
+      if (is_k && rt0 == 0 && lane == 0) write_cut(p, pre, group, W, N);
       if (dead) {
         cp_async_wait_all();
         if (lane == 0 && !is_s) {
@@ -257,7 +266,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         }
       }
     }
-  } else if (warp == 4) {
+  } else if (warp == MMA_WARP) {
     // ---- MMA issue ----
     if (lane == 0) {
       const uint64_t dq = smem_desc(sQ, 16, C::SBO, C::LAYOUT);
@@ -317,14 +326,16 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
       wait_drain_paged(BAR_DONE, 0, p.spin_limit);
     }
   } else {
-    // ---- softmax: thread = row of the tile ----
-    const int r = static_cast<int>(threadIdx.x);
-    const uint32_t tl = tmem + (static_cast<uint32_t>(warp) << 21);          // this warp's 32 lanes
+    // ---- softmax: warps w and w + 4 share the rows of Tensor Memory's quarter w & 3 (its own SM
+    // sub-partition); thread = row r, half hf of the tile's keys, of the head and of the output ----
+    const int r = 32 * (warp & 3) + lane, hf = warp >> 2;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(warp & 3) << 21);      // this warp's 32 lanes
+    const uint32_t pair_bar = 2u + (warp & 3);
     Segment sg;
     int ctx = 0, ql = 0;
     unsigned long long bits = 0;
     float cmul = p.c_log2;
-    bool bad = false;
+    bool bad = false;                              // a wait of this warp gave up; it still meets the barriers
     // Lengths, mask and query row of the segment that starts at x; the row goes to shared memory.  Runs when
     // the last segment's S = Q K^T are complete.
     auto fetch = [&](int rt, long long x) {
@@ -343,7 +354,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
           ((static_cast<long long>(sg.b) * p.T + t) * p.Hq + sg.hkv * p.G + pr - t * p.G) * D);
       if constexpr (!FP8) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int i = 0; i < D / 16; ++i) {
+          const int c = hf * (D / 16) + i;
           const uint4 u = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
           st_shared_v4(sQ + (c >> 3) * C::PANEL_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4), u.x, u.y, u.z, u.w);
         }
@@ -362,8 +374,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         ex = ex < -100 ? -100 : (ex > 100 ? 100 : ex);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
         cmul = p.c_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          const int c = hf * (D / 32) + i;
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
@@ -395,19 +408,41 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         const int my_ctx = ctx, my_ql = ql, L = ctx + ql;
         const unsigned long long my_bits = bits;
         const float my_cmul = cmul;
-        float m_run = -INFINITY, l_run = 0.f;
+        float m_run = -INFINITY, l_run = 0.f;      // the maximum of the row, the sum of this half
         float vref = 0.f, vup = 0.f;               // E4M3: power of two above the value scales, 2^7 / vref
         for (int j = dn.t0; j < dn.t1; ++j, ++it) {
-          const int kb = 128 * j;
+          const int kb = 128 * j, c0 = 64 * hf;    // this thread's keys: kb + c0 ..
           const bool tail = kb + 128 > my_ctx;     // drafted keys, or the end of the sequence
-          const uint32_t sb = tl + 128u * (it & 1);
           if (!bad && !warp_wait(BAR_S(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
           if (FP8 && !bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
           const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF + 1024 * sslot);
-          if (!bad) tc_fence_after();
-          float alpha_v = 1.f;
-          bool vscale_odd = false;
+          uint32_t s[2][32];
+          if (!bad) {
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) tmem_ld32(tl + 128u * (it & 1) + c0 + 32u * q, s[q]);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) reg_fence(s[q][i]);
+          float alpha = 1.f;
+          bool vscale_odd = false, rescale = false;
           if constexpr (FP8) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 k4 = reinterpret_cast<const float4*>(sc + c0 + 32 * q)[i];
+                float y[4];
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[q][4 * i]), __uint_as_float(s[q][4 * i + 1])),
+                                 f2_pack(k4.x, k4.y)), y[0], y[1]);
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[q][4 * i + 2]), __uint_as_float(s[q][4 * i + 3])),
+                                 f2_pack(k4.z, k4.w)), y[2], y[3]);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) s[q][4 * i + h] = __float_as_uint(y[h]);
+              }
             // largest finite value scale of the tile's keys
             const float4 v4 = reinterpret_cast<const float4*>(sc + 128)[lane];
             const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
@@ -423,64 +458,35 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
               const float nref = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + (top < 0x1p126f ? 0x00800000u : 0u));
-              alpha_v = vref / nref;
+              alpha = vref / nref;
+              rescale = true;
               vref = nref;
               vup = 128.f / nref;
             }
           }
-          // CH columns of S, scaled by the keys' scales, hidden ones -inf
-          auto load_s = [&](int c0, uint32_t (&s)[C::CH / 32][32]) {
-            if (!bad) {
+          if (tail) {
 #pragma unroll
-              for (int q = 0; q < C::CH / 32; ++q) tmem_ld32(sb + c0 + 32u * q, s[q]);
-              tmem_wait_ld();
+            for (int q = 0; q < 2; ++q) {
+              // 32 columns' visibility: the context, then this row's drafts (bits past q_len are clear)
+              const int rel = kb + c0 + 32 * q - my_ctx;
+              const uint32_t vis = rel >= 0    ? (rel < 64 ? static_cast<uint32_t>(my_bits >> rel) : 0u)
+                                   : rel > -32 ? (static_cast<uint32_t>(my_bits << -rel) | ((1u << -rel) - 1))
+                                               : ~0u;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((vis >> i) & 1)) s[q][i] = __float_as_uint(-INFINITY);
             }
-#pragma unroll
-            for (int q = 0; q < C::CH / 32; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) reg_fence(s[q][i]);
-            if constexpr (FP8) {
-#pragma unroll
-              for (int q = 0; q < C::CH / 32; ++q)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float4 k4 = reinterpret_cast<const float4*>(sc + c0 + 32 * q)[i];
-                  float y[4];
-                  f2_unpack(f2_mul(f2_pack(__uint_as_float(s[q][4 * i]), __uint_as_float(s[q][4 * i + 1])),
-                                   f2_pack(k4.x, k4.y)), y[0], y[1]);
-                  f2_unpack(f2_mul(f2_pack(__uint_as_float(s[q][4 * i + 2]), __uint_as_float(s[q][4 * i + 3])),
-                                   f2_pack(k4.z, k4.w)), y[2], y[3]);
-#pragma unroll
-                  for (int h = 0; h < 4; ++h) s[q][4 * i + h] = __float_as_uint(y[h]);
-                }
-            }
-            if (tail) {
-#pragma unroll
-              for (int q = 0; q < C::CH / 32; ++q) {
-                // 32 columns' visibility: the context, then this row's drafts (bits past q_len are clear)
-                const int rel = kb + c0 + 32 * q - my_ctx;
-                const uint32_t vis = rel >= 0    ? (rel < 64 ? static_cast<uint32_t>(my_bits >> rel) : 0u)
-                                     : rel > -32 ? (static_cast<uint32_t>(my_bits << -rel) | ((1u << -rel) - 1))
-                                                 : ~0u;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!((vis >> i) & 1)) s[q][i] = __float_as_uint(-INFINITY);
-              }
-            }
-          };
-          float mt = -INFINITY;
-#pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += C::CH) {
-            uint32_t s[C::CH / 32][32];
-            load_s(c0, s);
-#pragma unroll
-            for (int q = 0; q < C::CH / 32; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) mt = max3(mt, __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
           }
-          mt *= my_cmul;
-          bool rescale = alpha_v != 1.f;
-          float alpha = alpha_v;
+          float mt = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) mt = max3(mt, __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
+          // the halves' maxima meet; both threads of a row then decide alike
+          float* rm = red + 256 * (it & 1);
+          rm[128 * hf + r] = mt;
+          named_bar_sync(pair_bar, 64u);
+          mt = fmaxf(mt, rm[128 * (hf ^ 1) + r]) * my_cmul;
           if (mt > m_run + (FP8 ? TAU_E4M3 : TAU_BF16) || (m_run == -INFINITY && mt != -INFINITY)) {
             const float f = m_run == -INFINITY ? 0.f : ex2(m_run - mt);
             alpha *= f;
@@ -492,53 +498,48 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
           const uint32_t pb = tl + C::P_COL + 64u * (it & 1);
           const uint64_t cm2 = f2_pack(my_cmul, my_cmul), of2 = f2_pack(-off, -off);
           uint64_t sum = f2_pack(0.f, 0.f);
-#pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += C::CH) {
-            uint32_t s[C::CH / 32][32];
-            load_s(c0, s);
 #pragma unroll
-            for (int q = 0; q < C::CH / 32; ++q) {
-              if constexpr (!FP8) {
-                uint32_t pk[16];
+          for (int q = 0; q < 2; ++q) {
+            if constexpr (!FP8) {
+              uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  float a, b;
-                  f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), cm2, of2), a, b);
-                  a = ex2(a);
-                  b = ex2(b);
-                  sum = f2_add(sum, f2_pack(a, b));
-                  pk[i] = pack_bf16x2(a, b);
+              for (int i = 0; i < 16; ++i) {
+                float a, b;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), cm2, of2), a, b);
+                a = ex2(a);
+                b = ex2(b);
+                sum = f2_add(sum, f2_pack(a, b));
+                pk[i] = pack_bf16x2(a, b);
+              }
+              if (!bad) tmem_st16(pb + c0 / 2 + 16u * q, pk);
+            } else {
+              uint32_t hi[8], lo[8];
+              const uint64_t up2 = f2_pack(vup, vup);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + c0 + 32 * q)[i];
+                float e[4], y[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][4 * i + 2 * h]), __uint_as_float(s[q][4 * i + 2 * h + 1])),
+                                   cm2, of2), e[2 * h], e[2 * h + 1]);
+                  e[2 * h] = ex2(e[2 * h]);
+                  e[2 * h + 1] = ex2(e[2 * h + 1]);
+                  const uint64_t e2 = f2_pack(e[2 * h], e[2 * h + 1]);
+                  sum = f2_add(sum, e2);
+                  f2_unpack(f2_mul(f2_mul(e2, up2), h == 0 ? f2_pack(v4.x, v4.y) : f2_pack(v4.z, v4.w)), y[2 * h],
+                            y[2 * h + 1]);
                 }
-                if (!bad) tmem_st16(pb + c0 / 2 + 16u * q, pk);
-              } else {
-                uint32_t hi[8], lo[8];
-                const uint64_t up2 = f2_pack(vup, vup);
+                if (tail || vscale_odd) {          // hidden: 0 whatever the scale; seen and not finite: NaN
+                  const float v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + c0 + 32 * q)[i];
-                  float e[4], y[4];
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][4 * i + 2 * h]), __uint_as_float(s[q][4 * i + 2 * h + 1])),
-                                     cm2, of2), e[2 * h], e[2 * h + 1]);
-                    e[2 * h] = ex2(e[2 * h]);
-                    e[2 * h + 1] = ex2(e[2 * h + 1]);
-                    const uint64_t e2 = f2_pack(e[2 * h], e[2 * h + 1]);
-                    sum = f2_add(sum, e2);
-                    f2_unpack(f2_mul(f2_mul(e2, up2), h == 0 ? f2_pack(v4.x, v4.y) : f2_pack(v4.z, v4.w)), y[2 * h],
-                              y[2 * h + 1]);
-                  }
-                  if (tail || vscale_odd) {        // hidden: 0 whatever the scale; seen and not finite: NaN
-                    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] : __int_as_float(0x7fffffff));
-                  }
-                  e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
+                  for (int h = 0; h < 4; ++h) y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] : __int_as_float(0x7fffffff));
                 }
-                if (!bad) {
-                  tmem_st8(pb + c0 / 4 + 8u * q, hi);
-                  tmem_st8(pb + 32u + c0 / 4 + 8u * q, lo);
-                }
+                e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
+              }
+              if (!bad) {
+                tmem_st8(pb + c0 / 4 + 8u * q, hi);
+                tmem_st8(pb + 32u + c0 / 4 + 8u * q, lo);
               }
             }
           }
@@ -548,27 +549,29 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             l_run += s0 + s1;
           }
           if (!bad && j > dn.t0 && __any_sync(0xffffffffu, rescale)) {
-            // O must hold PV(it - 1) complete; PV(it) waits for this warp's arrival below
+            // O must hold PV(it - 1) complete; PV(it) waits for both warps' arrivals below.  Each half of the
+            // columns is one warp's
             if (!warp_wait(BAR_PV, (it - 1) & 1, ctl, WHERE_PAGED_USE)) {
               bad = true;
             } else {
               tc_fence_after();
 #pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
+              for (int q = 0; q < D / 64; ++q) {
+                const uint32_t at = tl + C::O_COL + hf * (D / 2) + 32u * q;
                 uint32_t o[32];
-                tmem_ld32(tl + C::O_COL + 32u * q, o);
+                tmem_ld32(at, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                   reg_fence(o[i]);
                   o[i] = __float_as_uint(__uint_as_float(o[i]) * (rescale ? alpha : 1.f));
                 }
-                tmem_st32(tl + C::O_COL + 32u * q, o);
+                tmem_st32(at, o);
               }
             }
           }
           if (tail) {
-            // thread = key row of the value tile: what must not meet a zero numerator is taken out
+            // thread = half of key row r of the value tile: what must not meet a zero numerator is taken out
             if (!bad && !warp_wait(FULLV(it % C::NV), (it / C::NV) & 1, ctl, WHERE_PAGED_USE)) bad = true;
             const int key = kb + r;
             if (!bad && key >= my_ctx) {
@@ -576,9 +579,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
               bool clear = key >= L;
               if (FP8 && !clear) clear = !finite_f(sc[128 + r]);
               bool odd = false;
+              constexpr int NC = C::ROW_BYTES / 32;
 #pragma unroll 1
-              for (int c = 0; c < C::ROW_BYTES / 16; ++c) {
-                uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * C::PANEL_BYTES + (((c & 7) ^ (r & 3)) << 4));
+              for (int i = 0; i < NC; ++i) {
+                const int c = hf * NC + i;
+                uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * C::PANEL_BYTES + (((c & 7) ^ (r & (NC - 1) & 3)) << 4));
                 if (clear) {
                   *at = make_uint4(0u, 0u, 0u, 0u);
                 } else if (!FP8) {
@@ -586,9 +591,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                   uint32_t* w = reinterpret_cast<uint32_t*>(&u);
                   bool hit = false;
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    if ((w[i] & 0x7f80u) == 0x7f80u) { w[i] &= 0xffff0000u; hit = true; }
-                    if ((w[i] & 0x7f800000u) == 0x7f800000u) { w[i] &= 0xffffu; hit = true; }
+                  for (int y = 0; y < 4; ++y) {
+                    if ((w[y] & 0x7f80u) == 0x7f80u) { w[y] &= 0xffff0000u; hit = true; }
+                    if ((w[y] & 0x7f800000u) == 0x7f800000u) { w[y] &= 0xffffu; hit = true; }
                   }
                   if (hit) *at = u;
                   odd = odd || hit;
@@ -610,11 +615,13 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             spar ^= 1;
           }
         }
-        // ---- end of the segment: what the value rows held that was not finite, the next segment's queries,
-        // then the output ----
-        named_bar_sync(1, 128);
+        // ---- end of the segment: the halves' sums, what the value rows held that was not finite, the next
+        // segment's queries, then the output ----
+        red[512 + 128 * hf + r] = l_run;
+        named_bar_sync(1, 256);
+        l_run = red[512 + r] + red[512 + 128 + r];
         const unsigned long long vodd = vodd_sh[seg & 1] & my_bits;
-        if (r == 0) vodd_sh[(seg & 1) ^ 1] = 0;    // read by all before this barrier; next written after BAR_Q
+        if (threadIdx.x == 0) vodd_sh[(seg & 1) ^ 1] = 0;    // read by all before this barrier; next written after BAR_Q
         x += dn.t1 - dn.t0;
         {
           const int rn = rt + p.group_ctas;
@@ -636,7 +643,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                                 ((static_cast<long long>(dn.b) * p.T + t) * p.Hq + head) * D;
           float* wrow = p.ws_o + (ws_slot * PAGED_TREE_ROWS + r) * D;
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
+          for (int q = hf * (D / 64); q < (hf + 1) * (D / 64); ++q) {
             uint32_t o[32];
             tmem_ld32(tl + C::O_COL + 32u * q, o);
             tmem_wait_ld();
@@ -676,8 +683,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             }
             __syncwarp();
           }
-          if (!whole) p.ws_l[ws_slot * PAGED_TREE_ROWS + r] = lse2;
-          else if (valid && p.lse != nullptr) p.lse[(static_cast<long long>(dn.b) * p.Hq + head) * p.T + t] = lse2 * LN2_P;
+          if (hf == 0) {
+            if (!whole) p.ws_l[ws_slot * PAGED_TREE_ROWS + r] = lse2;
+            else if (valid && p.lse != nullptr) p.lse[(static_cast<long long>(dn.b) * p.Hq + head) * p.T + t] = lse2 * LN2_P;
+          }
           tc_fence_before();                       // these reads of O before the next P's arrival
         }
       }
@@ -686,7 +695,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

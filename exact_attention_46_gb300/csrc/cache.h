@@ -88,6 +88,7 @@ struct PagedParams {
   long long page_stride, head_stride, tok_stride;   // elements
   float* ws_o;          // [slots][RB][D] partial outputs
   float* ws_l;          // [slots][RB] partial lse, log2 units
+  int4* cuts;           // [n_cta] (parts, sequence, key/value head, q_len) of the units to merge; nullptr: none
   int B, T, Hq, Hkv, G;
   uint32_t g_magic;     // ceil(2^32 / G), 0 for G = 1
   int n_pages, page_size, max_pages;
