@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     fence_barrier_init();
   }
   grid_launch_dependents();
+  grid_dependency_wait();       // everything below reads what earlier kernels may have written
   if (!tile_prefix(p, pre, scratch, NTHREADS)) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_LENS);
     if (threadIdx.x == 0) write_cut(p, pre, blockIdx.x, 0, 0);
@@ -200,13 +201,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     bool dead = false;                             // a wait gave up (the same in every lane)
     for (long long x = x0; x < x1 && !dead;) {
       const Segment s = find_segment(p, pre, x, x1);
-      const int L = __ldg(p.ctx_lens + s.b) + (p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T);
+      const int L = *(p.ctx_lens + s.b) + (p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
       const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
       // page of this lane's box in the batch that starts at tile j (-1: past the end).  The entry is
       // read before the length is known -- it lies in the table -- so the two loads overlap
       auto look_up = [&](int j) {
         const int at = (128 * j + (lane << br_log)) >> ps_log;
-        return j < s.t1 && at < p.max_pages ? __ldg(table + at) : -1;
+        return j < s.t1 && at < p.max_pages ? *(table + at) : -1;
       };
       const int batch = 32 >> pt_log;              // tiles of a batch
       int next = look_up(s.t0);
@@ -282,8 +283,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   unsigned long long my_bits;
   auto fetch = [&](long long x) {
     sg = find_segment(p, pre, x, x1);
-    ctx = __ldg(p.ctx_lens + sg.b);
-    ql = p.q_lens != nullptr ? __ldg(p.q_lens + sg.b) : p.T;
+    ctx = *(p.ctx_lens + sg.b);
+    ql = p.q_lens != nullptr ? *(p.q_lens + sg.b) : p.T;
     const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q) +
                               (static_cast<long long>(sg.b) * p.T * p.Hq + static_cast<long long>(sg.hkv) * p.G) * D;
 #pragma unroll
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (threadIdx.x < RB) {
       const int t = token_of(p, static_cast<int>(threadIdx.x));
       if (t < p.T)
-        my_bits = p.tree_mask != nullptr ? __ldg(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
+        my_bits = p.tree_mask != nullptr ? *(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
                                          : (t >= 63 ? ~0ull : (2ull << t) - 1);
     }
   };
@@ -787,8 +788,9 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
   __shared__ float part[NW][D + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = static_cast<int>(blockIdx.x / p.row_tiles), rt = static_cast<int>(blockIdx.x % p.row_tiles);
+  grid_launch_dependents();
   grid_dependency_wait();       // in every block: this grid's end stands for the key kernel's too
-  const int4 cut = __ldcg(p.cuts + c0 + 1);
+  const int4 cut = ld_l2(p.cuts + c0 + 1);
   const int n = cut.x;                                          // parts: groups c0 .. c0 + n - 1
   const int first = ROWS * blockIdx.y, rows = cut.w * p.G - rt * RB - first;
   if (n == 0 || rows <= 0) return;
@@ -798,54 +800,55 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
     float mx = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    // add a part of (lse l, weight s, output v); one that saw no key has l = -inf and weight 0, and zeros (or
+    // NaN, which stays)
+    auto add = [&](float l, float s, const float* v) {
+      const float m = fmaxf(mx, l);
+      const float f = mx == -INFINITY ? 1.f : ex2(mx - m), w = l == -INFINITY ? 1.f : ex2(l - m);
+      mx = m;
+      sum = fmaf(sum, f, s * w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * v[e]);
+    };
     // c0's part is its last unit's (slot 1), the others' their first's (slot 0)
     auto slot = [&](int c) { return 2ll * ((c0 + c) * static_cast<long long>(p.row_tiles) + rt) + (c == 0 ? 1 : 0); };
     if (live) {
-      for (int c = lane; c < n; c += 32) mx = fmaxf(mx, __ldcg(p.ws_l + slot(c) * RB + r));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       // lane: columns E lane ..; eight parts in flight
       for (int cb = sub; cb < n; cb += 8 * share) {
         float l[8], v[8][E];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          // past the last part: that part again, with no weight (no branch between the loads)
+          // past the last part: that part again, not added (no branch between the loads)
           const int c = cb + k * share < n ? cb + k * share : n - 1;
-          l[k] = __ldcg(p.ws_l + slot(c) * RB + r);
+          l[k] = ld_l2(p.ws_l + slot(c) * RB + r);
           const float* src = p.ws_o + (slot(c) * RB + r) * D + lane * E;
           if constexpr (E == 4) {
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(src));
+            const float4 u = ld_l2(reinterpret_cast<const float4*>(src));
             v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
           } else {
-            const float2 u = __ldcg(reinterpret_cast<const float2*>(src));
+            const float2 u = ld_l2(reinterpret_cast<const float2*>(src));
             v[k][0] = u.x; v[k][1] = u.y;
           }
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (cb + k * share >= n) break;
-          // a part that saw no key holds zeros (or NaN, which stays)
-          const float w = l[k] == -INFINITY ? 1.f : ex2(l[k] - mx);
-          sum += l[k] == -INFINITY ? 0.f : w;
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+          add(l[k], l[k] == -INFINITY ? 0.f : 1.f, v[k]);
         }
       }
     }
     if (share > 1) {
-      __syncthreads();
       if (live) {
 #pragma unroll
         for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-        if (lane == 0) part[warp][D] = sum;
+        if (lane == 0) {
+          part[warp][D] = mx;
+          part[warp][D + 1] = sum;
+        }
       }
       __syncthreads();
       if (live && sub == 0)
-        for (int w = 1; w < share; ++w) {
-          sum += part[warp + w][D];
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += part[warp + w][lane * E + e];
-        }
+        for (int w = 1; w < share; ++w) add(part[warp + w][D], part[warp + w][D + 1], &part[warp + w][lane * E]);
     }
     if (live && sub == 0) {
       const int pr = rt * RB + r, t = token_of(p, pr);
@@ -864,16 +867,8 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
 template <int D, int RB>
 cudaError_t launch_paged_combine(const PagedParams& p, cudaStream_t st) {
   if (p.n_cta < 2) return cudaSuccess;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_cta - 1) * p.row_tiles, RB / COMBINE_ROWS<RB>);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, RB>, p);
+  return launch_overlapped(paged_combine_kernel<D, RB>, dim3(static_cast<unsigned>(p.n_cta - 1) * p.row_tiles, RB / COMBINE_ROWS<RB>),
+                           256, 0, st, p);
 }
 
 template <int D, bool FP8, int NRB, bool WIDE>
@@ -889,8 +884,8 @@ cudaError_t launch_paged_d(const CUtensorMap& tk, const CUtensorMap& tv, const P
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  attn_paged_kernel<D, FP8, NRB, WIDE><<<p.n_cta, NTHREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess || !combine) return e;
+  e = launch_overlapped(attn_paged_kernel<D, FP8, NRB, WIDE>, dim3(p.n_cta), NTHREADS, C::SMEM_BYTES, st, tk, tv, p);
+  if (e != cudaSuccess || !combine) return e;
   return launch_paged_combine<D, C::RB>(p, st);
 }
 

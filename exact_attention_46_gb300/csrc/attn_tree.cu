@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     fence_barrier_init();
   }
   grid_launch_dependents();
+  grid_dependency_wait();       // everything below reads what earlier kernels may have written
   const bool fine = tile_prefix(p, pre, scratch, TREE_THREADS);
   if (!fine) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_LENS);
@@ -201,11 +202,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
       for (int rt = rt0; rt < p.row_tiles && !dead; rt += p.group_ctas)
         for (long long x = x0; x < x1 && !dead;) {
           const Segment s = find_segment(p, pre, x, x1);
-          const int L = __ldg(p.ctx_lens + s.b) + (p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T);
+          const int L = *(p.ctx_lens + s.b) + (p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
           const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
           auto look_up = [&](int j) {
             const int at = (128 * j + (lane << br_log)) >> ps_log;
-            return j < s.t1 && at < p.max_pages ? __ldg(table + at) : -1;
+            return j < s.t1 && at < p.max_pages ? *(table + at) : -1;
           };
           int next = look_up(s.t0);
           for (int j0 = s.t0; j0 < s.t1 && !dead; j0 += batch) {
@@ -340,13 +341,13 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // the last segment's S = Q K^T are complete.
     auto fetch = [&](int rt, long long x) {
       sg = find_segment(p, pre, x, x1);
-      ctx = __ldg(p.ctx_lens + sg.b);
-      ql = p.q_lens != nullptr ? __ldg(p.q_lens + sg.b) : p.T;
+      ctx = *(p.ctx_lens + sg.b);
+      ql = p.q_lens != nullptr ? *(p.q_lens + sg.b) : p.T;
       const int pr = rt * PAGED_TREE_ROWS + r, t = token_of(p, pr);
       const bool there = t < p.T;
       bits = 0;
       if (there)
-        bits = p.tree_mask != nullptr ? __ldg(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
+        bits = p.tree_mask != nullptr ? *(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
                                       : (t >= 63 ? ~0ull : (2ull << t) - 1);
       if (ql < 64) bits &= (1ull << ql) - 1;
       const uint4* src = reinterpret_cast<const uint4*>(
@@ -356,14 +357,14 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const int c = hf * (D / 16) + i;
-          const uint4 u = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 u = there ? *(src + c) : make_uint4(0u, 0u, 0u, 0u);
           st_shared_v4(sQ + (c >> 3) * C::PANEL_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4), u.x, u.y, u.z, u.w);
         }
       } else {
         float m = 0.f;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 u = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 u = there ? *(src + c) : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint4 u = there ? __ldg(src + 2 * c + y) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 u = there ? *(src + 2 * c + y) : make_uint4(0u, 0u, 0u, 0u);
             e4m3_terms4(__uint_as_float(u.x << 16) * up, __uint_as_float(u.x & 0xffff0000u) * up,
                         __uint_as_float(u.y << 16) * up, __uint_as_float(u.y & 0xffff0000u) * up, hi[2 * y], lo[2 * y]);
             e4m3_terms4(__uint_as_float(u.z << 16) * up, __uint_as_float(u.z & 0xffff0000u) * up,
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
               for (unsigned long long left = vodd; left != 0; left &= left - 1) {
                 const int key = my_ctx + __ffsll(left) - 1;
                 if (key < 128 * dn.t0 || key >= 128 * dn.t1) continue;
-                const int page = __ldg(p.page_table + static_cast<long long>(dn.b) * p.max_pages + key / p.page_size);
+                const int page = *(p.page_table + static_cast<long long>(dn.b) * p.max_pages + key / p.page_size);
                 if (page < 0 || page >= p.n_pages) continue;
                 const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_cache) + page * p.page_stride +
                                          dn.hkv * p.head_stride + (key % p.page_size) * p.tok_stride + 32 * q;
@@ -714,8 +715,8 @@ cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  attn_tree_kernel<D, FP8><<<p.n_cta * p.group_ctas, TREE_THREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess || !combine) return e;
+  e = launch_overlapped(attn_tree_kernel<D, FP8>, dim3(p.n_cta * p.group_ctas), TREE_THREADS, C::SMEM_BYTES, st, tk, tv, p);
+  if (e != cudaSuccess || !combine) return e;
   return launch_tree_combine(p, D, st);
 }
 

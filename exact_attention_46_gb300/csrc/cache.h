@@ -117,6 +117,24 @@ cudaError_t launch_attn_tree(const CUtensorMap& tk, const CUtensorMap& tv, const
                              bool combine, cudaStream_t st);
 cudaError_t launch_tree_combine(const PagedParams& p, int D, cudaStream_t st);
 
+// Launch a kernel that may become resident while the one before it on the stream ends; it waits for that
+// one's completion (griddepcontrol.wait) before it reads or writes anything.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                              const A&... a) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a...);
+}
+
 // Shared pieces of the C-ABI layer (api.cu).
 int api_fail(int code, const char* fmt, ...);
 int api_ok();

@@ -82,8 +82,8 @@ struct Turn {
       if (on[k]) {
         // entries (c, s) of pairs from c0 on (half), or from chunk k's first pair
         const float4* t = reinterpret_cast<const float4*>(row + (HALF ? 2 * c0 + 8 * k : (k ? c1 : c0)));
-        e[2 * k] = __ldg(t);
-        e[2 * k + 1] = __ldg(t + 1);
+        e[2 * k] = *(t);
+        e[2 * k + 1] = *(t + 1);
       }
   }
 
@@ -106,7 +106,7 @@ struct Turn {
 
 // Position of token t, or -1 (reported) when the table has no row for it.
 __device__ __forceinline__ int position(const RopeParams& r, uint32_t t, int* err_word, int* err_info) {
-  const int p = r.pos != nullptr ? __ldg(r.pos + t) : static_cast<int>(t % static_cast<uint32_t>(r.pos_wrap));
+  const int p = r.pos != nullptr ? *(r.pos + t) : static_cast<int>(t % static_cast<uint32_t>(r.pos_wrap));
   if (p >= 0 && p < r.n_pos) return p;
   note_bad(err_word, err_info, WHERE_ROPE_POS);
   return -1;
@@ -122,6 +122,8 @@ __device__ __forceinline__ void item_of(uint32_t block, int lanes, int n, uint32
 
 template <int D, bool HALF>
 __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) rope_apply_kernel(const RopeApplyParams p) {
+  grid_launch_dependents();
+  grid_dependency_wait();       // everything below reads what earlier kernels may have written
   constexpr int LPR = D / 16;
   const int l = threadIdx.x % LPR;
   uint32_t t;
@@ -171,6 +173,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 template <int D, bool HALF, bool FP8>
 __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) cache_append_kernel(const AppendParams p) {
+  grid_launch_dependents();
+  grid_dependency_wait();       // everything below reads what earlier kernels may have written
   constexpr int LPR = D / 16;
   const int l = threadIdx.x % LPR;
   // the first q_blocks blocks take the queries, the rest keys and values: a block's groups do like work
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) cache_append_kernel(co
   long long slot = 0;
   bool store = pos >= 0;
   if (which != 0) {
-    slot = __ldg(p.slots + t);
+    slot = *(p.slots + t);
     const bool in = slot < static_cast<long long>(p.cache.n_pages) << ps_log;
     if (!in) note_bad(p.err_word, p.err_info, WHERE_APPEND_SLOT);
     store = store && slot >= 0 && in;
@@ -278,6 +282,8 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* f) {
 // a lane (as above).
 template <int D, bool FP8>
 __global__ void __launch_bounds__(THREADS) cache_gather_kernel(const GatherParams p) {
+  grid_launch_dependents();
+  grid_dependency_wait();       // everything below reads what earlier kernels may have written
   constexpr int LPR = D / 16;
   const int l = threadIdx.x % LPR;
   const int ps_log = 31 - __clz(p.cache.page_size);
@@ -291,12 +297,12 @@ __global__ void __launch_bounds__(THREADS) cache_gather_kernel(const GatherParam
   int lo = 0, hi = p.n_seq;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(p.cu_seqlens + mid) <= tok) lo = mid; else hi = mid;
+    if (*(p.cu_seqlens + mid) <= tok) lo = mid; else hi = mid;
   }
-  const long long off = static_cast<long long>(tok) - __ldg(p.cu_seqlens + lo);
-  const bool in = off >= 0 && tok < __ldg(p.cu_seqlens + lo + 1) && (off >> ps_log) < p.max_pages;
+  const long long off = static_cast<long long>(tok) - *(p.cu_seqlens + lo);
+  const bool in = off >= 0 && tok < *(p.cu_seqlens + lo + 1) && (off >> ps_log) < p.max_pages;
   long long page = -1;
-  if (in) page = __ldg(p.page_table + static_cast<long long>(lo) * p.max_pages + (off >> ps_log));
+  if (in) page = *(p.page_table + static_cast<long long>(lo) * p.max_pages + (off >> ps_log));
   if (page < 0 || page >= p.cache.n_pages) {
     note_bad(p.err_word, p.err_info, WHERE_GATHER);
     return;
@@ -318,7 +324,7 @@ __global__ void __launch_bounds__(THREADS) cache_gather_kernel(const GatherParam
             u[kv][h][c].x = w.x;
             u[kv][h][c].y = w.y;
           }
-          scale[kv][h] = __ldg((kv ? p.cache.v_scale : p.cache.k_scale) + ((page * p.cache.Hkv + h0 + h) << ps_log) + at);
+          scale[kv][h] = *((kv ? p.cache.v_scale : p.cache.k_scale) + ((page * p.cache.Hkv + h0 + h) << ps_log) + at);
         } else {
           const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(kv ? p.cache.v : p.cache.k) + e;
           u[kv][h][0] = *reinterpret_cast<const uint4*>(src);
@@ -355,9 +361,7 @@ unsigned blocks_for(int subs, int tokens, int D) {
 template <int D>
 cudaError_t rope_d(const RopeApplyParams& p, bool half, cudaStream_t st) {
   const unsigned grid = blocks_for((p.H + HEADS - 1) / HEADS, p.n_tokens, D);
-  if (half) rope_apply_kernel<D, true><<<grid, THREADS, 0, st>>>(p);
-  else rope_apply_kernel<D, false><<<grid, THREADS, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(half ? rope_apply_kernel<D, true> : rope_apply_kernel<D, false>, dim3(grid), THREADS, 0, st, p);
 }
 
 template <int D>
@@ -365,22 +369,16 @@ cudaError_t append_d(AppendParams p, bool half, cudaStream_t st) {
   p.q_blocks = p.q != nullptr ? blocks_for((p.Hq + HEADS - 1) / HEADS, p.n_tokens, D) : 0;
   const unsigned grid = p.q_blocks + blocks_for(2 * ((p.cache.Hkv + HEADS - 1) / HEADS), p.n_tokens, D);
   const bool fp8 = p.cache.k_scale != nullptr;
-  if (half) {
-    if (fp8) cache_append_kernel<D, true, true><<<grid, THREADS, 0, st>>>(p);
-    else cache_append_kernel<D, true, false><<<grid, THREADS, 0, st>>>(p);
-  } else {
-    if (fp8) cache_append_kernel<D, false, true><<<grid, THREADS, 0, st>>>(p);
-    else cache_append_kernel<D, false, false><<<grid, THREADS, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  void (*kernel)(AppendParams) = half ? (fp8 ? cache_append_kernel<D, true, true> : cache_append_kernel<D, true, false>)
+                                      : (fp8 ? cache_append_kernel<D, false, true> : cache_append_kernel<D, false, false>);
+  return launch_overlapped(kernel, dim3(grid), THREADS, 0, st, p);
 }
 
 template <int D>
 cudaError_t gather_d(const GatherParams& p, cudaStream_t st) {
   const unsigned grid = blocks_for((p.cache.Hkv + HEADS - 1) / HEADS, p.total, D);
-  if (p.cache.k_scale != nullptr) cache_gather_kernel<D, true><<<grid, THREADS, 0, st>>>(p);
-  else cache_gather_kernel<D, false><<<grid, THREADS, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(p.cache.k_scale != nullptr ? cache_gather_kernel<D, true> : cache_gather_kernel<D, false>,
+                           dim3(grid), THREADS, 0, st, p);
 }
 
 }  // namespace

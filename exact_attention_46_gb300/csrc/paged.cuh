@@ -19,6 +19,33 @@ constexpr float LN2_P = 0.69314718055994530942f;
 enum : int { WHERE_PAGED_LOAD = 51, WHERE_PAGED_USE = 52, WHERE_PAGED_LENS = 53, WHERE_PAGED_PAGE = 54,
              WHERE_PAGED_MMA = 55 };
 
+// Loads of what another kernel of the same stream wrote: ordered after the wait for it, past L1.  (The
+// kernels here may start before that kernel has ended, so they use no read-only-cache loads, which the
+// compiler may move above the wait.)
+__device__ __forceinline__ float ld_l2(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float2 ld_l2(const float2* p) {
+  float2 v;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_l2(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int4 ld_l2(const int4* p) {
+  int4 v;
+  asm volatile("ld.global.cg.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // 16-byte asynchronous copy global -> shared, and an arrival on `bar` when this thread's copies so
 // far have landed (counted in the barrier's initial count).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -38,19 +65,37 @@ __device__ __forceinline__ void wait_drain_paged(uint32_t bar, uint32_t parity, 
     if (clock64() - t0 > limit) return;
 }
 
+// Key tiles of sequence b; ok becomes false if its lengths are out of range.
+__device__ __forceinline__ int tiles_of(const PagedParams& p, int b, bool& ok) {
+  const int ctx = *(p.ctx_lens + b), ql = p.q_lens != nullptr ? *(p.q_lens + b) : p.T;
+  const bool fine = ctx >= 0 && ql >= 0 && ql <= p.T &&
+                    static_cast<long long>(ctx) + ql <= static_cast<long long>(p.max_pages) * p.page_size;
+  ok = ok && fine;
+  return fine && ql > 0 ? (ctx + ql + 127) >> 7 : 0;
+}
+
 // Prefix sums of the sequences' key tiles into pre[0 .. B]; returns 0 if any length is out of
-// range.  Called by all `n` threads (n >= 32 a multiple of 32, n <= 1024).
+// range.  Called by all `n` threads of the block (a multiple of 32, at most 1024).
 __device__ __forceinline__ bool tile_prefix(const PagedParams& p, int* pre, int* scratch, int n) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.B + n - 1) / n, b0 = tid * per, b1 = min(p.B, b0 + per);
   bool ok = true;
+  if (p.B <= 32) {                             // every warp sums for itself
+    int incl = lane < p.B ? tiles_of(p, lane, ok) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (warp == 0 && lane < p.B) pre[lane + 1] = incl;
+    if (tid == 0) pre[0] = 0;
+    ok = __all_sync(0xffffffffu, ok);
+    __syncthreads();
+    return ok;
+  }
+  const int per = (p.B + n - 1) / n, b0 = tid * per, b1 = min(p.B, b0 + per);
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
-    const int ctx = __ldg(p.ctx_lens + b), ql = p.q_lens != nullptr ? __ldg(p.q_lens + b) : p.T;
-    const bool fine = ctx >= 0 && ql >= 0 && ql <= p.T &&
-                      static_cast<long long>(ctx) + ql <= static_cast<long long>(p.max_pages) * p.page_size;
-    ok = ok && fine;
-    const int tiles = fine && ql > 0 ? (ctx + ql + 127) >> 7 : 0;
+    const int tiles = tiles_of(p, b, ok);
     pre[b + 1] = tiles;                       // own entries only, until the scan below
     sum += tiles;
   }
@@ -122,7 +167,7 @@ __device__ __forceinline__ void write_cut(const PagedParams& p, const int* pre, 
     // the group that holds list position y is the last c with c W / N <= y
     const long long c0 = quotient((x - s.t0 + 1) * N - 1, W), c1 = quotient((x - s.t0 + s.n) * N - 1, W);
     if (s.t0 > 0 && c0 == i - 1)
-      c = make_int4(static_cast<int>(c1 - c0) + 1, s.b, s.hkv, p.q_lens != nullptr ? __ldg(p.q_lens + s.b) : p.T);
+      c = make_int4(static_cast<int>(c1 - c0) + 1, s.b, s.hkv, p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
   }
   p.cuts[i] = c;
 }

@@ -378,3 +378,46 @@ def test_prefill_then_drafts_then_read_back(fp8):
     assert (lse[:, -1] - one_lse[0, :, 0]).abs().max() <= 2.0 ** -8 * 24
     for i, t in enumerate(path):                        # the tree's rows on the accepted path
         assert (o[n + i].float() - tree[0, t].float()).abs().max() <= tol
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 36])
+def test_each_launch_sees_the_one_before(T, fp8):
+    # the launches may overlap at their ends, so: every step writes new rows over the old ones and attends to
+    # them at once, with new lengths, without a synchronisation between; every result must be the one
+    # that the same inputs give by themselves
+    B, Hq, Hkv, D, page, n = 5, 4, 2, 64, 16, 333
+    qkv = torch.from_numpy(synth.normal((6, B * n, Hq + 2 * Hkv, D), synth.seed_for(154, 0))).to(torch.bfloat16).cuda()
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    table = torch.randperm(B * 25, generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda().view(B, 25)
+    j = torch.arange(n, device="cuda")
+    slots = (table.long()[:, j // page] * page + j % page).reshape(-1)
+    pos = j.to(torch.int32).repeat(B)
+    cs = ops.rope_scaled_table(512, D)
+    step_lens = [torch.tensor([n - T - 7 * (i + b) for b in range(B)], dtype=torch.int32, device="cuda") for i in range(6)]
+
+    def new():
+        kc, vc = (torch.zeros((B * 25, Hkv, page, D), dtype=dt, device="cuda") for _ in range(2))
+        sc = [torch.ones((B * 25, Hkv, page), device="cuda") for _ in range(2)] if fp8 else [None, None]
+        return kc, vc, sc
+
+    def step(i, kc, vc, sc, ctx):
+        x = qkv[i]
+        q = ops.rope_kv_cache_append(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cs, pos, kc, vc, slots, *sc)
+        return ops.attn_decode_paged(q.view(B, n, Hq, D)[:, n - T:].contiguous(), kc, vc, table, ctx, *sc)
+
+    kc, vc, sc = new()
+    ctx = torch.empty(B, dtype=torch.int32, device="cuda")
+    got = []
+    for rep in range(3):
+        for i in range(6):
+            ctx.copy_(step_lens[i])
+            got.append(step(i, kc, vc, sc, ctx))
+    ops.check()
+    for i in range(6):
+        kc, vc, sc = new()
+        torch.cuda.synchronize()
+        want = step(i, kc, vc, sc, step_lens[i])
+        ops.check()
+        for rep in range(3):
+            assert torch.equal(got[6 * rep + i][0], want[0]) and torch.equal(got[6 * rep + i][1], want[1]), (rep, i)
