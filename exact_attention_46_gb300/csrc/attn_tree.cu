@@ -30,6 +30,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
+#include <type_traits>
 
 #include "cache.h"
 #include "paged.cuh"
@@ -67,12 +68,14 @@ struct TreeCfg {
   static constexpr int K_OFF = NQ * TILE_BYTES, V_OFF = K_OFF + NK * TILE_BYTES;
   static constexpr int SC_OFF = V_OFF + NV * TILE_BYTES;
   static constexpr int PRE_OFF = SC_OFF + NSC * 1024;
-  static constexpr int RED_OFF = PRE_OFF + (PAGED_MAX_BATCH + 2) * 4;       // [3][2][128] floats: maxima (twice), sums
+  static constexpr int RED_OFF = PRE_OFF + (PAGED_MAX_BATCH + 4) * 4;       // [3][2][128] floats: maxima (twice), sums
   static constexpr int FLAG_OFF = RED_OFF + 3 * 2 * 128 * 4;                // vodd [2] x 8, tmem, abort, scratch
-  static constexpr int BAR_OFF = FLAG_OFF + 96;
+  static constexpr int STAGE_ROW = 20;                                      // floats: 16 columns and padding
+  static constexpr int STAGE_OFF = FLAG_OFF + 96;                           // [8 warps][32][STAGE_ROW]
+  static constexpr int BAR_OFF = STAGE_OFF + 8 * 32 * STAGE_ROW * 4;
   static constexpr int NBAR = 8 + 2 * (NK + NV + NSC);
   static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NBAR * 8;
-  static_assert(FLAG_OFF % 8 == 0 && BAR_OFF % 8 == 0, "alignment");
+  static_assert(FLAG_OFF % 8 == 0 && STAGE_OFF % 16 == 0 && BAR_OFF % 8 == 0, "alignment");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
   static_assert(P_COL + 128 <= 512, "Tensor Memory budget");
 };
@@ -82,6 +85,11 @@ constexpr int MMA_WARP = 8, K_WARP = 9, S_WARP = 11;
 // Lazy rescale threshold (log2).  Numerators reach 2^TAU; E4M3's two terms then span [2^-10, 2^8] around
 // numerators scaled by 2^7.
 constexpr float TAU_BF16 = 8.0f, TAU_E4M3 = 1.0f;
+
+// Registers of a warpgroup, out of the block's: 384 threads x 168 = 2 x 128 x 200 + 128 x 104.  The E4M3
+// softmax spills 588 bytes in 168; bf16 fits.
+__device__ __forceinline__ void softmax_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
+__device__ __forceinline__ void other_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
 
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
@@ -185,6 +193,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{p.spin_limit, abort_flag, p.err_word, p.err_info};
+
+  if constexpr (FP8) {
+    if (warp >= MMA_WARP) other_registers();
+    else softmax_registers();
+  }
 
   if (warp >= K_WARP) {
     // ---- loads: K, V, E4M3 scales, a warp each.  Box i of a segment's list of boxes is br rows of
@@ -353,39 +366,46 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const __nv_bfloat16*>(p.q) +
           ((static_cast<long long>(sg.b) * p.T + t) * p.Hq + sg.hkv * p.G + pr - t * p.G) * D);
+      // this half of the row, all of it on its way before the first use
+      uint4 u[D / 16];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) u[i] = there ? src[hf * (D / 16) + i] : make_uint4(0u, 0u, 0u, 0u);
       if constexpr (!FP8) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const int c = hf * (D / 16) + i;
-          const uint4 u = there ? *(src + c) : make_uint4(0u, 0u, 0u, 0u);
-          st_shared_v4(sQ + (c >> 3) * C::PANEL_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4), u.x, u.y, u.z, u.w);
+          st_shared_v4(sQ + (c >> 3) * C::PANEL_BYTES + r * 128 + (((c & 7) ^ (r & 7)) << 4), u[i].x, u[i].y, u[i].z, u[i].w);
         }
       } else {
         float m = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 u = there ? *(src + c) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+          for (int k = 0; k < 4; ++k)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
         }
-        // power of two that brings the largest element into [128, 256): exact
+        // the row's largest element over its two threads (the sums' array is free here), and the power of
+        // two that brings it into [128, 256): exact
+        named_bar_sync(pair_bar, 64u);
+        red[512 + 128 * hf + r] = m;
+        named_bar_sync(pair_bar, 64u);
+        m = fmaxf(m, red[512 + 128 * (hf ^ 1) + r]);
         int ex = static_cast<int>(__float_as_uint(m) >> 23) - 127;
         ex = ex < -100 ? -100 : (ex > 100 ? 100 : ex);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
         cmul = p.c_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const int c = hf * (D / 32) + i;
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint4 u = there ? *(src + 2 * c + y) : make_uint4(0u, 0u, 0u, 0u);
-            e4m3_terms4(__uint_as_float(u.x << 16) * up, __uint_as_float(u.x & 0xffff0000u) * up,
-                        __uint_as_float(u.y << 16) * up, __uint_as_float(u.y & 0xffff0000u) * up, hi[2 * y], lo[2 * y]);
-            e4m3_terms4(__uint_as_float(u.z << 16) * up, __uint_as_float(u.z & 0xffff0000u) * up,
-                        __uint_as_float(u.w << 16) * up, __uint_as_float(u.w & 0xffff0000u) * up, hi[2 * y + 1],
+            const uint4 w = u[2 * i + y];
+            e4m3_terms4(__uint_as_float(w.x << 16) * up, __uint_as_float(w.x & 0xffff0000u) * up,
+                        __uint_as_float(w.y << 16) * up, __uint_as_float(w.y & 0xffff0000u) * up, hi[2 * y], lo[2 * y]);
+            e4m3_terms4(__uint_as_float(w.z << 16) * up, __uint_as_float(w.z & 0xffff0000u) * up,
+                        __uint_as_float(w.w << 16) * up, __uint_as_float(w.w & 0xffff0000u) * up, hi[2 * y + 1],
                         lo[2 * y + 1]);
           }
           const uint32_t at = sQ + r * C::PANEL_ROW +
@@ -410,40 +430,17 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         const unsigned long long my_bits = bits;
         const float my_cmul = cmul;
         float m_run = -INFINITY, l_run = 0.f;      // the maximum of the row, the sum of this half
-        float vref = 0.f, vup = 0.f;               // E4M3: power of two above the value scales, 2^7 / vref
+        float vref = 0.f;                          // E4M3: power of two above the value scales
         for (int j = dn.t0; j < dn.t1; ++j, ++it) {
           const int kb = 128 * j, c0 = 64 * hf;    // this thread's keys: kb + c0 ..
           const bool tail = kb + 128 > my_ctx;     // drafted keys, or the end of the sequence
           if (!bad && !warp_wait(BAR_S(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
           if (FP8 && !bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
           const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF + 1024 * sslot);
-          uint32_t s[2][32];
-          if (!bad) {
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 2; ++q) tmem_ld32(tl + 128u * (it & 1) + c0 + 32u * q, s[q]);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) reg_fence(s[q][i]);
+          if (!bad) tc_fence_after();
           float alpha = 1.f;
           bool vscale_odd = false, rescale = false;
           if constexpr (FP8) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 k4 = reinterpret_cast<const float4*>(sc + c0 + 32 * q)[i];
-                float y[4];
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[q][4 * i]), __uint_as_float(s[q][4 * i + 1])),
-                                 f2_pack(k4.x, k4.y)), y[0], y[1]);
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[q][4 * i + 2]), __uint_as_float(s[q][4 * i + 3])),
-                                 f2_pack(k4.z, k4.w)), y[2], y[3]);
-#pragma unroll
-                for (int h = 0; h < 4; ++h) s[q][4 * i + h] = __float_as_uint(y[h]);
-              }
             // largest finite value scale of the tile's keys
             const float4 v4 = reinterpret_cast<const float4*>(sc + 128)[lane];
             const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
@@ -462,27 +459,61 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
               alpha = vref / nref;
               rescale = true;
               vref = nref;
-              vup = 128.f / nref;
             }
           }
-          if (tail) {
+          // 32 columns of S from column c, times the keys' scales, hidden ones -inf
+          auto load_s = [&](int c, uint32_t (&s)[32]) {
+            if (!bad) {
+              tmem_ld32(tl + 128u * (it & 1) + c, s);
+              tmem_wait_ld();
+            }
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              // 32 columns' visibility: the context, then this row's drafts (bits past q_len are clear)
-              const int rel = kb + c0 + 32 * q - my_ctx;
+            for (int i = 0; i < 32; ++i) reg_fence(s[i]);
+            if constexpr (FP8) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 k4 = reinterpret_cast<const float4*>(sc + c)[i];
+                float y[4];
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), f2_pack(k4.x, k4.y)), y[0],
+                          y[1]);
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), f2_pack(k4.z, k4.w)),
+                          y[2], y[3]);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) s[4 * i + h] = __float_as_uint(y[h]);
+              }
+            }
+            if (tail) {
+              // the columns' visibility: the context, then this row's drafts (bits past q_len are clear)
+              const int rel = kb + c - my_ctx;
               const uint32_t vis = rel >= 0    ? (rel < 64 ? static_cast<uint32_t>(my_bits >> rel) : 0u)
                                    : rel > -32 ? (static_cast<uint32_t>(my_bits << -rel) | ((1u << -rel) - 1))
                                                : ~0u;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (!((vis >> i) & 1)) s[q][i] = __float_as_uint(-INFINITY);
+                if (!((vis >> i) & 1)) s[i] = __float_as_uint(-INFINITY);
             }
-          }
+          };
+          auto max_of = [&](const uint32_t (&s)[32], float m) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) m = max3(m, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+            return m;
+          };
           float mt = -INFINITY;
+          [[maybe_unused]] uint32_t sr[2][32];
+          if constexpr (FP8) {
+            // the logits are read from Tensor Memory again below: a tile whose 64 columns are unrolled is
+            // 1.2x slower, it misses the instruction cache
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              uint32_t s[32];
+              load_s(c0 + 32 * q, s);
+              mt = max_of(s, mt);
+            }
+          } else {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) mt = max3(mt, __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
+            for (int q = 0; q < 2; ++q) load_s(c0 + 32 * q, sr[q]);
+            mt = max_of(sr[1], max_of(sr[0], mt));
+          }
           // the halves' maxima meet; both threads of a row then decide alike
           float* rm = red + 256 * (it & 1);
           rm[128 * hf + r] = mt;
@@ -497,57 +528,72 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
           }
           const float off = m_run == -INFINITY ? 0.f : m_run;
           const uint32_t pb = tl + C::P_COL + 64u * (it & 1);
-          const uint64_t cm2 = f2_pack(my_cmul, my_cmul), of2 = f2_pack(-off, -off);
+          // E4M3: numerators times 2^7 / vref, a power of two that goes into the exponent (no scale seen: 1);
+          // what would leave fp32's range there (scales below 2^-53 or above 2^67) is multiplied on
+          const int want = FP8 && vref > 0.f ? 134 - static_cast<int>(__float_as_uint(vref) >> 23) : 0;
+          const int shift = want > 60 ? 60 : (want < -60 ? -60 : want);
+          const float extra = __uint_as_float(static_cast<uint32_t>(127 + want - shift) << 23);
+          const float off_v = off - (FP8 ? static_cast<float>(shift) : 0.f);
+          const uint64_t cm2 = f2_pack(my_cmul, my_cmul), of2 = f2_pack(-off_v, -off_v);
           uint64_t sum = f2_pack(0.f, 0.f);
+          if constexpr (!FP8) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            if constexpr (!FP8) {
+            for (int q = 0; q < 2; ++q) {
               uint32_t pk[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 float a, b;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), cm2, of2), a, b);
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[q][2 * i]), __uint_as_float(sr[q][2 * i + 1])), cm2, of2), a, b);
                 a = ex2(a);
                 b = ex2(b);
                 sum = f2_add(sum, f2_pack(a, b));
                 pk[i] = pack_bf16x2(a, b);
               }
               if (!bad) tmem_st16(pb + c0 / 2 + 16u * q, pk);
-            } else {
-              uint32_t hi[8], lo[8];
-              const uint64_t up2 = f2_pack(vup, vup);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + c0 + 32 * q)[i];
-                float e[4], y[4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  f2_unpack(f2_fma(f2_pack(__uint_as_float(s[q][4 * i + 2 * h]), __uint_as_float(s[q][4 * i + 2 * h + 1])),
-                                   cm2, of2), e[2 * h], e[2 * h + 1]);
-                  e[2 * h] = ex2(e[2 * h]);
-                  e[2 * h + 1] = ex2(e[2 * h + 1]);
-                  const uint64_t e2 = f2_pack(e[2 * h], e[2 * h + 1]);
-                  sum = f2_add(sum, e2);
-                  f2_unpack(f2_mul(f2_mul(e2, up2), h == 0 ? f2_pack(v4.x, v4.y) : f2_pack(v4.z, v4.w)), y[2 * h],
-                            y[2 * h + 1]);
-                }
-                if (tail || vscale_odd) {          // hidden: 0 whatever the scale; seen and not finite: NaN
-                  const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                  for (int h = 0; h < 4; ++h) y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] : __int_as_float(0x7fffffff));
-                }
-                e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
-              }
-              if (!bad) {
-                tmem_st8(pb + c0 / 4 + 8u * q, hi);
-                tmem_st8(pb + 32u + c0 / 4 + 8u * q, lo);
-              }
             }
+          } else {
+            // FIX: tiles where some numerator may meet a scale that is not finite, or needs `extra`
+            auto numerators = [&](auto fix_c) {
+              constexpr bool FIX = decltype(fix_c)::value;
+#pragma unroll 1
+              for (int q = 0; q < 2; ++q) {
+                uint32_t s[32], hi[8], lo[8];
+                load_s(c0 + 32 * q, s);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + c0 + 32 * q)[i];
+                  float e[4], y[4];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * i + 2 * h]), __uint_as_float(s[4 * i + 2 * h + 1])), cm2,
+                                     of2), e[2 * h], e[2 * h + 1]);
+                    e[2 * h] = ex2(e[2 * h]);
+                    e[2 * h + 1] = ex2(e[2 * h + 1]);
+                    const uint64_t e2 = f2_pack(e[2 * h], e[2 * h + 1]);
+                    sum = f2_add(sum, e2);
+                    f2_unpack(f2_mul(e2, h == 0 ? f2_pack(v4.x, v4.y) : f2_pack(v4.z, v4.w)), y[2 * h], y[2 * h + 1]);
+                  }
+                  if (FIX) {                       // hidden: 0 whatever the scale; seen and not finite: NaN
+                    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                      y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] * extra : __int_as_float(0x7fffffff));
+                  }
+                  e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
+                }
+                if (!bad) {
+                  tmem_st8(pb + c0 / 4 + 8u * q, hi);
+                  tmem_st8(pb + 32u + c0 / 4 + 8u * q, lo);
+                }
+              }
+            };
+            if (tail || vscale_odd || extra != 1.f) numerators(std::true_type{});
+            else numerators(std::false_type{});
           }
           {
             float s0, s1;
             f2_unpack(sum, s0, s1);
-            l_run += s0 + s1;
+            l_run += FP8 ? (s0 + s1) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23) : s0 + s1;
           }
           if (!bad && j > dn.t0 && __any_sync(0xffffffffu, rescale)) {
             // O must hold PV(it - 1) complete; PV(it) waits for both warps' arrivals below.  Each half of the
@@ -640,9 +686,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
           if (FP8) inv *= vref * 0x1p-7f;
           const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
           const long long head = static_cast<long long>(dn.hkv) * p.G + pr - t * p.G;
-          __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.o) +
-                                ((static_cast<long long>(dn.b) * p.T + t) * p.Hq + head) * D;
-          float* wrow = p.ws_o + (ws_slot * PAGED_TREE_ROWS + r) * D;
+          // a thread holds a row, whose columns lie side by side in memory: 16 columns of the warp's 32 rows at
+          // a time go through shared memory, so that a store covers rows in pieces of 32 or 64 bytes
+          float* stage = reinterpret_cast<float*>(base + C::STAGE_OFF) + warp * 32 * C::STAGE_ROW;
 #pragma unroll 1
           for (int q = hf * (D / 64); q < (hf + 1) * (D / 64); ++q) {
             uint32_t o[32];
@@ -659,7 +705,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
               for (unsigned long long left = vodd; left != 0; left &= left - 1) {
                 const int key = my_ctx + __ffsll(left) - 1;
                 if (key < 128 * dn.t0 || key >= 128 * dn.t1) continue;
-                const int page = *(p.page_table + static_cast<long long>(dn.b) * p.max_pages + key / p.page_size);
+                const int page = p.page_table[static_cast<long long>(dn.b) * p.max_pages + key / p.page_size];
                 if (page < 0 || page >= p.n_pages) continue;
                 const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_cache) + page * p.page_stride +
                                          dn.hkv * p.head_stride + (key % p.page_size) * p.tok_stride + 32 * q;
@@ -670,17 +716,33 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                 }
               }
             }
-            if (valid && whole) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              __syncwarp();
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(orow + 32 * q + 8 * i) =
-                    make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
-                               pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
-            } else if (valid) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float4*>(wrow + 32 * q + 4 * i) =
-                    make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                *reinterpret_cast<float4*>(stage + lane * C::STAGE_ROW + 4 * i) =
+                    make_float4(f[16 * y + 4 * i], f[16 * y + 4 * i + 1], f[16 * y + 4 * i + 2], f[16 * y + 4 * i + 3]);
+              __syncwarp();
+              const int per = whole ? 2 : 4;       // lanes of a row
+              for (int k = 0; k < per; ++k) {
+                const int row = k * (32 / per) + lane / per, col = (lane % per) * (16 / per);
+                const int row_pr = rt * PAGED_TREE_ROWS + 32 * (warp & 3) + row, row_t = token_of(p, row_pr);
+                if (row_t >= my_ql) continue;
+                const float* src = stage + row * C::STAGE_ROW + col;
+                const float4 a = *reinterpret_cast<const float4*>(src);
+                if (whole) {
+                  const float4 e = *reinterpret_cast<const float4*>(src + 4);
+                  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) +
+                                       ((static_cast<long long>(dn.b) * p.T + row_t) * p.Hq + dn.hkv * p.G + row_pr - row_t * p.G) * D +
+                                       32 * q + 16 * y + col;
+                  *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w),
+                                                              pack_bf16x2(e.x, e.y), pack_bf16x2(e.z, e.w));
+                } else {
+                  *reinterpret_cast<float4*>(p.ws_o + (ws_slot * PAGED_TREE_ROWS + 32 * (warp & 3) + row) * D + 32 * q +
+                                             16 * y + col) = a;
+                }
+              }
             }
             __syncwarp();
           }

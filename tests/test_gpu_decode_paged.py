@@ -193,6 +193,15 @@ def test_logits_far_apart_and_a_given_scale():
         p.check(*run(p, scale=0.25), scale=0.25)
 
 
+@pytest.mark.parametrize("T", [1, 8, 36])
+@pytest.mark.parametrize("power", [-100, -58, 70, 100])
+def test_value_scales_at_the_ends_of_their_range(T, power):
+    p = Problem([200, 900, 0], T, 4, 4, 64, 32, fp8=True, tree=T > 1)
+    p.scale[1].mul_(2.0 ** power)
+    p.val[1] = p.val[1] * 2.0 ** power
+    p.check(*run(p))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("T,Hq", [(6, 4), (20, 8)])
 def test_hidden_drafts_may_hold_anything(T, Hq, fp8):
