@@ -322,7 +322,7 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
   if (max_pages < 1 || static_cast<long long>(max_pages) * page_size > 0x7fff0000ll)
     return api_fail(ATTN_ERR_INVALID_ARG, "need max_pages >= 1 and max_pages * page_size < 2^31 (got %d)", max_pages);
   const long long tiles = (static_cast<long long>(max_pages) * page_size + 127) / 128;
-  if (tiles * B > 0x7fffffffll) return api_fail(ATTN_ERR_INVALID_ARG, "the page table spans too many keys");
+  if ((tiles + 16) * B > 0x7fffffffll) return api_fail(ATTN_ERR_INVALID_ARG, "the page table spans too many keys");
   const int G = Hq / Hkv;
   if (G * static_cast<long long>(T) > 65535)
     return api_fail(ATTN_ERR_UNSUPPORTED, "(Hq / Hkv) * T = %lld query rows per key/value head, at most 65535",
@@ -371,6 +371,7 @@ int attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, c
   p.page_size = page_size;
   p.max_pages = max_pages;
   p.row_tiles = row_tiles;
+  p.lead = PAGED_LEAD;
   p.n_cta = n_cta;
   p.group_ctas = group;
   p.ws_o = static_cast<float*>(workspace);

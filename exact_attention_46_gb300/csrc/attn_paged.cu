@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint64_t pol = l2_policy_evict_first();
     int it = 0;
     bool dead = false;                             // a wait gave up (the same in every lane)
-    for (long long x = x0; x < x1 && !dead;) {
-      const Segment s = find_segment(p, pre, x, x1);
+    Segment s;
+    for (long long x = x0; !dead && next_segment(p, pre, x, x1, s);) {
       const int L = *(p.ctx_lens + s.b) + (p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
       const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
       // page of this lane's box in the batch that starts at tile j (-1: past the end).  The entry is
@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
       }
-      x += s.t1 - s.t0;
     }
     if (pw == 0 && lane == 0) write_cut(p, pre, blockIdx.x, W, N);   // the loads are all on their way
     if (dead) {
@@ -281,8 +280,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   int ctx, ql;
   uint2 qraw[QN];
   unsigned long long my_bits;
-  auto fetch = [&](long long x) {
-    sg = find_segment(p, pre, x, x1);
+  auto fetch = [&](long long& x) -> bool {
+    if (!next_segment(p, pre, x, x1, sg)) return false;
     ctx = *(p.ctx_lens + sg.b);
     ql = p.q_lens != nullptr ? *(p.q_lens + sg.b) : p.T;
     const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q) +
@@ -312,12 +311,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         my_bits = p.tree_mask != nullptr ? *(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
                                          : (t >= 63 ? ~0ull : (2ull << t) - 1);
     }
+    return true;
   };
   if (threadIdx.x < RB) qmax[threadIdx.x] = 0;
-  fetch(x0);
+  long long x = x0;
+  bool more = fetch(x);
   named_bar_sync(1, 32 * NWARP);
   int it = 0;
-  for (long long x = x0; x < x1;) {
+  while (more) {
     const int L = ctx + ql;
     if (FP8) {
 #pragma unroll
@@ -676,8 +677,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // ---- the warps' partial results meet; the next segment's inputs are on their way meanwhile ----
     const Segment dn = sg;
     const int ql_dn = ql;
-    x += sg.t1 - sg.t0;
-    if (x < x1) fetch(x);
+    more = fetch(x);
 #pragma unroll
     for (int rb = 0; rb < NRB; ++rb) {
       float l[2];
@@ -776,15 +776,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-// Rows of a merge block.  Few rows a unit: the parts of a row are read by several warps at once.
+// Rows of a merge block of eight warps: one a warp where a unit has 128; few rows a unit: the parts of a row
+// are read by several warps at once.  (Four rows a warp, one after the other: 3 us more on 128 rows.)
 template <int RB>
 constexpr int COMBINE_ROWS = RB == PAGED_TREE_ROWS ? 8 : RB / 8;
 
 // Merge of the units that several groups share.  A block takes ROWS rows of one row tile of the unit that
-// group i + 1's start cuts first, if it cuts one; eight warps, 8 / ROWS for the parts of a row.
+// group i + 1's start cuts first, if it cuts one.
 template <int D, int RB>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p) {
-  constexpr int NW = 8, E = D / 32, ROWS = COMBINE_ROWS<RB>, share = NW / ROWS;
+  constexpr int NW = 8, E = D / 32, ROWS = COMBINE_ROWS<RB>;
+  constexpr int SHARE = NW / ROWS;
+  constexpr int BATCH = SHARE == 1 ? 4 : 8;                     // parts of a row in flight
   __shared__ float part[NW][D + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = static_cast<int>(blockIdx.x / p.row_tiles), rt = static_cast<int>(blockIdx.x % p.row_tiles);
@@ -794,72 +797,70 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
   const int n = cut.x;                                          // parts: groups c0 .. c0 + n - 1
   const int first = ROWS * blockIdx.y, rows = cut.w * p.G - rt * RB - first;
   if (n == 0 || rows <= 0) return;
-  {
-    const int r = first + warp / share, sub = warp % share;
-    const bool live = r - first < rows;
-    float mx = -INFINITY, sum = 0.f, acc[E];
+  // c0's part is its last unit's (slot 1), the others' their first's (slot 0)
+  auto slot = [&](int c) { return 2ll * ((c0 + c) * static_cast<long long>(p.row_tiles) + rt) + (c == 0 ? 1 : 0); };
+  const int r = first + warp / SHARE, sub = warp % SHARE;
+  const bool live = r - first < rows;
+  float mx = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    // add a part of (lse l, weight s, output v); one that saw no key has l = -inf and weight 0, and zeros (or
-    // NaN, which stays)
-    auto add = [&](float l, float s, const float* v) {
-      const float m = fmaxf(mx, l);
-      const float f = mx == -INFINITY ? 1.f : ex2(mx - m), w = l == -INFINITY ? 1.f : ex2(l - m);
-      mx = m;
-      sum = fmaf(sum, f, s * w);
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  // add a part of (lse l, weight s, output v); one that saw no key has l = -inf and weight 0, and zeros (or
+  // NaN, which stays)
+  auto add = [&](float l, float s, const float* v) {
+    const float m = fmaxf(mx, l);
+    const float f = mx == -INFINITY ? 1.f : ex2(mx - m), w = l == -INFINITY ? 1.f : ex2(l - m);
+    mx = m;
+    sum = fmaf(sum, f, s * w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * v[e]);
-    };
-    // c0's part is its last unit's (slot 1), the others' their first's (slot 0)
-    auto slot = [&](int c) { return 2ll * ((c0 + c) * static_cast<long long>(p.row_tiles) + rt) + (c == 0 ? 1 : 0); };
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, w * v[e]);
+  };
+  if (live) {
+    // lane: columns E lane ..
+    for (int cb = sub; cb < n; cb += BATCH * SHARE) {
+      float l[BATCH], v[BATCH][E];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        // past the last part: that part again, not added (no branch between the loads)
+        const int c = cb + k * SHARE < n ? cb + k * SHARE : n - 1;
+        l[k] = ld_l2(p.ws_l + slot(c) * RB + r);
+        const float* src = p.ws_o + (slot(c) * RB + r) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 u = ld_l2(reinterpret_cast<const float4*>(src));
+          v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
+        } else {
+          const float2 u = ld_l2(reinterpret_cast<const float2*>(src));
+          v[k][0] = u.x; v[k][1] = u.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        if (cb + k * SHARE >= n) break;
+        add(l[k], l[k] == -INFINITY ? 0.f : 1.f, v[k]);
+      }
+    }
+  }
+  if (SHARE > 1) {
     if (live) {
-      // lane: columns E lane ..; eight parts in flight
-      for (int cb = sub; cb < n; cb += 8 * share) {
-        float l[8], v[8][E];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          // past the last part: that part again, not added (no branch between the loads)
-          const int c = cb + k * share < n ? cb + k * share : n - 1;
-          l[k] = ld_l2(p.ws_l + slot(c) * RB + r);
-          const float* src = p.ws_o + (slot(c) * RB + r) * D + lane * E;
-          if constexpr (E == 4) {
-            const float4 u = ld_l2(reinterpret_cast<const float4*>(src));
-            v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
-          } else {
-            const float2 u = ld_l2(reinterpret_cast<const float2*>(src));
-            v[k][0] = u.x; v[k][1] = u.y;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (cb + k * share >= n) break;
-          add(l[k], l[k] == -INFINITY ? 0.f : 1.f, v[k]);
-        }
+      for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+      if (lane == 0) {
+        part[warp][D] = mx;
+        part[warp][D + 1] = sum;
       }
     }
-    if (share > 1) {
-      if (live) {
+    __syncthreads();
+    if (live && sub == 0)
+      for (int w = 1; w < SHARE; ++w) add(part[warp + w][D], part[warp + w][D + 1], &part[warp + w][lane * E]);
+  }
+  if (live && sub == 0) {
+    const int pr = rt * RB + r, t = token_of(p, pr);
+    const float inv = sum == 0.f ? 1.f : 1.f / sum;          // no key at all: the parts' zeros
+    const long long h = static_cast<long long>(cut.z) * p.G + pr - t * p.G;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<long long>(cut.y) * p.T + t) * p.Hq + h) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-        if (lane == 0) {
-          part[warp][D] = mx;
-          part[warp][D + 1] = sum;
-        }
-      }
-      __syncthreads();
-      if (live && sub == 0)
-        for (int w = 1; w < share; ++w) add(part[warp + w][D], part[warp + w][D + 1], &part[warp + w][lane * E]);
-    }
-    if (live && sub == 0) {
-      const int pr = rt * RB + r, t = token_of(p, pr);
-      const float inv = sum == 0.f ? 1.f : 1.f / sum;          // no key at all: the parts' zeros
-      const long long h = static_cast<long long>(cut.z) * p.G + pr - t * p.G;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + ((static_cast<long long>(cut.y) * p.T + t) * p.Hq + h) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-      if (lane == 0 && p.lse != nullptr)
-        p.lse[(static_cast<long long>(cut.y) * p.Hq + h) * p.T + t] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * LN2_P;
-    }
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[(static_cast<long long>(cut.y) * p.Hq + h) * p.T + t] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * LN2_P;
   }
 }
 

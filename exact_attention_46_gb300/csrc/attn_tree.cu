@@ -212,9 +212,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
       int it = 0, slot = 0;
       uint32_t par = 1;
       bool dead = false;                           // a wait gave up (the same in every lane)
+      Segment s;
       for (int rt = rt0; rt < p.row_tiles && !dead; rt += p.group_ctas)
-        for (long long x = x0; x < x1 && !dead;) {
-          const Segment s = find_segment(p, pre, x, x1);
+        for (long long x = x0; !dead && next_segment(p, pre, x, x1, s);) {
           const int L = *(p.ctx_lens + s.b) + (p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
           const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
           auto look_up = [&](int j) {
@@ -266,7 +266,6 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
               }
             }
           }
-          x += s.t1 - s.t0;
         }
       if (is_k && rt0 == 0 && lane == 0) write_cut(p, pre, group, W, N);
       if (dead) {
@@ -287,6 +286,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
       const uint64_t dk0 = smem_desc(sK, 16, C::SBO, C::LAYOUT);
       const uint64_t dv0 = smem_desc(sV, C::PANEL_BYTES, C::SBO, C::LAYOUT);
       bool ok = true;
+      Segment s;
       int it = 0, seg = 0;
       auto qk = [&](int i) -> bool {
         const int ks = i % C::NK;
@@ -307,8 +307,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         return true;
       };
       for (int rt = rt0; ok && rt < p.row_tiles; rt += p.group_ctas)
-        for (long long x = x0; ok && x < x1; ++seg) {
-          const Segment s = find_segment(p, pre, x, x1);
+        for (long long x = x0; ok && next_segment(p, pre, x, x1, s); ++seg) {
           const int n = s.t1 - s.t0;
           if (!(ok = wait_bounded(BAR_Q, seg & 1, ctl, WHERE_PAGED_MMA))) break;
           if (!(ok = qk(it))) break;
@@ -334,7 +333,6 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             mma_commit(EMPTYV(vs));
           }
           if (ok) mma_commit(BAR_O);
-          x += n;
         }
       mma_commit(BAR_DONE);
       wait_drain_paged(BAR_DONE, 0, p.spin_limit);
@@ -352,8 +350,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     bool bad = false;                              // a wait of this warp gave up; it still meets the barriers
     // Lengths, mask and query row of the segment that starts at x; the row goes to shared memory.  Runs when
     // the last segment's S = Q K^T are complete.
-    auto fetch = [&](int rt, long long x) {
-      sg = find_segment(p, pre, x, x1);
+    auto fetch = [&](int rt, long long& x) -> bool {
+      if (!next_segment(p, pre, x, x1, sg)) return false;
       ctx = *(p.ctx_lens + sg.b);
       ql = p.q_lens != nullptr ? *(p.q_lens + sg.b) : p.T;
       const int pr = rt * PAGED_TREE_ROWS + r, t = token_of(p, pr);
@@ -417,341 +415,341 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR_Q);
+      return true;
     };
     int it = 0, seg = 0, sslot = 0;
     uint32_t spar = 0;
-    bool first = true;
-    for (int rt = rt0; rt < p.row_tiles; rt += p.group_ctas)
-      for (long long x = x0; x < x1; ++seg) {
-        if (first) fetch(rt, x);
-        first = false;
-        const Segment dn = sg;
-        const int my_ctx = ctx, my_ql = ql, L = ctx + ql;
-        const unsigned long long my_bits = bits;
-        const float my_cmul = cmul;
-        float m_run = -INFINITY, l_run = 0.f;      // the maximum of the row, the sum of this half
-        float vref = 0.f;                          // E4M3: power of two above the value scales
-        for (int j = dn.t0; j < dn.t1; ++j, ++it) {
-          const int kb = 128 * j, c0 = 64 * hf;    // this thread's keys: kb + c0 ..
-          const bool tail = kb + 128 > my_ctx;     // drafted keys, or the end of the sequence
-          if (!bad && !warp_wait(BAR_S(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
-          if (FP8 && !bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
-          const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF + 1024 * sslot);
-          if (!bad) tc_fence_after();
-          float alpha = 1.f;
-          bool vscale_odd = false, rescale = false;
-          if constexpr (FP8) {
-            // largest finite value scale of the tile's keys
-            const float4 v4 = reinterpret_cast<const float4*>(sc + 128)[lane];
-            const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
-            float top = 0.f;
+    long long x = x0;
+    bool more = fetch(rt0, x);
+    for (int rt = rt0; more; ++seg) {
+      const Segment dn = sg;
+      const int dn_rt = rt;
+      const int my_ctx = ctx, my_ql = ql, L = ctx + ql;
+      const unsigned long long my_bits = bits;
+      const float my_cmul = cmul;
+      float m_run = -INFINITY, l_run = 0.f;      // the maximum of the row, the sum of this half
+      float vref = 0.f;                          // E4M3: power of two above the value scales
+      for (int j = dn.t0; j < dn.t1; ++j, ++it) {
+        const int kb = 128 * j, c0 = 64 * hf;    // this thread's keys: kb + c0 ..
+        const bool tail = kb + 128 > my_ctx;     // drafted keys, or the end of the sequence
+        if (!bad && !warp_wait(BAR_S(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+        if (FP8 && !bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
+        const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF + 1024 * sslot);
+        if (!bad) tc_fence_after();
+        float alpha = 1.f;
+        bool vscale_odd = false, rescale = false;
+        if constexpr (FP8) {
+          // largest finite value scale of the tile's keys
+          const float4 v4 = reinterpret_cast<const float4*>(sc + 128)[lane];
+          const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+          float top = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool in = kb + 4 * lane + i < L;
-              top = fmaxf(top, in && finite_f(vv[i]) ? vv[i] : 0.f);
-              vscale_odd = vscale_odd || (in && !finite_f(vv[i]));
-            }
-            vscale_odd = __any_sync(0xffffffffu, vscale_odd);
-            if (__any_sync(0xffffffffu, top > vref)) {
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const float nref = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + (top < 0x1p126f ? 0x00800000u : 0u));
-              alpha = vref / nref;
-              rescale = true;
-              vref = nref;
-            }
+          for (int i = 0; i < 4; ++i) {
+            const bool in = kb + 4 * lane + i < L;
+            top = fmaxf(top, in && finite_f(vv[i]) ? vv[i] : 0.f);
+            vscale_odd = vscale_odd || (in && !finite_f(vv[i]));
           }
-          // 32 columns of S from column c, times the keys' scales, hidden ones -inf
-          auto load_s = [&](int c, uint32_t (&s)[32]) {
-            if (!bad) {
-              tmem_ld32(tl + 128u * (it & 1) + c, s);
-              tmem_wait_ld();
-            }
+          vscale_odd = __any_sync(0xffffffffu, vscale_odd);
+          if (__any_sync(0xffffffffu, top > vref)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) reg_fence(s[i]);
-            if constexpr (FP8) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 k4 = reinterpret_cast<const float4*>(sc + c)[i];
-                float y[4];
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), f2_pack(k4.x, k4.y)), y[0],
-                          y[1]);
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), f2_pack(k4.z, k4.w)),
-                          y[2], y[3]);
-#pragma unroll
-                for (int h = 0; h < 4; ++h) s[4 * i + h] = __float_as_uint(y[h]);
-              }
-            }
-            if (tail) {
-              // the columns' visibility: the context, then this row's drafts (bits past q_len are clear)
-              const int rel = kb + c - my_ctx;
-              const uint32_t vis = rel >= 0    ? (rel < 64 ? static_cast<uint32_t>(my_bits >> rel) : 0u)
-                                   : rel > -32 ? (static_cast<uint32_t>(my_bits << -rel) | ((1u << -rel) - 1))
-                                               : ~0u;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((vis >> i) & 1)) s[i] = __float_as_uint(-INFINITY);
-            }
-          };
-          auto max_of = [&](const uint32_t (&s)[32], float m) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) m = max3(m, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-            return m;
-          };
-          float mt = -INFINITY;
-          [[maybe_unused]] uint32_t sr[2][32];
-          if constexpr (FP8) {
-            // the logits are read from Tensor Memory again below: a tile whose 64 columns are unrolled is
-            // 1.2x slower, it misses the instruction cache
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-              uint32_t s[32];
-              load_s(c0 + 32 * q, s);
-              mt = max_of(s, mt);
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) load_s(c0 + 32 * q, sr[q]);
-            mt = max_of(sr[1], max_of(sr[0], mt));
-          }
-          // the halves' maxima meet; both threads of a row then decide alike
-          float* rm = red + 256 * (it & 1);
-          rm[128 * hf + r] = mt;
-          named_bar_sync(pair_bar, 64u);
-          mt = fmaxf(mt, rm[128 * (hf ^ 1) + r]) * my_cmul;
-          if (mt > m_run + (FP8 ? TAU_E4M3 : TAU_BF16) || (m_run == -INFINITY && mt != -INFINITY)) {
-            const float f = m_run == -INFINITY ? 0.f : ex2(m_run - mt);
-            alpha *= f;
-            l_run *= f;
-            m_run = mt;
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float nref = __uint_as_float((__float_as_uint(top) & 0x7f800000u) + (top < 0x1p126f ? 0x00800000u : 0u));
+            alpha = vref / nref;
             rescale = true;
+            vref = nref;
           }
-          const float off = m_run == -INFINITY ? 0.f : m_run;
-          const uint32_t pb = tl + C::P_COL + 64u * (it & 1);
-          // E4M3: numerators times 2^7 / vref, a power of two that goes into the exponent (no scale seen: 1);
-          // what would leave fp32's range there (scales below 2^-53 or above 2^67) is multiplied on
-          const int want = FP8 && vref > 0.f ? 134 - static_cast<int>(__float_as_uint(vref) >> 23) : 0;
-          const int shift = want > 60 ? 60 : (want < -60 ? -60 : want);
-          const float extra = __uint_as_float(static_cast<uint32_t>(127 + want - shift) << 23);
-          const float off_v = off - (FP8 ? static_cast<float>(shift) : 0.f);
-          const uint64_t cm2 = f2_pack(my_cmul, my_cmul), of2 = f2_pack(-off_v, -off_v);
-          uint64_t sum = f2_pack(0.f, 0.f);
-          if constexpr (!FP8) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float a, b;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[q][2 * i]), __uint_as_float(sr[q][2 * i + 1])), cm2, of2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-                sum = f2_add(sum, f2_pack(a, b));
-                pk[i] = pack_bf16x2(a, b);
-              }
-              if (!bad) tmem_st16(pb + c0 / 2 + 16u * q, pk);
-            }
-          } else {
-            // FIX: tiles where some numerator may meet a scale that is not finite, or needs `extra`
-            auto numerators = [&](auto fix_c) {
-              constexpr bool FIX = decltype(fix_c)::value;
-#pragma unroll 1
-              for (int q = 0; q < 2; ++q) {
-                uint32_t s[32], hi[8], lo[8];
-                load_s(c0 + 32 * q, s);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + c0 + 32 * q)[i];
-                  float e[4], y[4];
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * i + 2 * h]), __uint_as_float(s[4 * i + 2 * h + 1])), cm2,
-                                     of2), e[2 * h], e[2 * h + 1]);
-                    e[2 * h] = ex2(e[2 * h]);
-                    e[2 * h + 1] = ex2(e[2 * h + 1]);
-                    const uint64_t e2 = f2_pack(e[2 * h], e[2 * h + 1]);
-                    sum = f2_add(sum, e2);
-                    f2_unpack(f2_mul(e2, h == 0 ? f2_pack(v4.x, v4.y) : f2_pack(v4.z, v4.w)), y[2 * h], y[2 * h + 1]);
-                  }
-                  if (FIX) {                       // hidden: 0 whatever the scale; seen and not finite: NaN
-                    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-                      y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] * extra : __int_as_float(0x7fffffff));
-                  }
-                  e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
-                }
-                if (!bad) {
-                  tmem_st8(pb + c0 / 4 + 8u * q, hi);
-                  tmem_st8(pb + 32u + c0 / 4 + 8u * q, lo);
-                }
-              }
-            };
-            if (tail || vscale_odd || extra != 1.f) numerators(std::true_type{});
-            else numerators(std::false_type{});
+        }
+        // 32 columns of S from column c, times the keys' scales, hidden ones -inf
+        auto load_s = [&](int c, uint32_t (&s)[32]) {
+          if (!bad) {
+            tmem_ld32(tl + 128u * (it & 1) + c, s);
+            tmem_wait_ld();
           }
-          {
-            float s0, s1;
-            f2_unpack(sum, s0, s1);
-            l_run += FP8 ? (s0 + s1) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23) : s0 + s1;
-          }
-          if (!bad && j > dn.t0 && __any_sync(0xffffffffu, rescale)) {
-            // O must hold PV(it - 1) complete; PV(it) waits for both warps' arrivals below.  Each half of the
-            // columns is one warp's
-            if (!warp_wait(BAR_PV, (it - 1) & 1, ctl, WHERE_PAGED_USE)) {
-              bad = true;
-            } else {
-              tc_fence_after();
-#pragma unroll 1
-              for (int q = 0; q < D / 64; ++q) {
-                const uint32_t at = tl + C::O_COL + hf * (D / 2) + 32u * q;
-                uint32_t o[32];
-                tmem_ld32(at, o);
-                tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  reg_fence(o[i]);
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) * (rescale ? alpha : 1.f));
-                }
-                tmem_st32(at, o);
-              }
+          for (int i = 0; i < 32; ++i) reg_fence(s[i]);
+          if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 k4 = reinterpret_cast<const float4*>(sc + c)[i];
+              float y[4];
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), f2_pack(k4.x, k4.y)), y[0],
+                        y[1]);
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), f2_pack(k4.z, k4.w)),
+                        y[2], y[3]);
+#pragma unroll
+              for (int h = 0; h < 4; ++h) s[4 * i + h] = __float_as_uint(y[h]);
             }
           }
           if (tail) {
-            // thread = half of key row r of the value tile: what must not meet a zero numerator is taken out
-            if (!bad && !warp_wait(FULLV(it % C::NV), (it / C::NV) & 1, ctl, WHERE_PAGED_USE)) bad = true;
-            const int key = kb + r;
-            if (!bad && key >= my_ctx) {
-              uint8_t* row = base + C::V_OFF + (it % C::NV) * C::TILE_BYTES + r * C::PANEL_ROW;
-              bool clear = key >= L;
-              if (FP8 && !clear) clear = !finite_f(sc[128 + r]);
-              bool odd = false;
-              constexpr int NC = C::ROW_BYTES / 32;
-#pragma unroll 1
-              for (int i = 0; i < NC; ++i) {
-                const int c = hf * NC + i;
-                uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * C::PANEL_BYTES + (((c & 7) ^ (r & (NC - 1) & 3)) << 4));
-                if (clear) {
-                  *at = make_uint4(0u, 0u, 0u, 0u);
-                } else if (!FP8) {
-                  uint4 u = *at;
-                  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-                  bool hit = false;
+            // the columns' visibility: the context, then this row's drafts (bits past q_len are clear)
+            const int rel = kb + c - my_ctx;
+            const uint32_t vis = rel >= 0    ? (rel < 64 ? static_cast<uint32_t>(my_bits >> rel) : 0u)
+                                 : rel > -32 ? (static_cast<uint32_t>(my_bits << -rel) | ((1u << -rel) - 1))
+                                             : ~0u;
 #pragma unroll
-                  for (int y = 0; y < 4; ++y) {
-                    if ((w[y] & 0x7f80u) == 0x7f80u) { w[y] &= 0xffff0000u; hit = true; }
-                    if ((w[y] & 0x7f800000u) == 0x7f800000u) { w[y] &= 0xffffu; hit = true; }
-                  }
-                  if (hit) *at = u;
-                  odd = odd || hit;
-                }
-              }
-              if (odd) atomicOr(vodd_sh + (seg & 1), 1ull << (key - my_ctx));
-            }
-            fence_proxy_async_smem();
+            for (int i = 0; i < 32; ++i)
+              if (!((vis >> i) & 1)) s[i] = __float_as_uint(-INFINITY);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(BAR_P(it & 1));
-            if (FP8) mbar_arrive(EMPTYS(sslot));
+        };
+        auto max_of = [&](const uint32_t (&s)[32], float m) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) m = max3(m, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          return m;
+        };
+        float mt = -INFINITY;
+        [[maybe_unused]] uint32_t sr[2][32];
+        if constexpr (FP8) {
+          // the logits are read from Tensor Memory again below: a tile whose 64 columns are unrolled is
+          // 1.2x slower, it misses the instruction cache
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            uint32_t s[32];
+            load_s(c0 + 32 * q, s);
+            mt = max_of(s, mt);
           }
-          if (FP8 && ++sslot == C::NSC) {
-            sslot = 0;
-            spar ^= 1;
-          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) load_s(c0 + 32 * q, sr[q]);
+          mt = max_of(sr[1], max_of(sr[0], mt));
         }
-        // ---- end of the segment: the halves' sums, what the value rows held that was not finite, the next
-        // segment's queries, then the output ----
-        red[512 + 128 * hf + r] = l_run;
-        named_bar_sync(1, 256);
-        l_run = red[512 + r] + red[512 + 128 + r];
-        const unsigned long long vodd = vodd_sh[seg & 1] & my_bits;
-        if (threadIdx.x == 0) vodd_sh[(seg & 1) ^ 1] = 0;    // read by all before this barrier; next written after BAR_Q
-        x += dn.t1 - dn.t0;
+        // the halves' maxima meet; both threads of a row then decide alike
+        float* rm = red + 256 * (it & 1);
+        rm[128 * hf + r] = mt;
+        named_bar_sync(pair_bar, 64u);
+        mt = fmaxf(mt, rm[128 * (hf ^ 1) + r]) * my_cmul;
+        if (mt > m_run + (FP8 ? TAU_E4M3 : TAU_BF16) || (m_run == -INFINITY && mt != -INFINITY)) {
+          const float f = m_run == -INFINITY ? 0.f : ex2(m_run - mt);
+          alpha *= f;
+          l_run *= f;
+          m_run = mt;
+          rescale = true;
+        }
+        const float off = m_run == -INFINITY ? 0.f : m_run;
+        const uint32_t pb = tl + C::P_COL + 64u * (it & 1);
+        // E4M3: numerators times 2^7 / vref, a power of two that goes into the exponent (no scale seen: 1);
+        // what would leave fp32's range there (scales below 2^-53 or above 2^67) is multiplied on
+        const int want = FP8 && vref > 0.f ? 134 - static_cast<int>(__float_as_uint(vref) >> 23) : 0;
+        const int shift = want > 60 ? 60 : (want < -60 ? -60 : want);
+        const float extra = __uint_as_float(static_cast<uint32_t>(127 + want - shift) << 23);
+        const float off_v = off - (FP8 ? static_cast<float>(shift) : 0.f);
+        const uint64_t cm2 = f2_pack(my_cmul, my_cmul), of2 = f2_pack(-off_v, -off_v);
+        uint64_t sum = f2_pack(0.f, 0.f);
+        if constexpr (!FP8) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float a, b;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[q][2 * i]), __uint_as_float(sr[q][2 * i + 1])), cm2, of2), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              sum = f2_add(sum, f2_pack(a, b));
+              pk[i] = pack_bf16x2(a, b);
+            }
+            if (!bad) tmem_st16(pb + c0 / 2 + 16u * q, pk);
+          }
+        } else {
+          // FIX: tiles where some numerator may meet a scale that is not finite, or needs `extra`
+          auto numerators = [&](auto fix_c) {
+            constexpr bool FIX = decltype(fix_c)::value;
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              uint32_t s[32], hi[8], lo[8];
+              load_s(c0 + 32 * q, s);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + c0 + 32 * q)[i];
+                float e[4], y[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  f2_unpack(f2_fma(f2_pack(__uint_as_float(s[4 * i + 2 * h]), __uint_as_float(s[4 * i + 2 * h + 1])), cm2,
+                                   of2), e[2 * h], e[2 * h + 1]);
+                  e[2 * h] = ex2(e[2 * h]);
+                  e[2 * h + 1] = ex2(e[2 * h + 1]);
+                  const uint64_t e2 = f2_pack(e[2 * h], e[2 * h + 1]);
+                  sum = f2_add(sum, e2);
+                  f2_unpack(f2_mul(e2, h == 0 ? f2_pack(v4.x, v4.y) : f2_pack(v4.z, v4.w)), y[2 * h], y[2 * h + 1]);
+                }
+                if (FIX) {                       // hidden: 0 whatever the scale; seen and not finite: NaN
+                  const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+                  for (int h = 0; h < 4; ++h)
+                    y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] * extra : __int_as_float(0x7fffffff));
+                }
+                e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
+              }
+              if (!bad) {
+                tmem_st8(pb + c0 / 4 + 8u * q, hi);
+                tmem_st8(pb + 32u + c0 / 4 + 8u * q, lo);
+              }
+            }
+          };
+          if (tail || vscale_odd || extra != 1.f) numerators(std::true_type{});
+          else numerators(std::false_type{});
+        }
         {
-          const int rn = rt + p.group_ctas;
-          if (x < x1) fetch(rt, x);
-          else if (rn < p.row_tiles) fetch(rn, x0);
+          float s0, s1;
+          f2_unpack(sum, s0, s1);
+          l_run += FP8 ? (s0 + s1) * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23) : s0 + s1;
         }
-        if (!bad && !warp_wait(BAR_O, seg & 1, ctl, WHERE_PAGED_USE)) bad = true;
-        if (!bad) {
-          tc_fence_after();
-          const int pr = rt * PAGED_TREE_ROWS + r, t = token_of(p, pr);
-          const bool valid = t < my_ql;
-          const bool whole = dn.t0 == 0 && dn.t1 == dn.n;
-          const long long ws_slot = 2ll * (group * static_cast<long long>(p.row_tiles) + rt) + (dn.t0 > 0 ? 0 : 1);
-          float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-          if (FP8) inv *= vref * 0x1p-7f;
-          const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
-          const long long head = static_cast<long long>(dn.hkv) * p.G + pr - t * p.G;
-          // a thread holds a row, whose columns lie side by side in memory: 16 columns of the warp's 32 rows at
-          // a time go through shared memory, so that a store covers rows in pieces of 32 or 64 bytes
-          float* stage = reinterpret_cast<float*>(base + C::STAGE_OFF) + warp * 32 * C::STAGE_ROW;
+        if (!bad && j > dn.t0 && __any_sync(0xffffffffu, rescale)) {
+          // O must hold PV(it - 1) complete; PV(it) waits for both warps' arrivals below.  Each half of the
+          // columns is one warp's
+          if (!warp_wait(BAR_PV, (it - 1) & 1, ctl, WHERE_PAGED_USE)) {
+            bad = true;
+          } else {
+            tc_fence_after();
 #pragma unroll 1
-          for (int q = hf * (D / 64); q < (hf + 1) * (D / 64); ++q) {
-            uint32_t o[32];
-            tmem_ld32(tl + C::O_COL + 32u * q, o);
-            tmem_wait_ld();
-            float f[32];
+            for (int q = 0; q < D / 64; ++q) {
+              const uint32_t at = tl + C::O_COL + hf * (D / 2) + 32u * q;
+              uint32_t o[32];
+              tmem_ld32(at, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              reg_fence(o[i]);
-              f[i] = __uint_as_float(o[i]) * inv;
-            }
-            if (valid && !FP8 && vodd != 0) {
-              // infinities and NaN of drafted value rows that this row sees
-              for (unsigned long long left = vodd; left != 0; left &= left - 1) {
-                const int key = my_ctx + __ffsll(left) - 1;
-                if (key < 128 * dn.t0 || key >= 128 * dn.t1) continue;
-                const int page = p.page_table[static_cast<long long>(dn.b) * p.max_pages + key / p.page_size];
-                if (page < 0 || page >= p.n_pages) continue;
-                const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_cache) + page * p.page_stride +
-                                         dn.hkv * p.head_stride + (key % p.page_size) * p.tok_stride + 32 * q;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float e = __bfloat162float(v[i]);
-                  if (!finite_f(e)) f[i] += e;
-                }
+              for (int i = 0; i < 32; ++i) {
+                reg_fence(o[i]);
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * (rescale ? alpha : 1.f));
               }
+              tmem_st32(at, o);
             }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(stage + lane * C::STAGE_ROW + 4 * i) =
-                    make_float4(f[16 * y + 4 * i], f[16 * y + 4 * i + 1], f[16 * y + 4 * i + 2], f[16 * y + 4 * i + 3]);
-              __syncwarp();
-              const int per = whole ? 2 : 4;       // lanes of a row
-              for (int k = 0; k < per; ++k) {
-                const int row = k * (32 / per) + lane / per, col = (lane % per) * (16 / per);
-                const int row_pr = rt * PAGED_TREE_ROWS + 32 * (warp & 3) + row, row_t = token_of(p, row_pr);
-                if (row_t >= my_ql) continue;
-                const float* src = stage + row * C::STAGE_ROW + col;
-                const float4 a = *reinterpret_cast<const float4*>(src);
-                if (whole) {
-                  const float4 e = *reinterpret_cast<const float4*>(src + 4);
-                  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) +
-                                       ((static_cast<long long>(dn.b) * p.T + row_t) * p.Hq + dn.hkv * p.G + row_pr - row_t * p.G) * D +
-                                       32 * q + 16 * y + col;
-                  *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w),
-                                                              pack_bf16x2(e.x, e.y), pack_bf16x2(e.z, e.w));
-                } else {
-                  *reinterpret_cast<float4*>(p.ws_o + (ws_slot * PAGED_TREE_ROWS + 32 * (warp & 3) + row) * D + 32 * q +
-                                             16 * y + col) = a;
-                }
-              }
-            }
-            __syncwarp();
           }
-          if (hf == 0) {
-            if (!whole) p.ws_l[ws_slot * PAGED_TREE_ROWS + r] = lse2;
-            else if (valid && p.lse != nullptr) p.lse[(static_cast<long long>(dn.b) * p.Hq + head) * p.T + t] = lse2 * LN2_P;
-          }
-          tc_fence_before();                       // these reads of O before the next P's arrival
         }
+        if (tail) {
+          // thread = half of key row r of the value tile: what must not meet a zero numerator is taken out
+          if (!bad && !warp_wait(FULLV(it % C::NV), (it / C::NV) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+          const int key = kb + r;
+          if (!bad && key >= my_ctx) {
+            uint8_t* row = base + C::V_OFF + (it % C::NV) * C::TILE_BYTES + r * C::PANEL_ROW;
+            bool clear = key >= L;
+            if (FP8 && !clear) clear = !finite_f(sc[128 + r]);
+            bool odd = false;
+            constexpr int NC = C::ROW_BYTES / 32;
+#pragma unroll 1
+            for (int i = 0; i < NC; ++i) {
+              const int c = hf * NC + i;
+              uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * C::PANEL_BYTES + (((c & 7) ^ (r & (NC - 1) & 3)) << 4));
+              if (clear) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              } else if (!FP8) {
+                uint4 u = *at;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+                bool hit = false;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  if ((w[y] & 0x7f80u) == 0x7f80u) { w[y] &= 0xffff0000u; hit = true; }
+                  if ((w[y] & 0x7f800000u) == 0x7f800000u) { w[y] &= 0xffffu; hit = true; }
+                }
+                if (hit) *at = u;
+                odd = odd || hit;
+              }
+            }
+            if (odd) atomicOr(vodd_sh + (seg & 1), 1ull << (key - my_ctx));
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(BAR_P(it & 1));
+          if (FP8) mbar_arrive(EMPTYS(sslot));
+        }
+        if (FP8 && ++sslot == C::NSC) {
+          sslot = 0;
+          spar ^= 1;
+        }
+      }
+      // ---- end of the segment: the halves' sums, what the value rows held that was not finite, the next
+      // segment's queries, then the output ----
+      red[512 + 128 * hf + r] = l_run;
+      named_bar_sync(1, 256);
+      l_run = red[512 + r] + red[512 + 128 + r];
+      const unsigned long long vodd = vodd_sh[seg & 1] & my_bits;
+      if (threadIdx.x == 0) vodd_sh[(seg & 1) ^ 1] = 0;    // read by all before this barrier; next written after BAR_Q
+      more = fetch(rt, x);
+      if (!more && rt + p.group_ctas < p.row_tiles) {      // the same keys for the CTA's next row tile
+        rt += p.group_ctas;
+        x = x0;
+        more = fetch(rt, x);
+      }
+      if (!bad && !warp_wait(BAR_O, seg & 1, ctl, WHERE_PAGED_USE)) bad = true;
+      if (!bad) {
+        tc_fence_after();
+        const int pr = dn_rt * PAGED_TREE_ROWS + r, t = token_of(p, pr);
+        const bool valid = t < my_ql;
+        const bool whole = dn.t0 == 0 && dn.t1 == dn.n;
+        const long long ws_slot = 2ll * (group * static_cast<long long>(p.row_tiles) + dn_rt) + (dn.t0 > 0 ? 0 : 1);
+        float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        if (FP8) inv *= vref * 0x1p-7f;
+        const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
+        const long long head = static_cast<long long>(dn.hkv) * p.G + pr - t * p.G;
+        // a thread holds a row, whose columns lie side by side in memory: 16 columns of the warp's 32 rows at
+        // a time go through shared memory, so that a store covers rows in pieces of 32 or 64 bytes
+        float* stage = reinterpret_cast<float*>(base + C::STAGE_OFF) + warp * 32 * C::STAGE_ROW;
+#pragma unroll 1
+        for (int q = hf * (D / 64); q < (hf + 1) * (D / 64); ++q) {
+          uint32_t o[32];
+          tmem_ld32(tl + C::O_COL + 32u * q, o);
+          tmem_wait_ld();
+          float f[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            reg_fence(o[i]);
+            f[i] = __uint_as_float(o[i]) * inv;
+          }
+          if (valid && !FP8 && vodd != 0) {
+            // infinities and NaN of drafted value rows that this row sees
+            for (unsigned long long left = vodd; left != 0; left &= left - 1) {
+              const int key = my_ctx + __ffsll(left) - 1;
+              if (key < 128 * dn.t0 || key >= 128 * dn.t1) continue;
+              const int page = p.page_table[static_cast<long long>(dn.b) * p.max_pages + key / p.page_size];
+              if (page < 0 || page >= p.n_pages) continue;
+              const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_cache) + page * p.page_stride +
+                                       dn.hkv * p.head_stride + (key % p.page_size) * p.tok_stride + 32 * q;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float e = __bfloat162float(v[i]);
+                if (!finite_f(e)) f[i] += e;
+              }
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(stage + lane * C::STAGE_ROW + 4 * i) =
+                  make_float4(f[16 * y + 4 * i], f[16 * y + 4 * i + 1], f[16 * y + 4 * i + 2], f[16 * y + 4 * i + 3]);
+            __syncwarp();
+            const int per = whole ? 2 : 4;       // lanes of a row
+            for (int k = 0; k < per; ++k) {
+              const int row = k * (32 / per) + lane / per, col = (lane % per) * (16 / per);
+              const int row_pr = dn_rt * PAGED_TREE_ROWS + 32 * (warp & 3) + row, row_t = token_of(p, row_pr);
+              if (row_t >= my_ql) continue;
+              const float* src = stage + row * C::STAGE_ROW + col;
+              const float4 a = *reinterpret_cast<const float4*>(src);
+              if (whole) {
+                const float4 e = *reinterpret_cast<const float4*>(src + 4);
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) +
+                                     ((static_cast<long long>(dn.b) * p.T + row_t) * p.Hq + dn.hkv * p.G + row_pr - row_t * p.G) * D +
+                                     32 * q + 16 * y + col;
+                *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w),
+                                                            pack_bf16x2(e.x, e.y), pack_bf16x2(e.z, e.w));
+              } else {
+                *reinterpret_cast<float4*>(p.ws_o + (ws_slot * PAGED_TREE_ROWS + 32 * (warp & 3) + row) * D + 32 * q +
+                                           16 * y + col) = a;
+              }
+            }
+          }
+          __syncwarp();
+        }
+        if (hf == 0) {
+          if (!whole) p.ws_l[ws_slot * PAGED_TREE_ROWS + r] = lse2;
+          else if (valid && p.lse != nullptr) p.lse[(static_cast<long long>(dn.b) * p.Hq + head) * p.T + t] = lse2 * LN2_P;
+        }
+        tc_fence_before();                       // these reads of O before the next P's arrival
+      }
       }
   }
 

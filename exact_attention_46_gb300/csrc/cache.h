@@ -93,6 +93,7 @@ struct PagedParams {
   uint32_t g_magic;     // ceil(2^32 / G), 0 for G = 1
   int n_pages, page_size, max_pages;
   int row_tiles;        // ceil(G * T / RB)
+  int lead;             // list entries a change of units costs (paged.cuh)
   int n_cta;            // groups of CTAs that share the key tiles out; a group has one CTA per row tile,
   int group_ctas;       // at most group_ctas
   float c_log2;         // softmax scale * log2(e)
@@ -107,6 +108,12 @@ constexpr int PAGED_MAX_DRAFT = 64;
 // Query rows per work unit for R = G * T packed rows.
 constexpr int PAGED_TREE_ROWS = 128;
 constexpr int paged_rows(int R) { return R <= 8 ? 8 : (R <= 16 ? 16 : (R <= 32 ? 32 : PAGED_TREE_ROWS)); }
+
+// List entries (128-key tiles) that a change of units is taken to cost.  Measured with 0, 2, 3, 4 and 6: trees
+// of 8 over long e4m3 contexts 92.2, 90.3, 89.4, 88.3, 87.8 us, trees of 32 bf16 50.0, 49.1, 48.3, 47.8, 47.5,
+// 30 e4m3 sequences of up to 2000 keys 25.8, 25.5, 25.2, 24.9, 25.1, bf16 units of 64 tiles 72.2, 72.2, 72.8, 73.4,
+// 73.6.
+constexpr int PAGED_LEAD = 4;
 
 // tk, tv: the cache as (D, page_size, Hkv, n_pages) with a box of one swizzle panel x
 // min(page_size, 128) rows.

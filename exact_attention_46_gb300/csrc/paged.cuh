@@ -2,7 +2,8 @@
 // it is cut over the CTAs, and the asynchronous copies outside TMA.
 //
 // A unit is (sequence, key/value head); its keys are cut into 128-key tiles.  The tiles of all units, in
-// the order sequence, key/value head, key, form one list of W; group i of N takes [i W / N,
+// the order sequence, key/value head, key, form one list, every unit led by p.lead empty entries that
+// stand for the time a CTA takes to change units; of the W entries group i of N takes [i W / N,
 // (i + 1) W / N).  A group is one CTA, or one per tile of packed query rows where there are several:
 // its CTAs go through the same keys at the same time, so all but the first find them in L2.
 // Everything is computed from the lengths on the device.
@@ -65,16 +66,16 @@ __device__ __forceinline__ void wait_drain_paged(uint32_t bar, uint32_t parity, 
     if (clock64() - t0 > limit) return;
 }
 
-// Key tiles of sequence b; ok becomes false if its lengths are out of range.
+// List entries of sequence b, per key/value head; ok becomes false if its lengths are out of range.
 __device__ __forceinline__ int tiles_of(const PagedParams& p, int b, bool& ok) {
   const int ctx = *(p.ctx_lens + b), ql = p.q_lens != nullptr ? *(p.q_lens + b) : p.T;
   const bool fine = ctx >= 0 && ql >= 0 && ql <= p.T &&
                     static_cast<long long>(ctx) + ql <= static_cast<long long>(p.max_pages) * p.page_size;
   ok = ok && fine;
-  return fine && ql > 0 ? (ctx + ql + 127) >> 7 : 0;
+  return fine && ql > 0 ? ((ctx + ql + 127) >> 7) + p.lead : 0;
 }
 
-// Prefix sums of the sequences' key tiles into pre[0 .. B]; returns 0 if any length is out of
+// Prefix sums of the sequences' list entries into pre[0 .. B]; returns 0 if any length is out of
 // range.  Called by all `n` threads of the block (a multiple of 32, at most 1024).
 __device__ __forceinline__ bool tile_prefix(const PagedParams& p, int* pre, int* scratch, int n) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -118,10 +119,11 @@ __device__ __forceinline__ bool tile_prefix(const PagedParams& p, int* pre, int*
   return ok;
 }
 
-// The piece of the tile list that starts at x and ends at x1 or with its unit.
+// The piece of the list that starts at x and ends at x1 or with its unit.
 struct Segment {
   int b, hkv;           // sequence, key/value head
-  int t0, t1, n;        // tiles [t0, t1) of the unit's n
+  int t0, t1, n;        // tiles [t0, t1) of the unit's n (none where the piece holds lead entries only)
+  int len;              // list entries
 };
 
 // x / y for y > 0, in 32 bits where both fit (the 64-bit division is a few hundred cycles).
@@ -145,13 +147,26 @@ __device__ __forceinline__ Segment find_segment(const PagedParams& p, const int*
   // x lies in sequence lo: empty ones before it have pre[lo + 1] == pre[lo]
   Segment s;
   s.b = lo;
-  s.n = pre[lo + 1] - pre[lo];
+  const int all = pre[lo + 1] - pre[lo];
   const long long y = x - pre[lo] * hr;
-  s.hkv = static_cast<int>(quotient(y, s.n));
-  s.t0 = static_cast<int>(y - static_cast<long long>(s.hkv) * s.n);
+  s.hkv = static_cast<int>(quotient(y, all));
+  const int at = static_cast<int>(y - static_cast<long long>(s.hkv) * all);
   const long long left = x1 - x;
-  s.t1 = left < s.n - s.t0 ? s.t0 + static_cast<int>(left) : s.n;
+  s.len = left < all - at ? static_cast<int>(left) : all - at;
+  s.n = all - p.lead;
+  s.t0 = max(0, at - p.lead);
+  s.t1 = max(0, at + s.len - p.lead);
   return s;
+}
+
+// The next piece with tiles in it, from x on; x becomes its end.  False: none before x1.
+__device__ __forceinline__ bool next_segment(const PagedParams& p, const int* pre, long long& x, long long x1, Segment& s) {
+  while (x < x1) {
+    s = find_segment(p, pre, x, x1);
+    x += s.len;
+    if (s.t1 > s.t0) return true;
+  }
+  return false;
 }
 
 __device__ __forceinline__ long long cta_start(long long i, long long W, long long N) { return quotient(i * W, N); }
@@ -164,7 +179,7 @@ __device__ __forceinline__ void write_cut(const PagedParams& p, const int* pre, 
   if (i < N) {
     const long long x = cta_start(i, W, N);
     const Segment s = find_segment(p, pre, x, W);
-    // the group that holds list position y is the last c with c W / N <= y
+    // the group that holds list position y is the last c with c W / N <= y; x - t0 is tile 0's
     const long long c0 = quotient((x - s.t0 + 1) * N - 1, W), c1 = quotient((x - s.t0 + s.n) * N - 1, W);
     if (s.t0 > 0 && c0 == i - 1)
       c = make_int4(static_cast<int>(c1 - c0) + 1, s.b, s.hkv, p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
