@@ -1,0 +1,760 @@
+// attn_lanes.cu -- attention of a few drafted tokens over a paged key/value cache: 9 to 64 query rows
+// (heads of a group x drafted tokens) per key/value head, for sm_103a.  What it computes, the
+// readings and the list of key tiles are attn_paged.cu's and paged.cuh's.
+//
+// The keys of a tile take the 128 rows of tcgen05's tile and the NR = 16, 32 or 64 query rows its columns:
+//     S^T = K Q^T      [128 keys x NR]      K as it lies in the cache, Q row-major
+//     O^T += V^T P^T   [D x NR]             V and the numerators with the long side contiguous
+// so no product is spent on rows that are not there, a softmax thread holds one key (its scales, its place
+// in the tree are one scalar each) and the cache's E4M3 codes go to the tensor core unconverted.
+//   * warps 0..7 softmax: thread = key r, half hf of the rows.  Its numerators go to shared memory as one
+//     row of P (two tiles of terms for E4M3), its sums stay in registers until the unit ends.  The maxima of
+//     the rows run over threads, and moving them is rare: the four warps of a half vote once per tile
+//     whether any logit passed its row's maximum by 2^TAU, and only then reduce them over the lanes;
+//   * warp 8 issues the MMAs, one S ahead of PV and across units; 9 to 11 load K, V and scales
+//     (load_tiles); 12..15 bring the next unit's queries, a buffer ahead;
+//   * O^T's lanes are the columns of an output row, so the epilogue's stores cover rows as they are.
+// E4M3: queries and numerators are two E4M3 terms each (attn_tree.cu has the arithmetic); a thread multiplies
+// its numerators by its value's scale over vref, a power of two at or above the scales so far.
+// Hidden keys, value rows past the end and drafted values that are not finite: as in attn_tree.cu.
+// Every mbarrier wait is bounded.
+#include <atomic>
+#include <cfloat>
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "cache.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace ea46 {
+
+namespace {
+
+template <int D, bool FP8, int NR>
+struct LanesCfg {
+  static constexpr int ESZ = FP8 ? 1 : 2;
+  static constexpr int ROW_BYTES = D * ESZ;
+  static constexpr int PANEL_ROW = ROW_BYTES >= 128 ? 128 : ROW_BYTES;
+  static constexpr int NPANEL = ROW_BYTES / PANEL_ROW;
+  static constexpr int PANEL_BYTES = 128 * PANEL_ROW;
+  static constexpr int TILE_BYTES = 128 * ROW_BYTES;
+  static constexpr int NQ = FP8 ? 2 : 1;                       // terms of queries
+  static constexpr int NP = FP8 ? 3 : 1;                       // terms of numerators
+  static constexpr int HALF = NR / 2;                          // rows of a softmax warp
+  static constexpr int Q_TERM = NR * ROW_BYTES;
+  static constexpr int P_ROW = NR * ESZ > 64 ? 128 : 64;       // bytes of a key's row of P, swizzled as wide
+  static constexpr int P_TERM = 128 * P_ROW;
+  static constexpr int NSC = FP8 ? 6 : 0;                      // stages of 128 key and 128 value scales
+  static constexpr uint32_t SBO = 8 * PANEL_ROW, LAYOUT = PANEL_ROW == 128 ? 2u : 4u;
+  static constexpr uint32_t P_SBO = 8 * P_ROW, P_LAYOUT = P_ROW == 128 ? 2u : 4u;
+  static constexpr int KSTEPS_QK = ROW_BYTES / 32, STEPS_PER_PANEL = PANEL_ROW / 32;
+  static constexpr int UMMA_K = FP8 ? 32 : 16, KSTEPS_PV = 128 / UMMA_K;
+  static constexpr uint32_t FMT = FP8 ? 0u : 1u;
+  static constexpr uint32_t IDESC_QK = instr_desc(FMT, 0, 128, NR);
+  // A = V^T with its rows (the columns of V) contiguous: bit 15.  The tile has 128 rows for D = 64 too: the upper
+  // half multiplies whatever lies behind the panel in shared memory, and its lanes are never read.
+  static constexpr uint32_t IDESC_PV = instr_desc(FMT, 1, 128, NR) | (1u << 15) | (FP8 ? 1u << 10 : 0u);
+  static_assert(!FP8 || FMT == 0, "bits 7 and 10: formats of A (E4M3) and B (E5M2)");
+  // Tensor Memory: two S buffers, O
+  static constexpr uint32_t O_COL = 2 * NR, COLS = NR == 64 ? 256 : (NR == 32 ? 128 : 64);
+  // shared memory from the end of what the K and V rings leave
+  static constexpr int SMALL = 1024 * NSC + (PAGED_MAX_BATCH + 4) * 4 + 4 * 8 * HALF * 4 + 8 * HALF * 8 + 2 * NR * 12 + 128 + 1024;
+  static constexpr int ROOM = (227 * 1024 - 1024 - SMALL - 2 * (NP * P_TERM + NQ * Q_TERM)) / TILE_BYTES;
+  static constexpr int NK = ROOM >= 16 ? 8 : (ROOM + 1) / 2, NV = ROOM >= 16 ? 8 : ROOM / 2;
+  static constexpr int V_OFF = NK * TILE_BYTES;
+  static constexpr int P_OFF = V_OFF + NV * TILE_BYTES;         // [2][NP]
+  static constexpr int Q_OFF = P_OFF + 2 * NP * P_TERM;         // [2][NQ]
+  static constexpr int SC_OFF = Q_OFF + 2 * NQ * Q_TERM;
+  static constexpr int VIS_OFF = SC_OFF + NSC * 1024;           // [2][NR] u64: drafted keys a row sees
+  static constexpr int ROWAT_OFF = VIS_OFF + 2 * NR * 8;        // [8 warps][HALF] i64
+  static constexpr int QMUL_OFF = ROWAT_OFF + 8 * HALF * 8;     // [2][NR] floats: softmax scale of a row's codes
+  static constexpr int NMAX_OFF = QMUL_OFF + 2 * NR * 4;        // [8 warps][HALF] minus the running maxima
+  static constexpr int FAC_OFF = NMAX_OFF + 8 * HALF * 4;       // [8 warps][HALF]
+  static constexpr int RED_OFF = FAC_OFF + 8 * HALF * 4;        // [2 halves][4 quarters][HALF]: maxima, then sums
+  static constexpr int PRE_OFF = RED_OFF + 2 * 8 * HALF * 4;
+  static constexpr int FLAG_OFF = PRE_OFF + (PAGED_MAX_BATCH + 4) * 4;   // vodd [4] x 8, vtop [8], tmem, abort, scratch [16]
+  static constexpr int BAR_OFF = FLAG_OFF + 32 + 32 + 8 + 64;
+  static constexpr int NBAR = 11 + 2 * (NK + NV + NSC);
+  static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NBAR * 8;
+  static_assert(VIS_OFF % 16 == 0 && QMUL_OFF % 16 == 0 && NMAX_OFF % 16 == 0 && FLAG_OFF % 8 == 0 && BAR_OFF % 8 == 0, "alignment");
+  static_assert(Q_OFF % 1024 == 0 && Q_TERM % 1024 == 0, "swizzle atoms");
+  static_assert(2 * NP * P_TERM >= PANEL_BYTES, "the panel behind the last V tile");
+  static_assert(NV >= 2 && SMEM_BYTES <= 227 * 1024, "shared memory budget");
+};
+
+constexpr int LANES_THREADS = 512;
+constexpr int MMA_WARP = 8, K_WARP = 9, S_WARP = 11, Q_WARP = 12;
+// Lazy rescale threshold (log2).  Numerators reach 2^TAU; over E4M3 they are scaled by 2^(15 - TAU), the top of E5M2.
+constexpr float TAU_BF16 = 8.0f, TAU_E4M3 = 4.0f, TOP_E4M3 = 2048.0f;
+
+// Four numerators in [0, 2^15] as three E5M2 terms (packed bytes): fp16 first (2^-11), whose upper byte is
+// the first term, the remainder's upper byte the second, and what is left then rounded: each takes three bits
+// at least, so the sum is off by 2^-9 of the number, or 2^-17, half of E5M2's smallest step.
+__device__ __forceinline__ void e5m2_terms4(float a, float b, float c, float d, uint32_t (&t)[3]) {
+  asm("{\n\t.reg .b32 x, y, p, q, r, s;\n\t.reg .b16 u, v;\n\t"
+      "cvt.rn.f16x2.f32 x, %4, %3;\n\tcvt.rn.f16x2.f32 y, %6, %5;\n\t"
+      "prmt.b32 %0, x, y, 0x7531;\n\t"
+      "and.b32 p, x, 0xff00ff00;\n\tand.b32 q, y, 0xff00ff00;\n\t"
+      "sub.rn.f16x2 x, x, p;\n\tsub.rn.f16x2 y, y, q;\n\t"
+      "prmt.b32 %1, x, y, 0x7531;\n\t"
+      "and.b32 r, x, 0xff00ff00;\n\tand.b32 s, y, 0xff00ff00;\n\t"
+      "sub.rn.f16x2 x, x, r;\n\tsub.rn.f16x2 y, y, s;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 u, x;\n\tcvt.rn.satfinite.e5m2x2.f16x2 v, y;\n\t"
+      "mov.b32 %2, {u, v};\n\t}"
+      : "=r"(t[0]), "=r"(t[1]), "=r"(t[2]) : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
+// Registers of a warpgroup for NR = 64, out of the block's: 512 threads x 128 = 256 x 168 + 256 x 88.  Its
+// softmax spills 416 bytes (E4M3: 480) in 128.
+__device__ __forceinline__ void softmax_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 168;"); }
+__device__ __forceinline__ void other_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+
+// N columns of this warp's 32 lanes of Tensor Memory.
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) { tmem_ld32(at, r); }
+
+// Whether any thread of named barrier `id`'s n threads brings `mine`; a barrier among them.
+__device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t n, bool mine) {
+  uint32_t any;
+  asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %3, 0;\n\tbarrier.cta.red.or.pred b, %1, %2, a;\n\t"
+               "selp.u32 %0, 1, 0, b;\n\t}" : "=r"(any) : "r"(id), "r"(n), "r"(mine ? 1u : 0u) : "memory");
+  return any != 0;
+}
+
+// Floats as unsigned integers in the same order (no NaN).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float((u >> 31) ? u ^ 0x80000000u : ~u);
+}
+
+// Sum over the warp's lanes of column lane % N.
+template <int N>
+__device__ __forceinline__ float column_sum(const float (&x)[N]) {
+  const uint32_t lane = lane_id();
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = x[i];
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = (lane & o) != 0;
+      const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + o], o);
+      v[i] = (up ? v[i + o] : v[i]) + other;
+    }
+#pragma unroll
+  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  return v[0];
+}
+
+template <int D, bool FP8, int NR>
+__global__ void __launch_bounds__(LANES_THREADS, 1)
+    attn_lanes_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const PagedParams p) {
+  using C = LanesCfg<D, FP8, NR>;
+  constexpr int HALF = C::HALF;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_u32 - raw_u32);
+  const uint32_t sK = base_u32, sV = base_u32 + C::V_OFF, sP = base_u32 + C::P_OFF, sQ = base_u32 + C::Q_OFF;
+  unsigned long long* vis_sh = reinterpret_cast<unsigned long long*>(base + C::VIS_OFF);
+  float* qmul_sh = reinterpret_cast<float*>(base + C::QMUL_OFF);
+  float* red = reinterpret_cast<float*>(base + C::RED_OFF);
+  int* pre = reinterpret_cast<int*>(base + C::PRE_OFF);
+  unsigned long long* vodd_sh = reinterpret_cast<unsigned long long*>(base + C::FLAG_OFF);   // [4]
+  uint32_t* vtop_sh = reinterpret_cast<uint32_t*>(base + C::FLAG_OFF + 32);                  // [8 warps]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::FLAG_OFF + 64);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::FLAG_OFF + 68);
+  int* scratch = reinterpret_cast<int*>(base + C::FLAG_OFF + 72);                            // [16]
+  const uint32_t bar0 = base_u32 + C::BAR_OFF;
+  const uint32_t BAR_O = bar0, BAR_PV = bar0 + 8, BAR_DONE = bar0 + 16;
+  auto BAR_S = [&](int b) { return bar0 + 24 + 8u * b; };
+  auto BAR_P = [&](int b) { return bar0 + 40 + 8u * b; };
+  auto FULLQ = [&](int b) { return bar0 + 56 + 8u * b; };
+  auto EMPTYQ = [&](int b) { return bar0 + 72 + 8u * b; };
+  auto FULLK = [&](int s) { return bar0 + 88 + 8u * s; };
+  auto EMPTYK = [&](int s) { return bar0 + 88 + 8u * (C::NK + s); };
+  auto FULLV = [&](int s) { return bar0 + 88 + 8u * (2 * C::NK + s); };
+  auto EMPTYV = [&](int s) { return bar0 + 88 + 8u * (2 * C::NK + C::NV + s); };
+  auto FULLS = [&](int s) { return bar0 + 88 + 8u * (2 * (C::NK + C::NV) + s); };
+  auto EMPTYS = [&](int s) { return bar0 + 88 + 8u * (2 * (C::NK + C::NV) + C::NSC + s); };
+
+  const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
+  if (threadIdx.x == 0) {
+    mbar_init(BAR_O, 1);
+    mbar_init(BAR_PV, 1);
+    mbar_init(BAR_DONE, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(BAR_S(b), 1);
+      mbar_init(BAR_P(b), 8);
+      mbar_init(FULLQ(b), 4);
+      mbar_init(EMPTYQ(b), 1 + 8);
+    }
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(FULLK(s), 1);
+      mbar_init(EMPTYK(s), 1);
+    }
+    for (int s = 0; s < C::NV; ++s) {
+      mbar_init(FULLV(s), 1);
+      mbar_init(EMPTYV(s), 1);
+    }
+    for (int s = 0; s < C::NSC; ++s) {
+      mbar_init(FULLS(s), 32);
+      mbar_init(EMPTYS(s), 8);
+    }
+    *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) vodd_sh[i] = 0;
+    fence_barrier_init();
+  }
+  grid_launch_dependents();
+  grid_dependency_wait();       // everything below reads what earlier kernels may have written
+  const bool fine = tile_prefix(p, pre, scratch, LANES_THREADS);
+  if (!fine) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_LENS);
+    if (threadIdx.x == 0) write_cut(p, pre, blockIdx.x, 0, 0);
+    return;
+  }
+  const long long W = static_cast<long long>(pre[p.B]) * p.Hkv;
+  const long long N = W < p.n_cta ? W : p.n_cta;
+  const int group = blockIdx.x;
+  if (group >= N) {
+    if (threadIdx.x == 0) write_cut(p, pre, group, W, N);
+    return;
+  }
+  const long long x0 = cta_start(group, W, N), x1 = cta_start(group + 1ll, W, N);
+  if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_slot), C::COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{p.spin_limit, abort_flag, p.err_word, p.err_info};
+  const TileRings rings{sK, sV, base_u32 + C::SC_OFF, FULLK(0), EMPTYK(0), FULLV(0), EMPTYV(0), FULLS(0), EMPTYS(0)};
+
+  if constexpr (NR == 64) {
+    if (warp >= MMA_WARP) other_registers();
+    else softmax_registers();
+  }
+
+  if (warp >= Q_WARP) {
+    // ---- queries: a warp every fourth row, lane = D / 32 elements ----
+    constexpr int E = D / 32, ROWS = NR / 4, BATCH = ROWS < 8 ? ROWS : 8;
+    const int w = warp - Q_WARP;
+    Segment s;
+    long long x = x0;
+    for (int seg = 0; next_segment(p, pre, x, x1, s); ++seg) {
+      const int buf = seg & 1;
+      if (!warp_wait(EMPTYQ(buf), ((seg >> 1) & 1) ^ 1, ctl, WHERE_PAGED_LOAD)) break;
+      const int ql = p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T;
+      if (w < NR / 32 || (NR < 32 && w == 0 && lane < NR)) {
+        const int r = 32 * w + lane, t = token_of(p, r);
+        unsigned long long bits = 0;
+        if (t < p.T)
+          bits = p.tree_mask != nullptr ? *(p.tree_mask + static_cast<long long>(s.b) * p.T + t)
+                                        : (t >= 63 ? ~0ull : (2ull << t) - 1);
+        if (ql < 64) bits &= (1ull << ql) - 1;
+        vis_sh[buf * NR + r] = bits;
+        if (!FP8) qmul_sh[buf * NR + r] = p.c_log2;
+      }
+#pragma unroll 1
+      for (int i0 = 0; i0 < ROWS; i0 += BATCH) {
+        uint32_t u[BATCH][E / 2];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int r = 4 * (i0 + i) + w, t = token_of(p, r);
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+              ((static_cast<long long>(s.b) * p.T + t) * p.Hq + s.hkv * p.G + r - t * p.G) * D + E * lane;
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) u[i][k] = 0;
+          if (t < p.T) {
+            if constexpr (E == 4) {
+              const uint2 y = *reinterpret_cast<const uint2*>(src);
+              u[i][0] = y.x;
+              u[i][E / 2 - 1] = y.y;
+            } else {
+              u[i][0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int r = 4 * (i0 + i) + w;
+          const int at = E * C::ESZ * lane, pb = at % C::PANEL_ROW;      // this lane's bytes of the row
+          const int swz = C::PANEL_ROW == 128 ? (r & 7) : ((r >> 1) & 3);
+          const uint32_t dst = sQ + buf * C::NQ * C::Q_TERM + (at / C::PANEL_ROW) * (NR * C::PANEL_ROW) + r * C::PANEL_ROW +
+                               (((pb >> 4) ^ swz) << 4) + (pb & 15);
+          if constexpr (!FP8) {
+            if constexpr (E == 4)
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(u[i][0]), "r"(u[i][E / 2 - 1]) : "memory");
+            else
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(u[i][0]) : "memory");
+          } else {
+            // the row's largest element and the power of two that brings it into [128, 256): exact
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k) m = max(m, max(u[i][k] & 0x7fffu, (u[i][k] >> 16) & 0x7fffu));
+            m = __reduce_max_sync(0xffffffffu, m);
+            int ex = static_cast<int>(m >> 7) - 127;
+            ex = ex < -100 ? -100 : (ex > 100 ? 100 : ex);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
+            float f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              f[k] = k < E ? __uint_as_float((k & 1) ? u[i][(k / 2) % (E / 2)] & 0xffff0000u : u[i][(k / 2) % (E / 2)] << 16) * up : 0.f;
+            uint32_t hi, lo;
+            e4m3_terms4(f[0], f[1], f[2], f[3], hi, lo);
+            if constexpr (E == 4) {
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(hi) : "memory");
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + C::Q_TERM), "r"(lo) : "memory");
+            } else {
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(static_cast<uint16_t>(hi)) : "memory");
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + C::Q_TERM), "h"(static_cast<uint16_t>(lo)) : "memory");
+            }
+            // an infinite query element, which E4M3 cannot hold, makes its row's logits NaN
+            if (lane == 0)
+              qmul_sh[buf * NR + r] = m >= 0x7f80u ? __int_as_float(0x7fffffff)
+                                                   : p.c_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(FULLQ(buf));
+    }
+  } else if (warp >= K_WARP) {
+    if (FP8 || warp < S_WARP) load_tiles<C>(p, pre, tmK, tmV, rings, warp - K_WARP, 0, x0, x1, ctl);
+    if (warp == K_WARP && lane == 0) write_cut(p, pre, group, W, N);
+  } else if (warp == MMA_WARP) {
+    // ---- MMA issue ----
+    if (elect_one()) {
+      const uint64_t dk0 = smem_desc(sK, 16, C::SBO, C::LAYOUT);
+      const uint64_t dv0 = smem_desc(sV, C::PANEL_BYTES, C::SBO, C::LAYOUT);
+      const uint64_t dq0 = smem_desc(sQ, 16, C::SBO, C::LAYOUT);
+      const uint64_t dp0 = smem_desc(sP, C::P_TERM, C::P_SBO, C::P_LAYOUT);
+      const uint32_t hk = static_cast<uint32_t>(dk0 >> 32), hq = static_cast<uint32_t>(dq0 >> 32);
+      const uint32_t hv = static_cast<uint32_t>(dv0 >> 32), hp = static_cast<uint32_t>(dp0 >> 32);
+      Segment s;
+      long long x = x0;
+      int left = 0, seg = -1, ki = 0;            // of the tiles that S was issued for
+      uint32_t first = 0, last = 0;              // bit ki & 1: first, last tile of its segment
+      // S of the next tile; 0: there is none, -1: a wait gave up
+      auto qk = [&]() -> int {
+        const uint32_t bit = 1u << (ki & 1);
+        first &= ~bit;
+        last &= ~bit;
+        if (left == 0) {
+          if (!next_segment(p, pre, x, x1, s)) return 0;
+          left = s.t1 - s.t0;
+          ++seg;
+          first |= bit;
+          if (!wait_bounded(FULLQ(seg & 1), (seg >> 1) & 1, ctl, WHERE_PAGED_MMA)) return -1;
+        }
+        const int ks = ki % C::NK;
+        if (!wait_bounded(FULLK(ks), (ki / C::NK) & 1, ctl, WHERE_PAGED_MMA)) return -1;
+        tc_fence_after();
+        const uint32_t ak = static_cast<uint32_t>(dk0) + ((ks * C::TILE_BYTES) >> 4);
+        const uint32_t bq = static_cast<uint32_t>(dq0) + (((seg & 1) * C::NQ * C::Q_TERM) >> 4);
+        const uint32_t d = tmem + static_cast<uint32_t>(NR) * (ki & 1);
+#pragma unroll
+        for (int term = 0; term < C::NQ; ++term)
+#pragma unroll
+          for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
+            const uint32_t in = (kk % C::STEPS_PER_PANEL) * 32, pn = kk / C::STEPS_PER_PANEL;
+            const uint32_t a = ak + ((pn * C::PANEL_BYTES + in) >> 4);
+            const uint32_t b = bq + ((term * C::Q_TERM + pn * (NR * C::PANEL_ROW) + in) >> 4);
+            mma_ss<FP8>(d, a, hk, b, hq, C::IDESC_QK, (kk > 0 || term > 0) ? 1u : 0u);
+          }
+        mma_commit(BAR_S(ki & 1));
+        mma_commit(EMPTYK(ks));
+        if (--left == 0) {
+          mma_commit(EMPTYQ(seg & 1));
+          last |= bit;
+        }
+        ++ki;
+        return 1;
+      };
+      int more = qk();
+      for (int it = 0; more > 0; ++it) {
+        // S(it + 1) overwrites S(it - 1), which the softmax read before it handed over P(it - 1)
+        const bool is_first = (first >> (it & 1)) & 1, is_last = (last >> (it & 1)) & 1;
+        more = qk();
+        if (more < 0) break;
+        if (!wait_bounded(BAR_P(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_MMA)) break;
+        const int vs = it % C::NV;
+        if (!wait_bounded(FULLV(vs), (it / C::NV) & 1, ctl, WHERE_PAGED_MMA)) break;
+        tc_fence_after();
+        const uint32_t av = static_cast<uint32_t>(dv0) + ((vs * C::TILE_BYTES) >> 4);
+        const uint32_t bp = static_cast<uint32_t>(dp0) + (((it & 1) * C::NP * C::P_TERM) >> 4);
+#pragma unroll
+        for (int term = 0; term < C::NP; ++term)
+#pragma unroll
+          for (int kk = 0; kk < C::KSTEPS_PV; ++kk) {
+            const uint32_t a = av + ((kk * C::UMMA_K * C::PANEL_ROW) >> 4);
+            const uint32_t b = bp + ((term * C::P_TERM + kk * C::UMMA_K * C::P_ROW) >> 4);
+            const uint32_t acc = (!is_first || kk > 0 || term > 0) ? 1u : 0u;
+            mma_ss<FP8>(tmem + C::O_COL, a, hv, b, hp, C::IDESC_PV, acc);
+          }
+        mma_commit(BAR_PV);
+        mma_commit(EMPTYV(vs));
+        if (is_last) mma_commit(BAR_O);
+      }
+      mma_commit(BAR_DONE);
+      wait_drain_paged(BAR_DONE, 0, p.spin_limit);
+    }
+  } else {
+    // ---- softmax: thread = key r of the tile, rows c0 .. c0 + HALF ----
+    const int quarter = warp & 3, hf = warp >> 2, r = 32 * quarter + lane, c0 = HALF * hf;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quarter) << 21);       // this warp's 32 lanes
+    const uint32_t half_bar = 2u + hf;
+    constexpr float TAU = FP8 ? TAU_E4M3 : TAU_BF16;
+    const bool holds_o = 32 * quarter < D;                                    // lanes of O^T (D = 64: the lower half)
+    float* nmax = reinterpret_cast<float*>(base + C::NMAX_OFF) + warp * HALF;  // minus the rows' maxima
+    float* fac = reinterpret_cast<float*>(base + C::FAC_OFF) + warp * HALF;
+    long long* row_at = reinterpret_cast<long long*>(base + C::ROWAT_OFF) + warp * HALF;
+    float* red_max = red + hf * 4 * HALF;
+    float* red_sum = red + 8 * HALF + hf * 4 * HALF;
+    bool bad = false;                              // a wait of this warp gave up; it still meets the barriers
+    Segment s;
+    long long x = x0;
+    int it = 0, sslot = 0;
+    uint32_t spar = 0;
+    for (int seg = 0; next_segment(p, pre, x, x1, s); ++seg) {
+      const int buf = seg & 1;
+      const int ctx = *(p.ctx_lens + s.b), ql = p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T, L = ctx + ql;
+      const float* qmul = qmul_sh + buf * NR + c0;
+      const unsigned long long* vis = vis_sh + buf * NR + c0;
+      if (lane < HALF) nmax[lane] = FLT_MAX;
+      __syncwarp();
+      if (!bad && !warp_wait(FULLQ(buf), (seg >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+      float l[HALF];                               // this thread's keys' part of the rows' sums
+#pragma unroll
+      for (int i = 0; i < HALF; ++i) l[i] = 0.f;
+      float vref = 0.f, rv = 0.f;                  // E4M3: power of two at or above the value scales, its reciprocal
+      for (int j = s.t0; j < s.t1; ++j, ++it) {
+        const int key = 128 * j + r;
+        const bool tail = 128 * j + 128 > ctx;     // drafted keys, or the end of the sequence
+        if (!bad && !warp_wait(BAR_S(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+        if (FP8 && !bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
+        float ks = 1.f, vsc = 0.f;
+        bool odd = false;                          // this key's value scale is not finite
+        if constexpr (FP8) {
+          const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF + 1024 * sslot);
+          ks = sc[r];
+          vsc = key < L ? sc[128 + r] : 0.f;
+          odd = !finite_f(vsc);
+        }
+        if (!bad) tc_fence_after();
+        const uint32_t s_at = tl + static_cast<uint32_t>(NR) * (it & 1) + c0;
+        // logits of columns i .. i + M in log2 units, plus `add[]` (with): hidden ones -inf
+        auto logits = [&](int i, auto& y, const float* add) {
+          constexpr int M = sizeof(y) / sizeof(y[0]);
+          uint32_t u[M];
+          if constexpr (M == HALF || M == 8) {
+            if (!bad) {
+              tmem_ld(s_at + i, u);
+              tmem_wait_ld();
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < M; ++k) reg_fence(u[k]);
+          const uint64_t ks2 = f2_pack(ks, ks);
+#pragma unroll
+          for (int k = 0; k < M; k += 4) {
+            const float4 c4 = *reinterpret_cast<const float4*>(qmul + i + k);
+            float4 a4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (add != nullptr) a4 = *reinterpret_cast<const float4*>(add + i + k);
+            uint64_t lo = f2_pack(__uint_as_float(u[k]), __uint_as_float(u[k + 1]));
+            uint64_t hi = f2_pack(__uint_as_float(u[k + 2]), __uint_as_float(u[k + 3]));
+            if constexpr (FP8) {
+              lo = f2_mul(lo, ks2);
+              hi = f2_mul(hi, ks2);
+            }
+            f2_unpack(f2_fma(lo, f2_pack(c4.x, c4.y), f2_pack(a4.x, a4.y)), y[k], y[k + 1]);
+            f2_unpack(f2_fma(hi, f2_pack(c4.z, c4.w), f2_pack(a4.z, a4.w)), y[k + 2], y[k + 3]);
+          }
+          if (tail) {
+            const int rel = key - ctx;
+#pragma unroll
+            for (int k = 0; k < M; ++k)
+              if (rel >= 0 && (rel >= 64 || !((vis[i + k] >> rel) & 1))) y[k] = -INFINITY;
+          }
+        };
+        float y[HALF];
+        logits(0, y, nmax);
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < HALF; i += 2) top = max3(top, y[i], y[i + 1]);
+        const bool any = named_bar_any(half_bar, 128, top > TAU || (FP8 && !odd && vsc > vref));
+        if (any) {
+          // some row's maximum moves (or the scales' bound): the rows' maxima over the tile's keys
+#pragma unroll 1
+          for (int i = 0; i < HALF; i += 8) {
+            float z[8];
+            logits(i, z, nullptr);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t m = __reduce_max_sync(0xffffffffu, ordered(z[k] == z[k] ? z[k] : -INFINITY));
+              if (lane == 0) red_max[quarter * HALF + i + k] = unordered(m);
+            }
+          }
+          if constexpr (FP8) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, odd ? 0u : __float_as_uint(vsc));
+            if (lane == 0) vtop_sh[warp] = m;
+          }
+          named_bar_sync(half_bar, 128);
+          float vfac = 1.f;
+          if constexpr (FP8) {
+            float vt = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) vt = fmaxf(vt, __uint_as_float(vtop_sh[4 * hf + w]));
+            if (vt > vref) {
+              const float nref = __uint_as_float((__float_as_uint(vt) & 0x7f800000u) + (vt < 0x1p126f ? 0x00800000u : 0u));
+              vfac = vref / nref;
+              vref = nref;
+              rv = 1.f / nref;
+            }
+          }
+          if (lane < HALF) {
+            const float old = -nmax[lane];
+            float m = old;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) m = fmaxf(m, red_max[w * HALF + lane]);
+            nmax[lane] = -m;
+            fac[lane] = ex2(old - m);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < HALF; i += 4) {
+            const float4 f4 = *reinterpret_cast<const float4*>(fac + i);
+            l[i] *= f4.x;
+            l[i + 1] *= f4.y;
+            l[i + 2] *= f4.z;
+            l[i + 3] *= f4.w;
+          }
+          if (!bad && j > s.t0) {
+            // O must hold PV(it - 1) complete; PV(it) waits for every warp's arrival below
+            if (!warp_wait(BAR_PV, (it - 1) & 1, ctl, WHERE_PAGED_USE)) {
+              bad = true;
+            } else if (holds_o) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < HALF; i += 8) {
+                uint32_t o[8];
+                tmem_ld(tl + C::O_COL + c0 + i, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  reg_fence(o[k]);
+                  o[k] = __float_as_uint(__uint_as_float(o[k]) * fac[i + k] * vfac);
+                }
+                tmem_st8(tl + C::O_COL + c0 + i, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          logits(0, y, nmax);
+        }
+        // numerators
+        const uint32_t prow = sP + (it & 1) * C::NP * C::P_TERM + r * C::P_ROW;
+        const int swz = C::P_ROW == 128 ? (r & 7) : ((r >> 1) & 3);
+        if constexpr (!FP8) {
+#pragma unroll
+          for (int i = 0; i < HALF; i += 8) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+              const float a = ex2(y[i + k]), b = ex2(y[i + k + 1]);
+              l[i + k] += a;
+              l[i + k + 1] += b;
+              pk[k / 2] = pack_bf16x2(a, b);
+            }
+            st_shared_v4(prow + ((((c0 + i) >> 3) ^ swz) << 4), pk[0], pk[1], pk[2], pk[3]);
+          }
+        } else {
+          const float w = odd ? __int_as_float(0x7fffffff) : vsc * rv * TOP_E4M3;
+          const bool fix = __any_sync(0xffffffffu, odd);       // hidden: 0 whatever the scale; seen and not finite: NaN
+#pragma unroll
+          for (int i = 0; i < HALF; i += 8) {
+            uint32_t t[2][3];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float e[4], f[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                e[k] = ex2(y[i + 4 * h + k]);
+                l[i + 4 * h + k] += e[k];
+                f[k] = e[k] * w;
+              }
+              if (fix) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[k] = e[k] == 0.f ? 0.f : f[k];
+              }
+              e5m2_terms4(f[0], f[1], f[2], f[3], t[h]);
+            }
+            const uint32_t at = prow + ((((c0 + i) >> 4) ^ swz) << 4) + ((c0 + i) & 8);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + k * C::P_TERM), "r"(t[0][k]), "r"(t[1][k]) : "memory");
+          }
+        }
+        if (tail) {
+          // thread = half of key row r of the value tile: what must not meet a zero numerator is taken out
+          if (!bad && !warp_wait(FULLV(it % C::NV), (it / C::NV) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+          if (!bad && key >= ctx) {
+            uint8_t* row = base + C::V_OFF + (it % C::NV) * C::TILE_BYTES + r * C::PANEL_ROW;
+            const bool clear = key >= L || odd;
+            bool hits = false;
+            constexpr int NC = C::ROW_BYTES / 32;
+#pragma unroll 1
+            for (int i = 0; i < NC; ++i) {
+              const int c = hf * NC + i;
+              const int vswz = C::PANEL_ROW == 128 ? (r & 7) : ((r >> 1) & 3);
+              uint4* at = reinterpret_cast<uint4*>(row + (c / (C::PANEL_ROW / 16)) * C::PANEL_BYTES + (((c % (C::PANEL_ROW / 16)) ^ vswz) << 4));
+              if (clear) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              } else if (!FP8) {
+                uint4 u = *at;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+                bool hit = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((w[k] & 0x7f80u) == 0x7f80u) { w[k] &= 0xffff0000u; hit = true; }
+                  if ((w[k] & 0x7f800000u) == 0x7f800000u) { w[k] &= 0xffffu; hit = true; }
+                }
+                if (hit) *at = u;
+                hits = hits || hit;
+              }
+            }
+            if (hits) atomicOr(vodd_sh + (seg & 3), 1ull << (key - ctx));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(BAR_P(it & 1));
+          if (FP8) mbar_arrive(EMPTYS(sslot));
+        }
+        if (FP8 && ++sslot == C::NSC) {
+          sslot = 0;
+          spar ^= 1;
+        }
+      }
+      // ---- end of the segment: the sums over the lanes, then the output ----
+      {
+        const float part = column_sum(l);
+        if (lane < HALF) red_sum[quarter * HALF + lane] = part;
+      }
+      named_bar_sync(1, 256);
+      const unsigned long long vodd = vodd_sh[seg & 3];
+      // last read two segments ago, next written after the next segment's barrier
+      if (threadIdx.x == 0) vodd_sh[(seg + 2) & 3] = 0;
+      const bool whole = s.t0 == 0 && s.t1 == s.n;
+      const long long ws_row = (2ll * group + (s.t0 > 0 ? 0 : 1)) * NR;
+      if (lane < HALF) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sum += red_sum[w * HALF + lane];
+        const int pr = c0 + lane, t = token_of(p, pr);
+        const long long head = static_cast<long long>(s.hkv) * p.G + pr - t * p.G;
+        fac[lane] = sum == 0.f ? 0.f : 1.f / sum;
+        row_at[lane] = t >= ql ? -1 : (whole ? ((static_cast<long long>(s.b) * p.T + t) * p.Hq + head) * D : (ws_row + pr) * D);
+        if (quarter == 0) {
+          const float lse2 = sum == 0.f ? -INFINITY : __log2f(sum) - nmax[lane];
+          if (!whole) p.ws_l[ws_row + pr] = lse2;
+          else if (t < ql && p.lse != nullptr) p.lse[(static_cast<long long>(s.b) * p.Hq + head) * p.T + t] = lse2 * LN2_P;
+        }
+      }
+      __syncwarp();
+      if (!bad && !warp_wait(BAR_O, seg & 1, ctl, WHERE_PAGED_USE)) bad = true;
+      if (!bad && holds_o) {
+        tc_fence_after();
+        const float vmul = FP8 ? vref * (1.f / TOP_E4M3) : 1.f;
+#pragma unroll 1
+        for (int i = 0; i < HALF; i += 8) {
+          uint32_t o[8];
+          tmem_ld(tl + C::O_COL + c0 + i, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            reg_fence(o[k]);
+            float f = __uint_as_float(o[k]) * fac[i + k];
+            if (FP8) f *= vmul;
+            const long long at = row_at[i + k];
+            if (at < 0) continue;
+            if (!FP8 && vodd != 0) {
+              // infinities and NaN of drafted value rows that this row sees
+              for (unsigned long long left = vodd & vis[i + k]; left != 0; left &= left - 1) {
+                const int at_key = ctx + __ffsll(left) - 1;
+                if (at_key < 128 * s.t0 || at_key >= 128 * s.t1) continue;
+                const int page = p.page_table[static_cast<long long>(s.b) * p.max_pages + at_key / p.page_size];
+                if (page < 0 || page >= p.n_pages) continue;
+                const float e = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_cache)[page * p.page_stride +
+                    s.hkv * p.head_stride + (at_key % p.page_size) * p.tok_stride + r]);
+                if (!finite_f(e)) f += e;
+              }
+            }
+            if (whole) static_cast<__nv_bfloat16*>(p.o)[at + r] = __float2bfloat16(f);
+            else p.ws_o[at + r] = f;
+          }
+        }
+      }
+      tc_fence_before();                         // these reads of O before the next P's arrival
+      __syncwarp();
+      if (lane == 0) mbar_arrive(EMPTYQ(buf));
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::COLS);
+  }
+}
+
+template <int D, bool FP8, int NR>
+cudaError_t launch_lanes_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, cudaStream_t st) {
+  using C = LanesCfg<D, FP8, NR>;
+  static std::atomic<unsigned long long> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if ((configured.load() & bit) == 0) {
+    e = cudaFuncSetAttribute(attn_lanes_kernel<D, FP8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  return launch_overlapped(attn_lanes_kernel<D, FP8, NR>, dim3(p.n_cta), LANES_THREADS, C::SMEM_BYTES, st, tk, tv, p);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_lanes_n(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, cudaStream_t st) {
+  const int rb = paged_rows(p.G * p.T);
+  return rb == 16   ? launch_lanes_d<D, FP8, 16>(tk, tv, p, st)
+         : rb == 32 ? launch_lanes_d<D, FP8, 32>(tk, tv, p, st)
+                    : launch_lanes_d<D, FP8, 64>(tk, tv, p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_lanes(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8, cudaStream_t st) {
+  if (D == 64) return fp8 ? launch_lanes_n<64, true>(tk, tv, p, st) : launch_lanes_n<64, false>(tk, tv, p, st);
+  return fp8 ? launch_lanes_n<128, true>(tk, tv, p, st) : launch_lanes_n<128, false>(tk, tv, p, st);
+}
+
+}  // namespace ea46

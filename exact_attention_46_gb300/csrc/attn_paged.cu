@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 // Rows of a merge block of eight warps: one a warp where a unit has 128; few rows a unit: the parts of a row
 // are read by several warps at once.  (Four rows a warp, one after the other: 3 us more on 128 rows.)
 template <int RB>
-constexpr int COMBINE_ROWS = RB == PAGED_TREE_ROWS ? 8 : RB / 8;
+constexpr int COMBINE_ROWS = RB >= 64 ? 8 : RB / 8;
 
 // Merge of the units that several groups share.  A block takes ROWS rows of one row tile of the unit that
 // group i + 1's start cuts first, if it cuts one.
@@ -907,6 +907,13 @@ cudaError_t launch_tree_combine(const PagedParams& p, int D, cudaStream_t st) {
 cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
                               bool combine, cudaStream_t st) {
   if (paged_rows(p.G * p.T) == PAGED_TREE_ROWS) return launch_attn_tree(tk, tv, p, D, fp8, combine, st);
+  if (paged_rows(p.G * p.T) > 8) {
+    const cudaError_t e = launch_attn_lanes(tk, tv, p, D, fp8, st);
+    if (e != cudaSuccess || !combine) return e;
+    const int rb = paged_rows(p.G * p.T);
+    if (D == 64) return rb == 16 ? launch_paged_combine<64, 16>(p, st) : rb == 32 ? launch_paged_combine<64, 32>(p, st) : launch_paged_combine<64, 64>(p, st);
+    return rb == 16 ? launch_paged_combine<128, 16>(p, st) : rb == 32 ? launch_paged_combine<128, 32>(p, st) : launch_paged_combine<128, 64>(p, st);
+  }
   if (D == 64) return fp8 ? launch_paged_m<64, true>(tk, tv, p, combine, st) : launch_paged_m<64, false>(tk, tv, p, combine, st);
   return fp8 ? launch_paged_m<128, true>(tk, tv, p, combine, st) : launch_paged_m<128, false>(tk, tv, p, combine, st);
 }

@@ -91,33 +91,6 @@ constexpr float TAU_BF16 = 8.0f, TAU_E4M3 = 1.0f;
 __device__ __forceinline__ void softmax_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
 __device__ __forceinline__ void other_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
 
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// x (two fp16) as two E4M3 terms: hi = E4M3(x), lo = E4M3(x - hi); the pairs in the low 16 bits.
-__device__ __forceinline__ void e4m3_terms(uint32_t x, uint32_t& hi, uint32_t& lo) {
-  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, d;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 b, h;\n\t"
-      "sub.rn.f16x2 d, %2, b;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\t"
-      "cvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
-      : "=r"(hi), "=r"(lo) : "r"(x));
-}
-
-__device__ __forceinline__ void e4m3_terms4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
-  uint32_t h0, l0, h1, l1;
-  e4m3_terms(f16x2(a, b), h0, l0);
-  e4m3_terms(f16x2(c, d), h1, l1);
-  hi = __byte_perm(h0, h1, 0x5410);
-  lo = __byte_perm(l0, l1, 0x5410);
-}
-
-__device__ __forceinline__ bool finite_f(float x) { return fabsf(x) < INFINITY; }
-
 template <int D, bool FP8>
 __global__ void __launch_bounds__(TREE_THREADS, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -193,6 +166,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{p.spin_limit, abort_flag, p.err_word, p.err_info};
+  const TileRings rings{sK, sV, base_u32 + C::SC_OFF, FULLK(0), EMPTYK(0), FULLV(0), EMPTYV(0), FULLS(0), EMPTYS(0)};
 
   if constexpr (FP8) {
     if (warp >= MMA_WARP) other_registers();
@@ -200,88 +174,11 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
   }
 
   if (warp >= K_WARP) {
-    // ---- loads: K, V, E4M3 scales, a warp each.  Box i of a segment's list of boxes is br rows of
-    // one page; lane i % 32 looks its page up, one batch of 32 boxes ahead, and issues its copies ----
-    if (FP8 || warp < S_WARP) {
-      const bool is_k = warp == K_WARP, is_s = warp == S_WARP;
-      const CUtensorMap* tm = is_k ? &tmK : &tmV;
-      const int ps_log = 31 - __clz(p.page_size), br_log = ps_log < 7 ? ps_log : 7;
-      const int pt_log = 7 - br_log, per_tile = 1 << pt_log, batch = 32 >> pt_log;
-      const int stages = is_s ? C::NSC : (is_k ? C::NK : C::NV);
-      const uint64_t pol = p.row_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-      int it = 0, slot = 0;
-      uint32_t par = 1;
-      bool dead = false;                           // a wait gave up (the same in every lane)
-      Segment s;
-      for (int rt = rt0; rt < p.row_tiles && !dead; rt += p.group_ctas)
-        for (long long x = x0; !dead && next_segment(p, pre, x, x1, s);) {
-          const int L = *(p.ctx_lens + s.b) + (p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
-          const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
-          auto look_up = [&](int j) {
-            const int at = (128 * j + (lane << br_log)) >> ps_log;
-            return j < s.t1 && at < p.max_pages ? *(table + at) : -1;
-          };
-          int next = look_up(s.t0);
-          for (int j0 = s.t0; j0 < s.t1 && !dead; j0 += batch) {
-            const int page = next;
-            next = look_up(j0 + batch);
-            const int key = 128 * j0 + (lane << br_log);
-            const bool wanted = key < L && j0 + (lane >> pt_log) < s.t1;
-            const bool good = wanted && page >= 0 && page < p.n_pages;
-            if (is_k && wanted && !good && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_PAGE);
-            const unsigned boxes = __ballot_sync(0xffffffffu, good);
-            const int row = key & (p.page_size - 1);
-            for (int i = 0; i < batch && j0 + i < s.t1; ++i, ++it) {
-              dead = !warp_wait(is_s ? EMPTYS(slot) : (is_k ? EMPTYK(slot) : EMPTYV(slot)), par, ctl, WHERE_PAGED_LOAD);
-              if (dead) break;
-              if (!is_s) {
-                const uint32_t full = is_k ? FULLK(slot) : FULLV(slot);
-                const uint32_t dst = (is_k ? sK : sV) + slot * C::TILE_BYTES;
-                const unsigned mine = (boxes >> (i << pt_log)) & ((1u << per_tile) - 1);
-                if (lane == 0) mbar_arrive_expect_tx(full, (__popc(mine) << br_log) * C::ROW_BYTES);
-                __syncwarp();
-                const int box = lane & (per_tile - 1);
-                if ((lane >> pt_log) == i && ((mine >> box) & 1)) {
-#pragma unroll
-                  for (int pn = 0; pn < C::NPANEL; ++pn)
-                    tma_load_4d(dst + pn * C::PANEL_BYTES + (box << br_log) * C::PANEL_ROW, tm, full,
-                                pn * (C::PANEL_ROW / C::ESZ), row, s.hkv, page, pol);
-                }
-              } else if constexpr (FP8) {
-                // lane: the scales of four keys of the tile
-                const uint32_t dst = base_u32 + C::SC_OFF + 1024 * slot + 16 * lane;
-                const int src = (i << pt_log) + (lane >> (br_log - 2));
-                const int pg = __shfl_sync(0xffffffffu, page, src);
-                const int r0 = __shfl_sync(0xffffffffu, row, src) + ((4 * lane) & ((1 << br_log) - 1));
-                if ((boxes >> src) & 1) {
-                  const long long e = (static_cast<long long>(pg) * p.Hkv + s.hkv) * p.page_size + r0;
-                  cp_async16(dst, p.k_scale + e);
-                  cp_async16(dst + 512, p.v_scale + e);
-                }
-                cp_async_arrive(FULLS(slot));
-              }
-              if (++slot == stages) {
-                slot = 0;
-                par ^= 1;
-              }
-            }
-          }
-        }
-      if (is_k && rt0 == 0 && lane == 0) write_cut(p, pre, group, W, N);
-      if (dead) {
-        cp_async_wait_all();
-        if (lane == 0 && !is_s) {
-          // this warp's copies in flight: the slots issued last
-          const int n = it < stages ? it : stages;
-          for (int i = 0; i < n; ++i)
-            wait_drain_paged(is_k ? FULLK((it - 1 - i) % stages) : FULLV((it - 1 - i) % stages), ((it - 1 - i) / stages) & 1,
-                             p.spin_limit);
-        }
-      }
-    }
+    if (FP8 || warp < S_WARP) load_tiles<C>(p, pre, tmK, tmV, rings, warp - K_WARP, rt0, x0, x1, ctl);
+    if (warp == K_WARP && rt0 == 0 && lane == 0) write_cut(p, pre, group, W, N);
   } else if (warp == MMA_WARP) {
     // ---- MMA issue ----
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t dq = smem_desc(sQ, 16, C::SBO, C::LAYOUT);
       const uint64_t dk0 = smem_desc(sK, 16, C::SBO, C::LAYOUT);
       const uint64_t dv0 = smem_desc(sV, C::PANEL_BYTES, C::SBO, C::LAYOUT);

@@ -107,7 +107,9 @@ constexpr int PAGED_MAX_DRAFT = 64;
 
 // Query rows per work unit for R = G * T packed rows.
 constexpr int PAGED_TREE_ROWS = 128;
-constexpr int paged_rows(int R) { return R <= 8 ? 8 : (R <= 16 ? 16 : (R <= 32 ? 32 : PAGED_TREE_ROWS)); }
+constexpr int paged_rows(int R) {
+  return R <= 8 ? 8 : (R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : PAGED_TREE_ROWS)));
+}
 
 // List entries (128-key tiles) that a change of units is taken to cost.  Measured with 0, 2, 3, 4 and 6: trees
 // of 8 over long e4m3 contexts 92.2, 90.3, 89.4, 88.3, 87.8 us, trees of 32 bf16 50.0, 49.1, 48.3, 47.8, 47.5,
@@ -122,6 +124,8 @@ cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, cons
 
 cudaError_t launch_attn_tree(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
                              bool combine, cudaStream_t st);
+cudaError_t launch_attn_lanes(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
+                              cudaStream_t st);
 cudaError_t launch_tree_combine(const PagedParams& p, int D, cudaStream_t st);
 
 // Launch a kernel that may become resident while the one before it on the stream ends; it waits for that

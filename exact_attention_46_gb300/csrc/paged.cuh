@@ -10,6 +10,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda_bf16.h>
 
 #include "cache.h"
 #include "ptx.cuh"
@@ -185,6 +186,150 @@ __device__ __forceinline__ void write_cut(const PagedParams& p, const int* pre, 
       c = make_int4(static_cast<int>(c1 - c0) + 1, s.b, s.hkv, p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
   }
   p.cuts[i] = c;
+}
+
+// ---- E4M3 terms ----
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// x (two fp16) as two E4M3 terms: hi = E4M3(x), lo = E4M3(x - hi); the pairs in the low 16 bits.
+__device__ __forceinline__ void e4m3_terms(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 b, d;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 b, h;\n\t"
+      "sub.rn.f16x2 d, %2, b;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\t"
+      "cvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n\t}"
+      : "=r"(hi), "=r"(lo) : "r"(x));
+}
+
+__device__ __forceinline__ void e4m3_terms4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+  uint32_t h0, l0, h1, l1;
+  e4m3_terms(f16x2(a, b), h0, l0);
+  e4m3_terms(f16x2(c, d), h1, l1);
+  hi = __byte_perm(h0, h1, 0x5410);
+  lo = __byte_perm(l0, l1, 0x5410);
+}
+
+__device__ __forceinline__ bool finite_f(float x) { return fabsf(x) < INFINITY; }
+
+// ---- issue and loads of the kernels on tcgen05 ----
+
+// One lane of a converged warp.  The branch on it tells the compiler that one thread issues: 16 MMAs in
+// a branch on lane == 0 take 738 cycles to issue, in a branch on this 424.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// D (+)= A B with shared-memory descriptors whose upper halves are constants of the kernel.
+template <bool FP8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (FP8)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+                 "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n\t}\n"
+                 ::"r"(d), "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+                 "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}\n"
+                 ::"r"(d), "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Shared memory and barriers of the rings of K tiles, V tiles and (E4M3) 128 key and 128 value scales.
+struct TileRings {
+  uint32_t k, v, sc;
+  uint32_t full_k, empty_k, full_v, empty_v, full_s, empty_s;
+};
+
+// One warp loads the K tiles (what = 0), the V tiles (1) or the scales (2) of list entries [x0, x1).  C: the
+// kernel's configuration.  Box i of a segment's list of boxes is br rows of one page; lane i % 32 looks its page
+// up, one batch of 32 boxes ahead, and issues its copies.
+template <class C>
+__device__ __forceinline__ void load_tiles(const PagedParams& p, const int* pre, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                           const TileRings& g, int what, int rt0, long long x0, long long x1,
+                                           const WaitCtl& ctl) {
+  const int lane = static_cast<int>(lane_id());
+  const bool is_k = what == 0, is_s = what == 2;
+  const CUtensorMap* tm = is_k ? &tmK : &tmV;
+  const uint32_t data = is_k ? g.k : g.v;
+  const uint32_t fulls = is_s ? g.full_s : (is_k ? g.full_k : g.full_v), empties = is_s ? g.empty_s : (is_k ? g.empty_k : g.empty_v);
+  const int ps_log = 31 - __clz(p.page_size), br_log = ps_log < 7 ? ps_log : 7;
+  const int pt_log = 7 - br_log, per_tile = 1 << pt_log, batch = 32 >> pt_log;
+  const int stages = is_s ? C::NSC : (is_k ? C::NK : C::NV);
+  const uint64_t pol = p.row_tiles > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+  int it = 0, slot = 0;
+  uint32_t par = 1;
+  bool dead = false;                           // a wait gave up (the same in every lane)
+  Segment s;
+  for (int rt = rt0; rt < p.row_tiles && !dead; rt += p.group_ctas)
+    for (long long x = x0; !dead && next_segment(p, pre, x, x1, s);) {
+      const int L = *(p.ctx_lens + s.b) + (p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
+      const int* table = p.page_table + static_cast<long long>(s.b) * p.max_pages;
+      auto look_up = [&](int j) {
+        const int at = (128 * j + (lane << br_log)) >> ps_log;
+        return j < s.t1 && at < p.max_pages ? *(table + at) : -1;
+      };
+      int next = look_up(s.t0);
+      for (int j0 = s.t0; j0 < s.t1 && !dead; j0 += batch) {
+        const int page = next;
+        next = look_up(j0 + batch);
+        const int key = 128 * j0 + (lane << br_log);
+        const bool wanted = key < L && j0 + (lane >> pt_log) < s.t1;
+        const bool good = wanted && page >= 0 && page < p.n_pages;
+        if (is_k && wanted && !good && atomicCAS(p.err_word, 0, 1) == 0) atomicExch(p.err_info, WHERE_PAGED_PAGE);
+        const unsigned boxes = __ballot_sync(0xffffffffu, good);
+        const int row = key & (p.page_size - 1);
+        for (int i = 0; i < batch && j0 + i < s.t1; ++i, ++it) {
+          dead = !warp_wait(empties + 8u * slot, par, ctl, WHERE_PAGED_LOAD);
+          if (dead) break;
+          const uint32_t full = fulls + 8u * slot;
+          if (!is_s) {
+            const uint32_t dst = data + slot * C::TILE_BYTES;
+            const unsigned mine = (boxes >> (i << pt_log)) & ((1u << per_tile) - 1);
+            if (lane == 0) mbar_arrive_expect_tx(full, (__popc(mine) << br_log) * C::ROW_BYTES);
+            __syncwarp();
+            const int box = lane & (per_tile - 1);
+            if ((lane >> pt_log) == i && ((mine >> box) & 1)) {
+#pragma unroll
+              for (int pn = 0; pn < C::NPANEL; ++pn)
+                tma_load_4d(dst + pn * C::PANEL_BYTES + (box << br_log) * C::PANEL_ROW, tm, full,
+                            pn * (C::PANEL_ROW / C::ESZ), row, s.hkv, page, pol);
+            }
+          } else {
+            // lane: the scales of four keys of the tile
+            const uint32_t dst = g.sc + 1024 * slot + 16 * lane;
+            const int src = (i << pt_log) + (lane >> (br_log - 2));
+            const int pg = __shfl_sync(0xffffffffu, page, src);
+            const int r0 = __shfl_sync(0xffffffffu, row, src) + ((4 * lane) & ((1 << br_log) - 1));
+            if ((boxes >> src) & 1) {
+              const long long e = (static_cast<long long>(pg) * p.Hkv + s.hkv) * p.page_size + r0;
+              cp_async16(dst, p.k_scale + e);
+              cp_async16(dst + 512, p.v_scale + e);
+            }
+            cp_async_arrive(full);
+          }
+          if (++slot == stages) {
+            slot = 0;
+            par ^= 1;
+          }
+        }
+      }
+    }
+  if (dead) {
+    cp_async_wait_all();
+    if (lane == 0 && !is_s) {
+      // this warp's copies in flight: the slots issued last
+      const int n = it < stages ? it : stages;
+      for (int i = 0; i < n; ++i)
+        wait_drain_paged(fulls + 8u * ((it - 1 - i) % stages), ((it - 1 - i) / stages) & 1, p.spin_limit);
+    }
+  }
 }
 
 }  // namespace ea46

@@ -10,7 +10,7 @@ roundings: with X = max_j scale sum_d |q_d k_jd| over the seen keys and A = sum_
 * the output rounds to bf16: 2^-8 of it.
 So |err| <= 2^-8 |o| + (r + 2 dx + 2^-18) A (+ L 2^-26 448 max scale), r = 2^-8 or 2^-11, and
 |lse err| <= dx + 2^-18 (1 + |lse|).
-Over an E4M3 cache with more than 32 rows (group x drafts) the products run on E4M3 terms:
+Over an E4M3 cache with more than 8 rows (group x drafts) the products run on E4M3 terms:
 * a query row, scaled so that its largest element lies in [128, 256), is the sum of two terms.  An
   element of eight significant bits leaves a remainder of four after the first term, which the
   second holds exactly unless it lies below E4M3's smallest step 2^-9: that is off by at most half
@@ -103,7 +103,7 @@ class Problem:
     def check(self, o, lse, scale=None):
         scale = 1 / np.sqrt(self.D) if scale is None else scale
         o, lse = to64(o), to64(lse)
-        terms = self.fp8 and self.T * self.Hq // self.Hkv > 32
+        terms = self.fp8 and self.T * self.Hq // self.Hkv > 8
         r = 2.0 ** -8 + 2.0 ** -11 if terms else (2.0 ** -11 if self.fp8 else 2.0 ** -8)
         for b in range(self.B):
             n = self.ql[b]
