@@ -7,15 +7,17 @@
 //     O^T += V^T P^T   [D x NR]             V and the numerators with the long side contiguous
 // so no product is spent on rows that are not there, a softmax thread holds one key (its scales, its place
 // in the tree are one scalar each) and the cache's E4M3 codes go to the tensor core unconverted.
-//   * warps 0..7 softmax: thread = key r, half hf of the rows.  Its numerators go to shared memory as one
-//     row of P (two tiles of terms for E4M3), its sums stay in registers until the unit ends.  The maxima of
-//     the rows run over threads, and moving them is rare: the four warps of a half vote once per tile
-//     whether any logit passed its row's maximum by 2^TAU, and only then reduce them over the lanes;
-//   * warp 8 issues the MMAs, one S ahead of PV and across units; 9 to 11 load K, V and scales
+//   * warps 0..7 softmax, in two groups that take every other tile: a tile's way through the softmax is
+//     mostly waiting (for S, the vote, the copies into shared memory to be seen), so two are under way at once.
+//     A group has maxima, sums and O of its own; the unit's end adds the two up.  Thread = key: its numerators go
+//     to shared memory as one row of P (three tiles of terms for E4M3), its sums stay in registers.  The maxima
+//     of the rows run over threads, and moving them is rare: a group votes once per tile whether any
+//     logit passed its row's maximum by 2^TAU, and only then reduces them over the lanes;
+//   * warp 8 issues the MMAs, S up to three tiles ahead of PV and across units; 9 to 11 load K, V and scales
 //     (load_tiles); 12..15 bring the next unit's queries, a buffer ahead;
 //   * O^T's lanes are the columns of an output row, so the epilogue's stores cover rows as they are.
-// E4M3: queries and numerators are two E4M3 terms each (attn_tree.cu has the arithmetic); a thread multiplies
-// its numerators by its value's scale over vref, a power of two at or above the scales so far.
+// E4M3: queries are two E4M3 terms (attn_tree.cu has the arithmetic), numerators three E5M2 terms; a thread
+// multiplies its numerators by its value's scale over vref, a power of two at or above the scales so far.
 // Hidden keys, value rows past the end and drafted values that are not finite: as in attn_tree.cu.
 // Every mbarrier wait is bounded.
 #include <atomic>
@@ -41,7 +43,6 @@ struct LanesCfg {
   static constexpr int TILE_BYTES = 128 * ROW_BYTES;
   static constexpr int NQ = FP8 ? 2 : 1;                       // terms of queries
   static constexpr int NP = FP8 ? 3 : 1;                       // terms of numerators
-  static constexpr int HALF = NR / 2;                          // rows of a softmax warp
   static constexpr int Q_TERM = NR * ROW_BYTES;
   static constexpr int P_ROW = NR * ESZ > 64 ? 128 : 64;       // bytes of a key's row of P, swizzled as wide
   static constexpr int P_TERM = 128 * P_ROW;
@@ -56,10 +57,10 @@ struct LanesCfg {
   // half multiplies whatever lies behind the panel in shared memory, and its lanes are never read.
   static constexpr uint32_t IDESC_PV = instr_desc(FMT, 1, 128, NR) | (1u << 15) | (FP8 ? 1u << 10 : 0u);
   static_assert(!FP8 || FMT == 0, "bits 7 and 10: formats of A (E4M3) and B (E5M2)");
-  // Tensor Memory: two S buffers, O
-  static constexpr uint32_t O_COL = 2 * NR, COLS = NR == 64 ? 256 : (NR == 32 ? 128 : 64);
+  // Tensor Memory: four S buffers, O of either group
+  static constexpr uint32_t O_COL = 4 * NR, COLS = NR == 64 ? 512 : (NR == 32 ? 256 : 128);
   // shared memory from the end of what the K and V rings leave
-  static constexpr int SMALL = 1024 * NSC + (PAGED_MAX_BATCH + 4) * 4 + 4 * 8 * HALF * 4 + 8 * HALF * 8 + 2 * NR * 12 + 128 + 1024;
+  static constexpr int SMALL = 1024 * NSC + (PAGED_MAX_BATCH + 4) * 4 + 8 * NR * 16 + 8 * NR * 8 + 2 * NR * 12 + 1024;
   static constexpr int ROOM = (227 * 1024 - 1024 - SMALL - 2 * (NP * P_TERM + NQ * Q_TERM)) / TILE_BYTES;
   static constexpr int NK = ROOM >= 16 ? 8 : (ROOM + 1) / 2, NV = ROOM >= 16 ? 8 : ROOM / 2;
   static constexpr int V_OFF = NK * TILE_BYTES;
@@ -67,15 +68,15 @@ struct LanesCfg {
   static constexpr int Q_OFF = P_OFF + 2 * NP * P_TERM;         // [2][NQ]
   static constexpr int SC_OFF = Q_OFF + 2 * NQ * Q_TERM;
   static constexpr int VIS_OFF = SC_OFF + NSC * 1024;           // [2][NR] u64: drafted keys a row sees
-  static constexpr int ROWAT_OFF = VIS_OFF + 2 * NR * 8;        // [8 warps][HALF] i64
-  static constexpr int QMUL_OFF = ROWAT_OFF + 8 * HALF * 8;     // [2][NR] floats: softmax scale of a row's codes
-  static constexpr int NMAX_OFF = QMUL_OFF + 2 * NR * 4;        // [8 warps][HALF] minus the running maxima
-  static constexpr int FAC_OFF = NMAX_OFF + 8 * HALF * 4;       // [8 warps][HALF]
-  static constexpr int RED_OFF = FAC_OFF + 8 * HALF * 4;        // [2 halves][4 quarters][HALF]: maxima, then sums
-  static constexpr int PRE_OFF = RED_OFF + 2 * 8 * HALF * 4;
-  static constexpr int FLAG_OFF = PRE_OFF + (PAGED_MAX_BATCH + 4) * 4;   // vodd [4] x 8, vtop [8], tmem, abort, scratch [16]
-  static constexpr int BAR_OFF = FLAG_OFF + 32 + 32 + 8 + 64;
-  static constexpr int NBAR = 11 + 2 * (NK + NV + NSC);
+  static constexpr int ROWAT_OFF = VIS_OFF + 2 * NR * 8;        // [8 warps][NR / 2] i64: where an output row begins
+  static constexpr int QMUL_OFF = ROWAT_OFF + 8 * NR * 4;       // [2][NR] floats: softmax scale of a row's codes
+  static constexpr int NMAX_OFF = QMUL_OFF + 2 * NR * 4;        // [8 warps][NR] minus the running maxima
+  static constexpr int FAC_OFF = NMAX_OFF + 8 * NR * 4;         // [8 warps][NR]
+  static constexpr int RED_OFF = FAC_OFF + 8 * NR * 4;          // [2][2 groups][4 quarters][NR]: maxima, sums
+  static constexpr int PRE_OFF = RED_OFF + 2 * 8 * NR * 4;
+  static constexpr int FLAG_OFF = PRE_OFF + (PAGED_MAX_BATCH + 4) * 4;   // vodd [4] x 8, vtop [8], vmul [2], tmem, abort, scratch [16]
+  static constexpr int BAR_OFF = FLAG_OFF + 32 + 32 + 8 + 8 + 64;
+  static constexpr int NBAR = 14 + 2 * (NK + NV + NSC);
   static constexpr int SMEM_BYTES = 1024 + BAR_OFF + NBAR * 8;
   static_assert(VIS_OFF % 16 == 0 && QMUL_OFF % 16 == 0 && NMAX_OFF % 16 == 0 && FLAG_OFF % 8 == 0 && BAR_OFF % 8 == 0, "alignment");
   static_assert(Q_OFF % 1024 == 0 && Q_TERM % 1024 == 0, "swizzle atoms");
@@ -105,10 +106,9 @@ __device__ __forceinline__ void e5m2_terms4(float a, float b, float c, float d, 
       : "=r"(t[0]), "=r"(t[1]), "=r"(t[2]) : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 
-// Registers of a warpgroup for NR = 64, out of the block's: 512 threads x 128 = 256 x 168 + 256 x 88.  Its
-// softmax spills 416 bytes (E4M3: 480) in 128.
-__device__ __forceinline__ void softmax_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 168;"); }
-__device__ __forceinline__ void other_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+// Registers of a warpgroup, out of the block's: 512 threads x 128 = 256 x 176 + 256 x 80.
+__device__ __forceinline__ void softmax_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 176;"); }
+__device__ __forceinline__ void other_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
 
 // N columns of this warp's 32 lanes of Tensor Memory.
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[8]) {
@@ -130,32 +130,22 @@ __device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t n, bool mine
   return any != 0;
 }
 
-// Floats as unsigned integers in the same order (no NaN).
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t u) {
-  return __uint_as_float((u >> 31) ? u ^ 0x80000000u : ~u);
-}
-
-// Sum over the warp's lanes of column lane % N.
-template <int N>
-__device__ __forceinline__ float column_sum(const float (&x)[N]) {
+// Over the warp's lanes, of column lane % N: N - 1 exchanges for the first log2 N steps of all columns at once
+// (32 warp-wide reductions instead of the maxima of 32 columns took 3.5 us on a unit's first tile).
+template <bool MAX, int N>
+__device__ __forceinline__ float column_reduce(float (&v)[N]) {
   const uint32_t lane = lane_id();
-  float v[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = x[i];
+  auto both = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
 #pragma unroll
   for (int o = N / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const bool up = (lane & o) != 0;
       const float other = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + o], o);
-      v[i] = (up ? v[i + o] : v[i]) + other;
+      v[i] = both(up ? v[i + o] : v[i], other);
     }
 #pragma unroll
-  for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  for (int o = N; o < 32; o <<= 1) v[0] = both(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
   return v[0];
 }
 
@@ -164,7 +154,6 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
     attn_lanes_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const PagedParams p) {
   using C = LanesCfg<D, FP8, NR>;
-  constexpr int HALF = C::HALF;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
@@ -176,30 +165,32 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
   int* pre = reinterpret_cast<int*>(base + C::PRE_OFF);
   unsigned long long* vodd_sh = reinterpret_cast<unsigned long long*>(base + C::FLAG_OFF);   // [4]
   uint32_t* vtop_sh = reinterpret_cast<uint32_t*>(base + C::FLAG_OFF + 32);                  // [8 warps]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::FLAG_OFF + 64);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::FLAG_OFF + 68);
-  int* scratch = reinterpret_cast<int*>(base + C::FLAG_OFF + 72);                            // [16]
+  float* vmul_sh = reinterpret_cast<float*>(base + C::FLAG_OFF + 64);                        // [2 groups]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::FLAG_OFF + 72);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::FLAG_OFF + 76);
+  int* scratch = reinterpret_cast<int*>(base + C::FLAG_OFF + 80);                            // [16]
   const uint32_t bar0 = base_u32 + C::BAR_OFF;
-  const uint32_t BAR_O = bar0, BAR_PV = bar0 + 8, BAR_DONE = bar0 + 16;
-  auto BAR_S = [&](int b) { return bar0 + 24 + 8u * b; };
-  auto BAR_P = [&](int b) { return bar0 + 40 + 8u * b; };
-  auto FULLQ = [&](int b) { return bar0 + 56 + 8u * b; };
-  auto EMPTYQ = [&](int b) { return bar0 + 72 + 8u * b; };
-  auto FULLK = [&](int s) { return bar0 + 88 + 8u * s; };
-  auto EMPTYK = [&](int s) { return bar0 + 88 + 8u * (C::NK + s); };
-  auto FULLV = [&](int s) { return bar0 + 88 + 8u * (2 * C::NK + s); };
-  auto EMPTYV = [&](int s) { return bar0 + 88 + 8u * (2 * C::NK + C::NV + s); };
-  auto FULLS = [&](int s) { return bar0 + 88 + 8u * (2 * (C::NK + C::NV) + s); };
-  auto EMPTYS = [&](int s) { return bar0 + 88 + 8u * (2 * (C::NK + C::NV) + C::NSC + s); };
+  const uint32_t BAR_O = bar0, BAR_DONE = bar0 + 8;
+  auto BAR_PV = [&](int g) { return bar0 + 16 + 8u * g; };
+  auto BAR_P = [&](int g) { return bar0 + 32 + 8u * g; };
+  auto FULLQ = [&](int b) { return bar0 + 48 + 8u * b; };
+  auto EMPTYQ = [&](int b) { return bar0 + 64 + 8u * b; };
+  auto BAR_S = [&](int b) { return bar0 + 80 + 8u * b; };                                    // [4]
+  auto FULLK = [&](int s) { return bar0 + 112 + 8u * s; };
+  auto EMPTYK = [&](int s) { return bar0 + 112 + 8u * (C::NK + s); };
+  auto FULLV = [&](int s) { return bar0 + 112 + 8u * (2 * C::NK + s); };
+  auto EMPTYV = [&](int s) { return bar0 + 112 + 8u * (2 * C::NK + C::NV + s); };
+  auto FULLS = [&](int s) { return bar0 + 112 + 8u * (2 * (C::NK + C::NV) + s); };
+  auto EMPTYS = [&](int s) { return bar0 + 112 + 8u * (2 * (C::NK + C::NV) + C::NSC + s); };
 
   const int warp = static_cast<int>(warp_id()), lane = static_cast<int>(lane_id());
   if (threadIdx.x == 0) {
     mbar_init(BAR_O, 1);
-    mbar_init(BAR_PV, 1);
     mbar_init(BAR_DONE, 1);
+    for (int b = 0; b < 4; ++b) mbar_init(BAR_S(b), 1);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(BAR_S(b), 1);
-      mbar_init(BAR_P(b), 8);
+      mbar_init(BAR_PV(b), 1);
+      mbar_init(BAR_P(b), 4);
       mbar_init(FULLQ(b), 4);
       mbar_init(EMPTYQ(b), 1 + 8);
     }
@@ -213,7 +204,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
     }
     for (int s = 0; s < C::NSC; ++s) {
       mbar_init(FULLS(s), 32);
-      mbar_init(EMPTYS(s), 8);
+      mbar_init(EMPTYS(s), 4);
     }
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) vodd_sh[i] = 0;
@@ -243,7 +234,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
   const WaitCtl ctl{p.spin_limit, abort_flag, p.err_word, p.err_info};
   const TileRings rings{sK, sV, base_u32 + C::SC_OFF, FULLK(0), EMPTYK(0), FULLV(0), EMPTYV(0), FULLS(0), EMPTYS(0)};
 
-  if constexpr (NR == 64) {
+  if constexpr (NR >= 32) {
     if (warp >= MMA_WARP) other_registers();
     else softmax_registers();
   }
@@ -345,127 +336,148 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
       const uint64_t dp0 = smem_desc(sP, C::P_TERM, C::P_SBO, C::P_LAYOUT);
       const uint32_t hk = static_cast<uint32_t>(dk0 >> 32), hq = static_cast<uint32_t>(dq0 >> 32);
       const uint32_t hv = static_cast<uint32_t>(dv0 >> 32), hp = static_cast<uint32_t>(dp0 >> 32);
+      // S of up to three tiles ahead of PV, whichever can go: S(i) overwrites S(i - 4), which the softmax read
+      // before it handed over P(i - 4)
       Segment s;
       long long x = x0;
-      int left = 0, seg = -1, ki = 0;            // of the tiles that S was issued for
-      uint32_t first = 0, last = 0;              // bit ki & 1: first, last tile of its segment
-      // S of the next tile; 0: there is none, -1: a wait gave up
-      auto qk = [&]() -> int {
-        const uint32_t bit = 1u << (ki & 1);
-        first &= ~bit;
-        last &= ~bit;
-        if (left == 0) {
-          if (!next_segment(p, pre, x, x1, s)) return 0;
-          left = s.t1 - s.t0;
-          ++seg;
-          first |= bit;
-          if (!wait_bounded(FULLQ(seg & 1), (seg >> 1) & 1, ctl, WHERE_PAGED_MMA)) return -1;
-        }
-        const int ks = ki % C::NK;
-        if (!wait_bounded(FULLK(ks), (ki / C::NK) & 1, ctl, WHERE_PAGED_MMA)) return -1;
-        tc_fence_after();
-        const uint32_t ak = static_cast<uint32_t>(dk0) + ((ks * C::TILE_BYTES) >> 4);
-        const uint32_t bq = static_cast<uint32_t>(dq0) + (((seg & 1) * C::NQ * C::Q_TERM) >> 4);
-        const uint32_t d = tmem + static_cast<uint32_t>(NR) * (ki & 1);
+      bool more = next_segment(p, pre, x, x1, s);
+      int tile = 0, seg = 0;                     // next tile of S: its place in segment `seg`
+      int qi = 0, pi = 0;                        // tiles of S and PV issued
+      int ks = 0, vs = 0;                        // ring positions
+      uint32_t kpar = 0, vpar = 0, fresh = 0, last = 0;        // bit i & 3: first tile of its group, last of its segment
+      long long t0 = clock64();
+      while (more || pi < qi) {
+        bool moved = false;
+        if (pi < qi && mbar_test(BAR_P(pi & 1), (pi >> 1) & 1) && mbar_test(FULLV(vs), vpar)) {
+          tc_fence_after();
+          const uint32_t av = static_cast<uint32_t>(dv0) + ((vs * C::TILE_BYTES) >> 4);
+          const uint32_t bp = static_cast<uint32_t>(dp0) + (((pi & 1) * C::NP * C::P_TERM) >> 4);
+          const uint32_t d = tmem + C::O_COL + NR * (pi & 1);
+          const uint32_t acc0 = ((fresh >> (pi & 3)) & 1) ^ 1;
 #pragma unroll
-        for (int term = 0; term < C::NQ; ++term)
+          for (int term = 0; term < C::NP; ++term)
 #pragma unroll
-          for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
-            const uint32_t in = (kk % C::STEPS_PER_PANEL) * 32, pn = kk / C::STEPS_PER_PANEL;
-            const uint32_t a = ak + ((pn * C::PANEL_BYTES + in) >> 4);
-            const uint32_t b = bq + ((term * C::Q_TERM + pn * (NR * C::PANEL_ROW) + in) >> 4);
-            mma_ss<FP8>(d, a, hk, b, hq, C::IDESC_QK, (kk > 0 || term > 0) ? 1u : 0u);
+            for (int kk = 0; kk < C::KSTEPS_PV; ++kk)
+              mma_ss<FP8>(d, av + ((kk * C::UMMA_K * C::PANEL_ROW) >> 4), hv,
+                          bp + ((term * C::P_TERM + kk * C::UMMA_K * C::P_ROW) >> 4), hp, C::IDESC_PV,
+                          kk > 0 || term > 0 ? 1u : acc0);
+          mma_commit(BAR_PV(pi & 1));
+          mma_commit(EMPTYV(vs));
+          if ((last >> (pi & 3)) & 1) mma_commit(BAR_O);
+          if (++vs == C::NV) {
+            vs = 0;
+            vpar ^= 1;
           }
-        mma_commit(BAR_S(ki & 1));
-        mma_commit(EMPTYK(ks));
-        if (--left == 0) {
-          mma_commit(EMPTYQ(seg & 1));
-          last |= bit;
+          ++pi;
+          moved = true;
         }
-        ++ki;
-        return 1;
-      };
-      int more = qk();
-      for (int it = 0; more > 0; ++it) {
-        // S(it + 1) overwrites S(it - 1), which the softmax read before it handed over P(it - 1)
-        const bool is_first = (first >> (it & 1)) & 1, is_last = (last >> (it & 1)) & 1;
-        more = qk();
-        if (more < 0) break;
-        if (!wait_bounded(BAR_P(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_MMA)) break;
-        const int vs = it % C::NV;
-        if (!wait_bounded(FULLV(vs), (it / C::NV) & 1, ctl, WHERE_PAGED_MMA)) break;
-        tc_fence_after();
-        const uint32_t av = static_cast<uint32_t>(dv0) + ((vs * C::TILE_BYTES) >> 4);
-        const uint32_t bp = static_cast<uint32_t>(dp0) + (((it & 1) * C::NP * C::P_TERM) >> 4);
+        if (more && qi - pi < 4 && (tile > 0 || mbar_test(FULLQ(seg & 1), (seg >> 1) & 1)) && mbar_test(FULLK(ks), kpar)) {
+          tc_fence_after();
+          const uint32_t ak = static_cast<uint32_t>(dk0) + ((ks * C::TILE_BYTES) >> 4);
+          const uint32_t bq = static_cast<uint32_t>(dq0) + (((seg & 1) * C::NQ * C::Q_TERM) >> 4);
+          const uint32_t d = tmem + NR * (qi & 3);
 #pragma unroll
-        for (int term = 0; term < C::NP; ++term)
+          for (int term = 0; term < C::NQ; ++term)
 #pragma unroll
-          for (int kk = 0; kk < C::KSTEPS_PV; ++kk) {
-            const uint32_t a = av + ((kk * C::UMMA_K * C::PANEL_ROW) >> 4);
-            const uint32_t b = bp + ((term * C::P_TERM + kk * C::UMMA_K * C::P_ROW) >> 4);
-            const uint32_t acc = (!is_first || kk > 0 || term > 0) ? 1u : 0u;
-            mma_ss<FP8>(tmem + C::O_COL, a, hv, b, hp, C::IDESC_PV, acc);
+            for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
+              const uint32_t in = (kk % C::STEPS_PER_PANEL) * 32, pn = kk / C::STEPS_PER_PANEL;
+              mma_ss<FP8>(d, ak + ((pn * C::PANEL_BYTES + in) >> 4), hk,
+                          bq + ((term * C::Q_TERM + pn * (NR * C::PANEL_ROW) + in) >> 4), hq, C::IDESC_QK,
+                          (kk > 0 || term > 0) ? 1u : 0u);
+            }
+          mma_commit(BAR_S(qi & 3));
+          mma_commit(EMPTYK(ks));
+          const uint32_t bit = 1u << (qi & 3);
+          fresh = tile < 2 ? fresh | bit : fresh & ~bit;
+          last &= ~bit;
+          if (++tile == s.t1 - s.t0) {
+            last |= bit;
+            mma_commit(EMPTYQ(seg & 1));
+            more = next_segment(p, pre, x, x1, s);
+            tile = 0;
+            ++seg;
           }
-        mma_commit(BAR_PV);
-        mma_commit(EMPTYV(vs));
-        if (is_last) mma_commit(BAR_O);
+          if (++ks == C::NK) {
+            ks = 0;
+            kpar ^= 1;
+          }
+          ++qi;
+          moved = true;
+        }
+        if (moved) {
+          t0 = clock64();
+        } else {
+          if (*abort_flag) break;
+          if (clock64() - t0 > p.spin_limit) {
+            *abort_flag = 1;
+            if (atomicCAS(p.err_word, 0, 4 /* ATTN_ERR_TIMEOUT */) == 0) atomicExch(p.err_info, WHERE_PAGED_MMA);
+            break;
+          }
+        }
       }
       mma_commit(BAR_DONE);
       wait_drain_paged(BAR_DONE, 0, p.spin_limit);
     }
   } else {
-    // ---- softmax: thread = key r of the tile, rows c0 .. c0 + HALF ----
-    const int quarter = warp & 3, hf = warp >> 2, r = 32 * quarter + lane, c0 = HALF * hf;
+    // ---- softmax: group g takes every other tile, with maxima, sums and O of its own; thread = key r ----
+    const int quarter = warp & 3, g = warp >> 2, r = 32 * quarter + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter) << 21);       // this warp's 32 lanes
-    const uint32_t half_bar = 2u + hf;
+    const uint32_t o_at = tl + C::O_COL + NR * g, group_bar = 2u + g;
     constexpr float TAU = FP8 ? TAU_E4M3 : TAU_BF16;
+    constexpr int CH = 16;                                     // columns in registers at a time
     const bool holds_o = 32 * quarter < D;                                    // lanes of O^T (D = 64: the lower half)
-    float* nmax = reinterpret_cast<float*>(base + C::NMAX_OFF) + warp * HALF;  // minus the rows' maxima
-    float* fac = reinterpret_cast<float*>(base + C::FAC_OFF) + warp * HALF;
-    long long* row_at = reinterpret_cast<long long*>(base + C::ROWAT_OFF) + warp * HALF;
-    float* red_max = red + hf * 4 * HALF;
-    float* red_sum = red + 8 * HALF + hf * 4 * HALF;
+    float* nmax0 = reinterpret_cast<float*>(base + C::NMAX_OFF);
+    float* nmax = nmax0 + warp * NR;                                          // minus the rows' maxima
+    float* fac = reinterpret_cast<float*>(base + C::FAC_OFF) + warp * NR;
+    long long* row_at = reinterpret_cast<long long*>(base + C::ROWAT_OFF) + warp * (NR / 2);
+    float* red_max = red + g * 4 * NR;
+    float* red_sum = red + 8 * NR;
+    const uint32_t prow = sP + g * C::NP * C::P_TERM + r * C::P_ROW;
+    const int swz = C::P_ROW == 128 ? (r & 7) : ((r >> 1) & 3);
     bool bad = false;                              // a wait of this warp gave up; it still meets the barriers
     Segment s;
     long long x = x0;
-    int it = 0, sslot = 0;
+    int it = 0, done = 0;                          // tiles before the segment; this group's tiles so far
+    int sslot = g;
     uint32_t spar = 0;
     for (int seg = 0; next_segment(p, pre, x, x1, s); ++seg) {
       const int buf = seg & 1;
       const int ctx = *(p.ctx_lens + s.b), ql = p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T, L = ctx + ql;
-      const float* qmul = qmul_sh + buf * NR + c0;
-      const unsigned long long* vis = vis_sh + buf * NR + c0;
-      if (lane < HALF) nmax[lane] = FLT_MAX;
+      const float* qmul = qmul_sh + buf * NR;
+      const unsigned long long* vis = vis_sh + buf * NR;
+#pragma unroll
+      for (int i = 0; i < NR; i += 32)
+        if (i + lane < NR) nmax[i + lane] = FLT_MAX;
       __syncwarp();
       if (!bad && !warp_wait(FULLQ(buf), (seg >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
-      float l[HALF];                               // this thread's keys' part of the rows' sums
+      uint64_t l[NR / 2];                          // this thread's keys' part of the rows' sums, in pairs
 #pragma unroll
-      for (int i = 0; i < HALF; ++i) l[i] = 0.f;
+      for (int i = 0; i < NR / 2; ++i) l[i] = 0;
       float vref = 0.f, rv = 0.f;                  // E4M3: power of two at or above the value scales, its reciprocal
-      for (int j = s.t0; j < s.t1; ++j, ++it) {
+      const int first = s.t0 + ((g ^ it) & 1);
+      for (int j = first; j < s.t1; j += 2) {
+        const int at = it + j - s.t0;              // place among the CTA's tiles
         const int key = 128 * j + r;
         const bool tail = 128 * j + 128 > ctx;     // drafted keys, or the end of the sequence
-        if (!bad && !warp_wait(BAR_S(it & 1), (it >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
-        if (FP8 && !bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
         float ks = 1.f, vsc = 0.f;
         bool odd = false;                          // this key's value scale is not finite
         if constexpr (FP8) {
+          if (!bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
           const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF + 1024 * sslot);
           ks = sc[r];
           vsc = key < L ? sc[128 + r] : 0.f;
           odd = !finite_f(vsc);
         }
+        if (!bad && !warp_wait(BAR_S(at & 3), (at >> 2) & 1, ctl, WHERE_PAGED_USE)) bad = true;
         if (!bad) tc_fence_after();
-        const uint32_t s_at = tl + static_cast<uint32_t>(NR) * (it & 1) + c0;
-        // logits of columns i .. i + M in log2 units, plus `add[]` (with): hidden ones -inf
+        const uint32_t s_at = tl + NR * (at & 3);
+        // logits of columns i .. in log2 units plus add[]: hidden ones -inf
         auto logits = [&](int i, auto& y, const float* add) {
           constexpr int M = sizeof(y) / sizeof(y[0]);
           uint32_t u[M];
-          if constexpr (M == HALF || M == 8) {
-            if (!bad) {
-              tmem_ld(s_at + i, u);
-              tmem_wait_ld();
-            }
+          if (!bad) {
+            tmem_ld(s_at + i, u);
+            tmem_wait_ld();
           }
 #pragma unroll
           for (int k = 0; k < M; ++k) reg_fence(u[k]);
@@ -491,34 +503,39 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
               if (rel >= 0 && (rel >= 64 || !((vis[i + k] >> rel) & 1))) y[k] = -INFINITY;
           }
         };
-        float y[HALF];
-        logits(0, y, nmax);
+        float y[CH];
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < HALF; i += 2) top = max3(top, y[i], y[i + 1]);
-        const bool any = named_bar_any(half_bar, 128, top > TAU || (FP8 && !odd && vsc > vref));
+        for (int c = 0; c < NR; c += CH) {
+          logits(c, y, nmax);
+#pragma unroll
+          for (int i = 0; i < CH; i += 2) top = max3(top, y[i], y[i + 1]);
+        }
+        const bool any = named_bar_any(group_bar, 128, top > TAU || (FP8 && !odd && vsc > vref));
+        // P's buffer and O hold PV of this group's tile before
+        if (done > 0 && !bad) {
+          if (!warp_wait(BAR_PV(g), (done - 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+          else tc_fence_after();
+        }
         if (any) {
           // some row's maximum moves (or the scales' bound): the rows' maxima over the tile's keys
 #pragma unroll 1
-          for (int i = 0; i < HALF; i += 8) {
-            float z[8];
+          for (int i = 0; i < NR; i += 16) {
+            float z[16];
             logits(i, z, nullptr);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t m = __reduce_max_sync(0xffffffffu, ordered(z[k] == z[k] ? z[k] : -INFINITY));
-              if (lane == 0) red_max[quarter * HALF + i + k] = unordered(m);
-            }
+            const float m = column_reduce<true>(z);            // (a NaN counts for nothing)
+            if (lane < 16) red_max[quarter * NR + i + lane] = m;
           }
           if constexpr (FP8) {
             const uint32_t m = __reduce_max_sync(0xffffffffu, odd ? 0u : __float_as_uint(vsc));
             if (lane == 0) vtop_sh[warp] = m;
           }
-          named_bar_sync(half_bar, 128);
+          named_bar_sync(group_bar, 128);
           float vfac = 1.f;
           if constexpr (FP8) {
             float vt = 0.f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) vt = fmaxf(vt, __uint_as_float(vtop_sh[4 * hf + w]));
+            for (int w = 0; w < 4; ++w) vt = fmaxf(vt, __uint_as_float(vtop_sh[4 * g + w]));
             if (vt > vref) {
               const float nref = __uint_as_float((__float_as_uint(vt) & 0x7f800000u) + (vt < 0x1p126f ? 0x00800000u : 0u));
               vfac = vref / nref;
@@ -526,114 +543,111 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
               rv = 1.f / nref;
             }
           }
-          if (lane < HALF) {
-            const float old = -nmax[lane];
-            float m = old;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) m = fmaxf(m, red_max[w * HALF + lane]);
-            nmax[lane] = -m;
-            fac[lane] = ex2(old - m);
-          }
+          for (int i = 0; i < NR; i += 32)
+            if (i + lane < NR) {
+              const float old = -nmax[i + lane];
+              float m = old;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) m = fmaxf(m, red_max[w * NR + i + lane]);
+              nmax[i + lane] = -m;
+              fac[i + lane] = ex2(old - m);
+            }
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < HALF; i += 4) {
+          for (int i = 0; i < NR; i += 4) {
             const float4 f4 = *reinterpret_cast<const float4*>(fac + i);
-            l[i] *= f4.x;
-            l[i + 1] *= f4.y;
-            l[i + 2] *= f4.z;
-            l[i + 3] *= f4.w;
+            l[i / 2] = f2_mul(l[i / 2], f2_pack(f4.x, f4.y));
+            l[i / 2 + 1] = f2_mul(l[i / 2 + 1], f2_pack(f4.z, f4.w));
           }
-          if (!bad && j > s.t0) {
-            // O must hold PV(it - 1) complete; PV(it) waits for every warp's arrival below
-            if (!warp_wait(BAR_PV, (it - 1) & 1, ctl, WHERE_PAGED_USE)) {
-              bad = true;
-            } else if (holds_o) {
-              tc_fence_after();
+          if (!bad && j > first && holds_o) {
 #pragma unroll 1
-              for (int i = 0; i < HALF; i += 8) {
-                uint32_t o[8];
-                tmem_ld(tl + C::O_COL + c0 + i, o);
-                tmem_wait_ld();
+            for (int i = 0; i < NR; i += 8) {
+              uint32_t o[8];
+              tmem_ld(o_at + i, o);
+              tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  reg_fence(o[k]);
-                  o[k] = __float_as_uint(__uint_as_float(o[k]) * fac[i + k] * vfac);
-                }
-                tmem_st8(tl + C::O_COL + c0 + i, o);
+              for (int k = 0; k < 8; ++k) {
+                reg_fence(o[k]);
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * fac[i + k] * vfac);
               }
-              tmem_wait_st();
+              tmem_st8(o_at + i, o);
             }
+            tmem_wait_st();
           }
-          logits(0, y, nmax);
+          if (NR == CH) logits(0, y, nmax);
         }
         // numerators
-        const uint32_t prow = sP + (it & 1) * C::NP * C::P_TERM + r * C::P_ROW;
-        const int swz = C::P_ROW == 128 ? (r & 7) : ((r >> 1) & 3);
-        if constexpr (!FP8) {
+        const float w = odd ? __int_as_float(0x7fffffff) : vsc * rv * TOP_E4M3;
+        const bool fix = FP8 && __any_sync(0xffffffffu, odd);    // hidden: 0 whatever the scale; seen and not finite: NaN
 #pragma unroll
-          for (int i = 0; i < HALF; i += 8) {
-            uint32_t pk[4];
+        for (int c = 0; c < NR; c += CH) {
+          if (NR > CH) logits(c, y, nmax);
+          if constexpr (!FP8) {
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-              const float a = ex2(y[i + k]), b = ex2(y[i + k + 1]);
-              l[i + k] += a;
-              l[i + k + 1] += b;
-              pk[k / 2] = pack_bf16x2(a, b);
-            }
-            st_shared_v4(prow + ((((c0 + i) >> 3) ^ swz) << 4), pk[0], pk[1], pk[2], pk[3]);
-          }
-        } else {
-          const float w = odd ? __int_as_float(0x7fffffff) : vsc * rv * TOP_E4M3;
-          const bool fix = __any_sync(0xffffffffu, odd);       // hidden: 0 whatever the scale; seen and not finite: NaN
+            for (int i = 0; i < CH; i += 8) {
+              uint32_t pk[4];
 #pragma unroll
-          for (int i = 0; i < HALF; i += 8) {
-            uint32_t t[2][3];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float e[4], f[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                e[k] = ex2(y[i + 4 * h + k]);
-                l[i + 4 * h + k] += e[k];
-                f[k] = e[k] * w;
+              for (int k = 0; k < 8; k += 2) {
+                const float a = ex2(y[i + k]), b = ex2(y[i + k + 1]);
+                l[(c + i + k) / 2] = f2_add(l[(c + i + k) / 2], f2_pack(a, b));
+                pk[k / 2] = pack_bf16x2(a, b);
               }
-              if (fix) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) f[k] = e[k] == 0.f ? 0.f : f[k];
-              }
-              e5m2_terms4(f[0], f[1], f[2], f[3], t[h]);
+              st_shared_v4(prow + ((((c + i) >> 3) ^ swz) << 4), pk[0], pk[1], pk[2], pk[3]);
             }
-            const uint32_t at = prow + ((((c0 + i) >> 4) ^ swz) << 4) + ((c0 + i) & 8);
+          } else {
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + k * C::P_TERM), "r"(t[0][k]), "r"(t[1][k]) : "memory");
+            for (int i = 0; i < CH; i += 16) {
+              uint32_t tt[4][3];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                float e[4], f[4];
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                  e[k] = ex2(y[i + 4 * h + k]);
+                  e[k + 1] = ex2(y[i + 4 * h + k + 1]);
+                  const uint64_t e2 = f2_pack(e[k], e[k + 1]);
+                  uint64_t& lc = l[(c + i + 4 * h + k) / 2];
+                  lc = f2_add(lc, e2);
+                  f2_unpack(f2_mul(e2, f2_pack(w, w)), f[k], f[k + 1]);
+                }
+                if (fix) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) f[k] = e[k] == 0.f ? 0.f : f[k];
+                }
+                e5m2_terms4(f[0], f[1], f[2], f[3], tt[h]);
+              }
+              const uint32_t dst = prow + ((((c + i) >> 4) ^ swz) << 4);
+#pragma unroll
+              for (int k = 0; k < 3; ++k) st_shared_v4(dst + k * C::P_TERM, tt[0][k], tt[1][k], tt[2][k], tt[3][k]);
+            }
           }
         }
         if (tail) {
-          // thread = half of key row r of the value tile: what must not meet a zero numerator is taken out
-          if (!bad && !warp_wait(FULLV(it % C::NV), (it / C::NV) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+          // thread = key row r of the value tile: what must not meet a zero numerator is taken out.  (PV of the tile
+          // two before is complete, so the slot's phase before this one is too.)
+          if (!bad && !warp_wait(FULLV(at % C::NV), (at / C::NV) & 1, ctl, WHERE_PAGED_USE)) bad = true;
           if (!bad && key >= ctx) {
-            uint8_t* row = base + C::V_OFF + (it % C::NV) * C::TILE_BYTES + r * C::PANEL_ROW;
+            uint8_t* row = base + C::V_OFF + (at % C::NV) * C::TILE_BYTES + r * C::PANEL_ROW;
             const bool clear = key >= L || odd;
             bool hits = false;
-            constexpr int NC = C::ROW_BYTES / 32;
+            constexpr int PC = C::PANEL_ROW / 16;
+            const int vswz = C::PANEL_ROW == 128 ? (r & 7) : ((r >> 1) & 3);
 #pragma unroll 1
-            for (int i = 0; i < NC; ++i) {
-              const int c = hf * NC + i;
-              const int vswz = C::PANEL_ROW == 128 ? (r & 7) : ((r >> 1) & 3);
-              uint4* at = reinterpret_cast<uint4*>(row + (c / (C::PANEL_ROW / 16)) * C::PANEL_BYTES + (((c % (C::PANEL_ROW / 16)) ^ vswz) << 4));
+            for (int i = 0; i < C::ROW_BYTES / 16; ++i) {
+              uint4* v = reinterpret_cast<uint4*>(row + (i / PC) * C::PANEL_BYTES + (((i % PC) ^ vswz) << 4));
               if (clear) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
+                *v = make_uint4(0u, 0u, 0u, 0u);
               } else if (!FP8) {
-                uint4 u = *at;
-                uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+                uint4 u = *v;
+                uint32_t* q = reinterpret_cast<uint32_t*>(&u);
                 bool hit = false;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  if ((w[k] & 0x7f80u) == 0x7f80u) { w[k] &= 0xffff0000u; hit = true; }
-                  if ((w[k] & 0x7f800000u) == 0x7f800000u) { w[k] &= 0xffffu; hit = true; }
+                  if ((q[k] & 0x7f80u) == 0x7f80u) { q[k] &= 0xffff0000u; hit = true; }
+                  if ((q[k] & 0x7f800000u) == 0x7f800000u) { q[k] &= 0xffffu; hit = true; }
                 }
-                if (hit) *at = u;
+                if (hit) *v = u;
                 hits = hits || hit;
               }
             }
@@ -644,35 +658,55 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(BAR_P(it & 1));
+          mbar_arrive(BAR_P(g));
           if (FP8) mbar_arrive(EMPTYS(sslot));
         }
-        if (FP8 && ++sslot == C::NSC) {
-          sslot = 0;
-          spar ^= 1;
+        ++done;
+        if constexpr (FP8) {
+          sslot += 2;
+          if (sslot >= C::NSC) {
+            sslot -= C::NSC;
+            spar ^= 1;
+          }
         }
       }
-      // ---- end of the segment: the sums over the lanes, then the output ----
-      {
-        const float part = column_sum(l);
-        if (lane < HALF) red_sum[quarter * HALF + lane] = part;
+      // ---- end of the segment: the sums over the lanes and the groups, then the output; group g's warps take
+      // columns c0 .. c0 + NR / 2 of both groups' O ----
+#pragma unroll
+      for (int c = 0; c < NR; c += CH) {
+        float part[CH];
+#pragma unroll
+        for (int i = 0; i < CH; i += 2) f2_unpack(l[(c + i) / 2], part[i], part[i + 1]);
+        const float sum = column_reduce<false>(part);
+        if (lane < CH) red_sum[(4 * g + quarter) * NR + c + lane] = sum;
       }
+      if (FP8 && lane == 0 && quarter == 0) vmul_sh[g] = vref * (1.f / TOP_E4M3);
+      const int n = s.t1 - s.t0;
+      const bool has0 = n > 1 || (it & 1) == 0, has1 = n > 1 || (it & 1) == 1;        // groups with tiles in the segment
+      it += n;
       named_bar_sync(1, 256);
       const unsigned long long vodd = vodd_sh[seg & 3];
       // last read two segments ago, next written after the next segment's barrier
       if (threadIdx.x == 0) vodd_sh[(seg + 2) & 3] = 0;
       const bool whole = s.t0 == 0 && s.t1 == s.n;
       const long long ws_row = (2ll * group + (s.t0 > 0 ? 0 : 1)) * NR;
+      constexpr int HALF = NR / 2;
+      const int c0 = HALF * g;
       if (lane < HALF) {
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sum += red_sum[w * HALF + lane];
         const int pr = c0 + lane, t = token_of(p, pr);
+        float sums[2] = {0.f, 0.f}, f[2];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sums[k >> 2] += red_sum[k * NR + pr];
+        const float m0 = -nmax0[pr], m1 = -nmax0[4 * NR + pr], m = fmaxf(m0, m1);
+        f[0] = ex2(m0 - m);
+        f[1] = ex2(m1 - m);
+        const float sum = sums[0] * f[0] + sums[1] * f[1], inv = sum == 0.f ? 0.f : 1.f / sum;
+        fac[lane] = f[0] * inv;
+        fac[HALF + lane] = f[1] * inv;
         const long long head = static_cast<long long>(s.hkv) * p.G + pr - t * p.G;
-        fac[lane] = sum == 0.f ? 0.f : 1.f / sum;
         row_at[lane] = t >= ql ? -1 : (whole ? ((static_cast<long long>(s.b) * p.T + t) * p.Hq + head) * D : (ws_row + pr) * D);
         if (quarter == 0) {
-          const float lse2 = sum == 0.f ? -INFINITY : __log2f(sum) - nmax[lane];
+          const float lse2 = sum == 0.f ? -INFINITY : __log2f(sum) + m;
           if (!whole) p.ws_l[ws_row + pr] = lse2;
           else if (t < ql && p.lse != nullptr) p.lse[(static_cast<long long>(s.b) * p.Hq + head) * p.T + t] = lse2 * LN2_P;
         }
@@ -681,22 +715,24 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
       if (!bad && !warp_wait(BAR_O, seg & 1, ctl, WHERE_PAGED_USE)) bad = true;
       if (!bad && holds_o) {
         tc_fence_after();
-        const float vmul = FP8 ? vref * (1.f / TOP_E4M3) : 1.f;
+        const float v0 = FP8 ? vmul_sh[0] : 1.f, v1 = FP8 ? vmul_sh[1] : 1.f;
 #pragma unroll 1
         for (int i = 0; i < HALF; i += 8) {
-          uint32_t o[8];
-          tmem_ld(tl + C::O_COL + c0 + i, o);
+          uint32_t a[8], b[8];
+          tmem_ld(tl + C::O_COL + c0 + i, a);
+          tmem_ld(tl + C::O_COL + NR + c0 + i, b);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            reg_fence(o[k]);
-            float f = __uint_as_float(o[k]) * fac[i + k];
-            if (FP8) f *= vmul;
-            const long long at = row_at[i + k];
-            if (at < 0) continue;
+            reg_fence(a[k]);
+            reg_fence(b[k]);
+            // a group without tiles left nothing of this segment in its O
+            float f = (has0 ? __uint_as_float(a[k]) * fac[i + k] * v0 : 0.f) + (has1 ? __uint_as_float(b[k]) * fac[HALF + i + k] * v1 : 0.f);
+            const long long to = row_at[i + k];
+            if (to < 0) continue;
             if (!FP8 && vodd != 0) {
               // infinities and NaN of drafted value rows that this row sees
-              for (unsigned long long left = vodd & vis[i + k]; left != 0; left &= left - 1) {
+              for (unsigned long long left = vodd & vis[c0 + i + k]; left != 0; left &= left - 1) {
                 const int at_key = ctx + __ffsll(left) - 1;
                 if (at_key < 128 * s.t0 || at_key >= 128 * s.t1) continue;
                 const int page = p.page_table[static_cast<long long>(s.b) * p.max_pages + at_key / p.page_size];
@@ -706,13 +742,13 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
                 if (!finite_f(e)) f += e;
               }
             }
-            if (whole) static_cast<__nv_bfloat16*>(p.o)[at + r] = __float2bfloat16(f);
-            else p.ws_o[at + r] = f;
+            if (whole) static_cast<__nv_bfloat16*>(p.o)[to + r] = __float2bfloat16(f);
+            else p.ws_o[to + r] = f;
           }
         }
       }
-      tc_fence_before();                         // these reads of O before the next P's arrival
-      __syncwarp();
+      tc_fence_before();                         // all reads of O before the next P's arrival
+      named_bar_sync(1, 256);
       if (lane == 0) mbar_arrive(EMPTYQ(buf));
     }
   }

@@ -219,6 +219,14 @@ __device__ __forceinline__ bool finite_f(float x) { return fabsf(x) < INFINITY; 
 
 // ---- issue and loads of the kernels on tcgen05 ----
 
+// Whether the phase with this parity has completed.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done != 0;
+}
+
 // One lane of a converged warp.  The branch on it tells the compiler that one thread issues: 16 MMAs in
 // a branch on lane == 0 take 738 cycles to issue, in a branch on this 424.
 __device__ __forceinline__ bool elect_one() {
