@@ -106,9 +106,18 @@ __device__ __forceinline__ void e5m2_terms4(float a, float b, float c, float d, 
       : "=r"(t[0]), "=r"(t[1]), "=r"(t[2]) : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 
-// Registers of a warpgroup, out of the block's: 512 threads x 128 = 256 x 176 + 256 x 80.
-__device__ __forceinline__ void softmax_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 176;"); }
-__device__ __forceinline__ void other_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+// Registers of a warpgroup for 32 and 64 rows, out of the block's: 512 threads x 128 = 256 x 176 + 256 x 80 =
+// 256 x 184 + 256 x 72, what neither side spills in.
+template <int NR>
+__device__ __forceinline__ void softmax_registers() {
+  if constexpr (NR == 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+  if constexpr (NR == 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+}
+template <int NR>
+__device__ __forceinline__ void other_registers() {
+  if constexpr (NR == 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if constexpr (NR == 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+}
 
 // N columns of this warp's 32 lanes of Tensor Memory.
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[8]) {
@@ -234,10 +243,8 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
   const WaitCtl ctl{p.spin_limit, abort_flag, p.err_word, p.err_info};
   const TileRings rings{sK, sV, base_u32 + C::SC_OFF, FULLK(0), EMPTYK(0), FULLV(0), EMPTYV(0), FULLS(0), EMPTYS(0)};
 
-  if constexpr (NR >= 32) {
-    if (warp >= MMA_WARP) other_registers();
-    else softmax_registers();
-  }
+  if (warp >= MMA_WARP) other_registers<NR>();
+  else softmax_registers<NR>();
 
   if (warp >= Q_WARP) {
     // ---- queries: a warp every fourth row, lane = D / 32 elements ----
@@ -249,15 +256,15 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
       const int buf = seg & 1;
       if (!warp_wait(EMPTYQ(buf), ((seg >> 1) & 1) ^ 1, ctl, WHERE_PAGED_LOAD)) break;
       const int ql = p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T;
-      if (w < NR / 32 || (NR < 32 && w == 0 && lane < NR)) {
-        const int r = 32 * w + lane, t = token_of(p, r);
-        unsigned long long bits = 0;
+      // the drafted keys that row mr sees (the load is under way with the queries')
+      const int mr = 32 * w + lane;
+      const bool masks = mr < NR;
+      unsigned long long bits = 0;
+      if (masks) {
+        const int t = token_of(p, mr);
         if (t < p.T)
           bits = p.tree_mask != nullptr ? *(p.tree_mask + static_cast<long long>(s.b) * p.T + t)
                                         : (t >= 63 ? ~0ull : (2ull << t) - 1);
-        if (ql < 64) bits &= (1ull << ql) - 1;
-        vis_sh[buf * NR + r] = bits;
-        if (!FP8) qmul_sh[buf * NR + r] = p.c_log2;
       }
 #pragma unroll 1
       for (int i0 = 0; i0 < ROWS; i0 += BATCH) {
@@ -319,6 +326,11 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
                                                    : p.c_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
           }
         }
+      }
+      if (masks) {
+        if (ql < 64) bits &= (1ull << ql) - 1;
+        vis_sh[buf * NR + mr] = bits;
+        if (!FP8) qmul_sh[buf * NR + mr] = p.c_log2;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -424,7 +436,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter) << 21);       // this warp's 32 lanes
     const uint32_t o_at = tl + C::O_COL + NR * g, group_bar = 2u + g;
     constexpr float TAU = FP8 ? TAU_E4M3 : TAU_BF16;
-    constexpr int CH = 16;                                     // columns in registers at a time
+    constexpr int CH = NR == 64 ? 16 : NR;                                     // columns in registers at a time
     const bool holds_o = 32 * quarter < D;                                    // lanes of O^T (D = 64: the lower half)
     float* nmax0 = reinterpret_cast<float*>(base + C::NMAX_OFF);
     float* nmax = nmax0 + warp * NR;                                          // minus the rows' maxima
@@ -461,14 +473,17 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
         const bool tail = 128 * j + 128 > ctx;     // drafted keys, or the end of the sequence
         float ks = 1.f, vsc = 0.f;
         bool odd = false;                          // this key's value scale is not finite
+        const bool ready = mbar_test(BAR_S(at & 3), (at >> 2) & 1) && (!FP8 || mbar_test(FULLS(sslot), spar));
+        if (!__all_sync(0xffffffffu, ready) && !bad) {
+          if (!warp_wait(BAR_S(at & 3), (at >> 2) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+          if (FP8 && !bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
+        }
         if constexpr (FP8) {
-          if (!bad && !warp_wait(FULLS(sslot), spar, ctl, WHERE_PAGED_USE)) bad = true;
           const float* sc = reinterpret_cast<const float*>(base + C::SC_OFF + 1024 * sslot);
           ks = sc[r];
           vsc = key < L ? sc[128 + r] : 0.f;
           odd = !finite_f(vsc);
         }
-        if (!bad && !warp_wait(BAR_S(at & 3), (at >> 2) & 1, ctl, WHERE_PAGED_USE)) bad = true;
         if (!bad) tc_fence_after();
         const uint32_t s_at = tl + NR * (at & 3);
         // logits of columns i .. in log2 units plus add[]: hidden ones -inf
@@ -514,7 +529,8 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
         const bool any = named_bar_any(group_bar, 128, top > TAU || (FP8 && !odd && vsc > vref));
         // P's buffer and O hold PV of this group's tile before
         if (done > 0 && !bad) {
-          if (!warp_wait(BAR_PV(g), (done - 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+          if (!__all_sync(0xffffffffu, mbar_test(BAR_PV(g), (done - 1) & 1)) &&
+              !warp_wait(BAR_PV(g), (done - 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
           else tc_fence_after();
         }
         if (any) {

@@ -776,17 +776,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-// Rows of a merge block of eight warps: one a warp where a unit has 128; few rows a unit: the parts of a row
-// are read by several warps at once.  (Four rows a warp, one after the other: 3 us more on 128 rows.)
+// Rows of a merge block of eight warps where a unit has many parts: one a warp where a unit has 64 rows or more; few
+// rows a unit: the parts of a row are read by several warps at once.  (Four rows a warp, one after the other:
+// 3 us more on 128 rows.)
 template <int RB>
 constexpr int COMBINE_ROWS = RB >= 64 ? 8 : RB / 8;
 
-// Merge of the units that several groups share.  A block takes ROWS rows of one row tile of the unit that
-// group i + 1's start cuts first, if it cuts one.
+// Merge of the units that several groups share.  A block takes rows of one row tile of the unit that group
+// i + 1's start cuts first, if it cuts one.
 template <int D, int RB>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p) {
-  constexpr int NW = 8, E = D / 32, ROWS = COMBINE_ROWS<RB>;
-  constexpr int SHARE = NW / ROWS;
+  constexpr int NW = 8, E = D / 32, SHARE = NW / COMBINE_ROWS<RB>;
   constexpr int BATCH = SHARE == 1 ? 4 : 8;                     // parts of a row in flight
   __shared__ float part[NW][D + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -795,11 +795,14 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
   grid_dependency_wait();       // in every block: this grid's end stands for the key kernel's too
   const int4 cut = ld_l2(p.cuts + c0 + 1);
   const int n = cut.x;                                          // parts: groups c0 .. c0 + n - 1
-  const int first = ROWS * blockIdx.y, rows = cut.w * p.G - rt * RB - first;
+  // warps of a row.  16 and 32 rows of few parts take half the blocks, which then are on the device at once:
+  // 1.2 and 1.9 us less over 128 units; 8 rows want all the warps.
+  const int share = SHARE > 1 && SHARE < 8 && n <= 4 ? SHARE / 2 : SHARE;
+  const int first = (NW / share) * blockIdx.y, rows = min(RB, cut.w * p.G - rt * RB) - first;
   if (n == 0 || rows <= 0) return;
   // c0's part is its last unit's (slot 1), the others' their first's (slot 0)
   auto slot = [&](int c) { return 2ll * ((c0 + c) * static_cast<long long>(p.row_tiles) + rt) + (c == 0 ? 1 : 0); };
-  const int r = first + warp / SHARE, sub = warp % SHARE;
+  const int r = first + warp / share, sub = warp % share;
   const bool live = r - first < rows;
   float mx = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
@@ -816,12 +819,12 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
   };
   if (live) {
     // lane: columns E lane ..
-    for (int cb = sub; cb < n; cb += BATCH * SHARE) {
+    for (int cb = sub; cb < n; cb += BATCH * share) {
       float l[BATCH], v[BATCH][E];
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
         // past the last part: that part again, not added (no branch between the loads)
-        const int c = cb + k * SHARE < n ? cb + k * SHARE : n - 1;
+        const int c = cb + k * share < n ? cb + k * share : n - 1;
         l[k] = ld_l2(p.ws_l + slot(c) * RB + r);
         const float* src = p.ws_o + (slot(c) * RB + r) * D + lane * E;
         if constexpr (E == 4) {
@@ -834,12 +837,12 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
       }
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
-        if (cb + k * SHARE >= n) break;
+        if (cb + k * share >= n) break;
         add(l[k], l[k] == -INFINITY ? 0.f : 1.f, v[k]);
       }
     }
   }
-  if (SHARE > 1) {
+  if (share > 1) {
     if (live) {
 #pragma unroll
       for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
@@ -850,7 +853,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
     }
     __syncthreads();
     if (live && sub == 0)
-      for (int w = 1; w < SHARE; ++w) add(part[warp + w][D], part[warp + w][D + 1], &part[warp + w][lane * E]);
+      for (int w = 1; w < share; ++w) add(part[warp + w][D], part[warp + w][D + 1], &part[warp + w][lane * E]);
   }
   if (live && sub == 0) {
     const int pr = rt * RB + r, t = token_of(p, pr);
