@@ -7,12 +7,13 @@
 //     O^T += V^T P^T   [D x NR]             V and the numerators with the long side contiguous
 // so no product is spent on rows that are not there, a softmax thread holds one key (its scales, its place
 // in the tree are one scalar each) and the cache's E4M3 codes go to the tensor core unconverted.
-//   * warps 0..7 softmax, in two groups that take every other tile: a tile's way through the softmax is
-//     mostly waiting (for S, the vote, the copies into shared memory to be seen), so two are under way at once.
-//     A group has maxima, sums and O of its own; the unit's end adds the two up.  Thread = key: its numerators go
-//     to shared memory as one row of P (three tiles of terms for E4M3), its sums stay in registers.  The maxima
-//     of the rows run over threads, and moving them is rare: a group votes once per tile whether any
-//     logit passed its row's maximum by 2^TAU, and only then reduces them over the lanes;
+//   * warps 0..7 softmax, in two teams.  A tile's way through the softmax is mostly waiting (for S, the vote, the
+//     copies into shared memory to be seen), so with 16 and 32 rows the teams take every other tile, each with maxima,
+//     sums and O of its own that the unit's end adds up; with 64 rows, whose arithmetic takes longer than the loads,
+//     each has half of the rows.  Thread = key: its numerators go to shared memory as one row of P (three tiles of
+//     terms for E4M3), its sums stay in registers.  The maxima of the rows run over threads, and moving them is rare:
+//     a team votes once per tile whether any logit passed its row's maximum by 2^TAU, and only then reduces
+//     them over the lanes;
 //   * warp 8 issues the MMAs, S up to three tiles ahead of PV and across units; 9 to 11 load K, V and scales
 //     (load_tiles); 12..15 bring the next unit's queries, a buffer ahead;
 //   * O^T's lanes are the columns of an output row, so the epilogue's stores cover rows as they are.
@@ -43,6 +44,9 @@ struct LanesCfg {
   static constexpr int TILE_BYTES = 128 * ROW_BYTES;
   static constexpr int NQ = FP8 ? 2 : 1;                       // terms of queries
   static constexpr int NP = FP8 ? 3 : 1;                       // terms of numerators
+  // 16 and 32 rows: two teams of four warps take every other tile; 64: each the half of the rows of every tile
+  static constexpr int TURNS = NR == 64 ? 1 : 2;
+  static constexpr int COLS = NR == 16 ? 16 : 32;              // rows of a softmax thread
   static constexpr int Q_TERM = NR * ROW_BYTES;
   static constexpr int P_ROW = NR * ESZ > 64 ? 128 : 64;       // bytes of a key's row of P, swizzled as wide
   static constexpr int P_TERM = 128 * P_ROW;
@@ -57,10 +61,10 @@ struct LanesCfg {
   // half multiplies whatever lies behind the panel in shared memory, and its lanes are never read.
   static constexpr uint32_t IDESC_PV = instr_desc(FMT, 1, 128, NR) | (1u << 15) | (FP8 ? 1u << 10 : 0u);
   static_assert(!FP8 || FMT == 0, "bits 7 and 10: formats of A (E4M3) and B (E5M2)");
-  // Tensor Memory: four S buffers, O of either group
-  static constexpr uint32_t O_COL = 4 * NR, COLS = NR == 64 ? 512 : (NR == 32 ? 256 : 128);
+  // Tensor Memory: four S buffers, O of either team or of both
+  static constexpr uint32_t O_COL = 4 * NR, TMEM_COLS = NR == 64 ? 512 : (NR == 32 ? 256 : 128);
   // shared memory from the end of what the K and V rings leave
-  static constexpr int SMALL = 1024 * NSC + (PAGED_MAX_BATCH + 4) * 4 + 8 * NR * 16 + 8 * NR * 8 + 2 * NR * 12 + 1024;
+  static constexpr int SMALL = 1024 * NSC + (PAGED_MAX_BATCH + 4) * 4 + 8 * COLS * 16 + 8 * NR * 8 + 2 * NR * 12 + 1024;
   static constexpr int ROOM = (227 * 1024 - 1024 - SMALL - 2 * (NP * P_TERM + NQ * Q_TERM)) / TILE_BYTES;
   static constexpr int NK = ROOM >= 16 ? 8 : (ROOM + 1) / 2, NV = ROOM >= 16 ? 8 : ROOM / 2;
   static constexpr int V_OFF = NK * TILE_BYTES;
@@ -70,10 +74,11 @@ struct LanesCfg {
   static constexpr int VIS_OFF = SC_OFF + NSC * 1024;           // [2][NR] u64: drafted keys a row sees
   static constexpr int ROWAT_OFF = VIS_OFF + 2 * NR * 8;        // [8 warps][NR / 2] i64: where an output row begins
   static constexpr int QMUL_OFF = ROWAT_OFF + 8 * NR * 4;       // [2][NR] floats: softmax scale of a row's codes
-  static constexpr int NMAX_OFF = QMUL_OFF + 2 * NR * 4;        // [8 warps][NR] minus the running maxima
-  static constexpr int FAC_OFF = NMAX_OFF + 8 * NR * 4;         // [8 warps][NR]
-  static constexpr int RED_OFF = FAC_OFF + 8 * NR * 4;          // [2][2 groups][4 quarters][NR]: maxima, sums
-  static constexpr int PRE_OFF = RED_OFF + 2 * 8 * NR * 4;
+  static constexpr int NMAX_OFF = QMUL_OFF + 2 * NR * 4;        // [8 warps][COLS] minus the running maxima
+  static constexpr int STEP_OFF = NMAX_OFF + 8 * COLS * 4;      // [8 warps][COLS] what they move by
+  static constexpr int FAC_OFF = STEP_OFF + 8 * COLS * 4;       // [8 warps][NR]
+  static constexpr int RED_OFF = FAC_OFF + 8 * NR * 4;          // [2][8 warps][COLS]: maxima, sums
+  static constexpr int PRE_OFF = RED_OFF + 2 * 8 * COLS * 4;
   static constexpr int FLAG_OFF = PRE_OFF + (PAGED_MAX_BATCH + 4) * 4;   // vodd [4] x 8, vtop [8], vmul [2], tmem, abort, scratch [16]
   static constexpr int BAR_OFF = FLAG_OFF + 32 + 32 + 8 + 8 + 64;
   static constexpr int NBAR = 14 + 2 * (NK + NV + NSC);
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
     for (int b = 0; b < 4; ++b) mbar_init(BAR_S(b), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(BAR_PV(b), 1);
-      mbar_init(BAR_P(b), 4);
+      mbar_init(BAR_P(b), C::TURNS == 2 ? 4 : 8);
       mbar_init(FULLQ(b), 4);
       mbar_init(EMPTYQ(b), 1 + 8);
     }
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
     }
     for (int s = 0; s < C::NSC; ++s) {
       mbar_init(FULLS(s), 32);
-      mbar_init(EMPTYS(s), 4);
+      mbar_init(EMPTYS(s), C::TURNS == 2 ? 4 : 8);
     }
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) vodd_sh[i] = 0;
@@ -235,7 +240,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
     return;
   }
   const long long x0 = cta_start(group, W, N), x1 = cta_start(group + 1ll, W, N);
-  if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_slot), C::COLS);
+  if (warp == MMA_WARP) tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -356,7 +361,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
       int tile = 0, seg = 0;                     // next tile of S: its place in segment `seg`
       int qi = 0, pi = 0;                        // tiles of S and PV issued
       int ks = 0, vs = 0;                        // ring positions
-      uint32_t kpar = 0, vpar = 0, fresh = 0, last = 0;        // bit i & 3: first tile of its group, last of its segment
+      uint32_t kpar = 0, vpar = 0, fresh = 0, last = 0;        // bit i & 3: first tile of its O, last of its segment
       long long t0 = clock64();
       while (more || pi < qi) {
         bool moved = false;
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
           tc_fence_after();
           const uint32_t av = static_cast<uint32_t>(dv0) + ((vs * C::TILE_BYTES) >> 4);
           const uint32_t bp = static_cast<uint32_t>(dp0) + (((pi & 1) * C::NP * C::P_TERM) >> 4);
-          const uint32_t d = tmem + C::O_COL + NR * (pi & 1);
+          const uint32_t d = tmem + C::O_COL + (C::TURNS == 2 ? NR * (pi & 1) : 0);
           const uint32_t acc0 = ((fresh >> (pi & 3)) & 1) ^ 1;
 #pragma unroll
           for (int term = 0; term < C::NP; ++term)
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
           mma_commit(BAR_S(qi & 3));
           mma_commit(EMPTYK(ks));
           const uint32_t bit = 1u << (qi & 3);
-          fresh = tile < 2 ? fresh | bit : fresh & ~bit;
+          fresh = tile < C::TURNS ? fresh | bit : fresh & ~bit;
           last &= ~bit;
           if (++tile == s.t1 - s.t0) {
             last |= bit;
@@ -431,43 +436,41 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
       wait_drain_paged(BAR_DONE, 0, p.spin_limit);
     }
   } else {
-    // ---- softmax: group g takes every other tile, with maxima, sums and O of its own; thread = key r ----
-    const int quarter = warp & 3, g = warp >> 2, r = 32 * quarter + lane;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(quarter) << 21);       // this warp's 32 lanes
-    const uint32_t o_at = tl + C::O_COL + NR * g, group_bar = 2u + g;
+    // ---- softmax: a team of four warps has maxima and sums of its own; thread = key r, COLS rows from cb ----
+    constexpr int COLS = C::COLS, TURNS = C::TURNS;
     constexpr float TAU = FP8 ? TAU_E4M3 : TAU_BF16;
-    constexpr int CH = NR == 64 ? 16 : NR;                                     // columns in registers at a time
+    const int quarter = warp & 3, team = warp >> 2, r = 32 * quarter + lane, cb = TURNS == 1 ? COLS * team : 0;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quarter) << 21);       // this warp's 32 lanes
+    const uint32_t o_at = tl + C::O_COL + (TURNS == 2 ? NR * team : cb), team_bar = 2u + team;
     const bool holds_o = 32 * quarter < D;                                    // lanes of O^T (D = 64: the lower half)
     float* nmax0 = reinterpret_cast<float*>(base + C::NMAX_OFF);
-    float* nmax = nmax0 + warp * NR;                                          // minus the rows' maxima
+    float* nmax = nmax0 + warp * COLS;                                        // minus the rows' maxima
+    float* step = reinterpret_cast<float*>(base + C::STEP_OFF) + warp * COLS;
     float* fac = reinterpret_cast<float*>(base + C::FAC_OFF) + warp * NR;
     long long* row_at = reinterpret_cast<long long*>(base + C::ROWAT_OFF) + warp * (NR / 2);
-    float* red_max = red + g * 4 * NR;
-    float* red_sum = red + 8 * NR;
-    const uint32_t prow = sP + g * C::NP * C::P_TERM + r * C::P_ROW;
+    float* red_max = red + 4 * team * COLS;
+    float* red_sum = red + 8 * COLS;
     const int swz = C::P_ROW == 128 ? (r & 7) : ((r >> 1) & 3);
     bool bad = false;                              // a wait of this warp gave up; it still meets the barriers
     Segment s;
     long long x = x0;
-    int it = 0, done = 0;                          // tiles before the segment; this group's tiles so far
-    int sslot = g;
+    int it = 0;                                    // tiles before the segment
+    int sslot = TURNS == 2 ? team : 0;
     uint32_t spar = 0;
     for (int seg = 0; next_segment(p, pre, x, x1, s); ++seg) {
       const int buf = seg & 1;
       const int ctx = *(p.ctx_lens + s.b), ql = p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T, L = ctx + ql;
-      const float* qmul = qmul_sh + buf * NR;
+      const float* qmul = qmul_sh + buf * NR + cb;
       const unsigned long long* vis = vis_sh + buf * NR;
-#pragma unroll
-      for (int i = 0; i < NR; i += 32)
-        if (i + lane < NR) nmax[i + lane] = FLT_MAX;
+      if (lane < COLS) nmax[lane] = 0.f;
       __syncwarp();
       if (!bad && !warp_wait(FULLQ(buf), (seg >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
-      uint64_t l[NR / 2];                          // this thread's keys' part of the rows' sums, in pairs
+      uint64_t l[COLS / 2];                        // this thread's keys' part of the rows' sums, in pairs
 #pragma unroll
-      for (int i = 0; i < NR / 2; ++i) l[i] = 0;
+      for (int i = 0; i < COLS / 2; ++i) l[i] = 0;
       float vref = 0.f, rv = 0.f;                  // E4M3: power of two at or above the value scales, its reciprocal
-      const int first = s.t0 + ((g ^ it) & 1);
-      for (int j = first; j < s.t1; j += 2) {
+      const int first = s.t0 + (TURNS == 2 ? (team ^ it) & 1 : 0);
+      for (int j = first; j < s.t1; j += TURNS) {
         const int at = it + j - s.t0;              // place among the CTA's tiles
         const int key = 128 * j + r;
         const bool tail = 128 * j + 128 > ctx;     // drafted keys, or the end of the sequence
@@ -484,24 +487,23 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
           vsc = key < L ? sc[128 + r] : 0.f;
           odd = !finite_f(vsc);
         }
-        if (!bad) tc_fence_after();
-        const uint32_t s_at = tl + NR * (at & 3);
-        // logits of columns i .. in log2 units plus add[]: hidden ones -inf
-        auto logits = [&](int i, auto& y, const float* add) {
-          constexpr int M = sizeof(y) / sizeof(y[0]);
-          uint32_t u[M];
+        // logits in log2 units less the maxima so far; hidden ones -inf
+        float y[COLS];
+        float top = -INFINITY;
+        {
+          uint32_t u[COLS];
           if (!bad) {
-            tmem_ld(s_at + i, u);
+            tc_fence_after();
+            tmem_ld(tl + NR * (at & 3) + cb, u);
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int k = 0; k < M; ++k) reg_fence(u[k]);
+          for (int k = 0; k < COLS; ++k) reg_fence(u[k]);
           const uint64_t ks2 = f2_pack(ks, ks);
 #pragma unroll
-          for (int k = 0; k < M; k += 4) {
-            const float4 c4 = *reinterpret_cast<const float4*>(qmul + i + k);
-            float4 a4 = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (add != nullptr) a4 = *reinterpret_cast<const float4*>(add + i + k);
+          for (int k = 0; k < COLS; k += 4) {
+            const float4 c4 = *reinterpret_cast<const float4*>(qmul + k);
+            const float4 a4 = *reinterpret_cast<const float4*>(nmax + k);
             uint64_t lo = f2_pack(__uint_as_float(u[k]), __uint_as_float(u[k + 1]));
             uint64_t hi = f2_pack(__uint_as_float(u[k + 2]), __uint_as_float(u[k + 3]));
             if constexpr (FP8) {
@@ -514,44 +516,40 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
           if (tail) {
             const int rel = key - ctx;
 #pragma unroll
-            for (int k = 0; k < M; ++k)
-              if (rel >= 0 && (rel >= 64 || !((vis[i + k] >> rel) & 1))) y[k] = -INFINITY;
+            for (int k = 0; k < COLS; ++k)
+              if (rel >= 0 && (rel >= 64 || !((vis[cb + k] >> rel) & 1))) y[k] = -INFINITY;
           }
-        };
-        float y[CH];
-        float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NR; c += CH) {
-          logits(c, y, nmax);
-#pragma unroll
-          for (int i = 0; i < CH; i += 2) top = max3(top, y[i], y[i + 1]);
+          for (int k = 0; k < COLS; k += 2) top = max3(top, y[k], y[k + 1]);
         }
-        const bool any = named_bar_any(group_bar, 128, top > TAU || (FP8 && !odd && vsc > vref));
-        // P's buffer and O hold PV of this group's tile before
-        if (done > 0 && !bad) {
-          if (!__all_sync(0xffffffffu, mbar_test(BAR_PV(g), (done - 1) & 1)) &&
-              !warp_wait(BAR_PV(g), (done - 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+        // a unit's first tile sets the maxima
+        const bool any = named_bar_any(team_bar, 128, j == first || top > TAU || (FP8 && !odd && vsc > vref));
+        // P's buffer (and, in turns, O) are free with PV of the tile two before
+        if (at >= 2 && !bad) {
+          if (!__all_sync(0xffffffffu, mbar_test(BAR_PV(at & 1), ((at >> 1) - 1) & 1)) &&
+              !warp_wait(BAR_PV(at & 1), ((at >> 1) - 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
           else tc_fence_after();
         }
         if (any) {
           // some row's maximum moves (or the scales' bound): the rows' maxima over the tile's keys
-#pragma unroll 1
-          for (int i = 0; i < NR; i += 16) {
+#pragma unroll
+          for (int i = 0; i < COLS; i += 16) {
             float z[16];
-            logits(i, z, nullptr);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) z[k] = y[i + k];
             const float m = column_reduce<true>(z);            // (a NaN counts for nothing)
-            if (lane < 16) red_max[quarter * NR + i + lane] = m;
+            if (lane < 16) red_max[quarter * COLS + i + lane] = m;
           }
           if constexpr (FP8) {
             const uint32_t m = __reduce_max_sync(0xffffffffu, odd ? 0u : __float_as_uint(vsc));
             if (lane == 0) vtop_sh[warp] = m;
           }
-          named_bar_sync(group_bar, 128);
+          named_bar_sync(team_bar, 128);
           float vfac = 1.f;
           if constexpr (FP8) {
             float vt = 0.f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) vt = fmaxf(vt, __uint_as_float(vtop_sh[4 * g + w]));
+            for (int w = 0; w < 4; ++w) vt = fmaxf(vt, __uint_as_float(vtop_sh[4 * team + w]));
             if (vt > vref) {
               const float nref = __uint_as_float((__float_as_uint(vt) & 0x7f800000u) + (vt < 0x1p126f ? 0x00800000u : 0u));
               vfac = vref / nref;
@@ -559,98 +557,110 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
               rv = 1.f / nref;
             }
           }
+          if (lane < COLS) {
+            float m = red_max[lane];
 #pragma unroll
-          for (int i = 0; i < NR; i += 32)
-            if (i + lane < NR) {
-              const float old = -nmax[i + lane];
-              float m = old;
-#pragma unroll
-              for (int w = 0; w < 4; ++w) m = fmaxf(m, red_max[w * NR + i + lane]);
-              nmax[i + lane] = -m;
-              fac[i + lane] = ex2(old - m);
-            }
+            for (int w = 1; w < 4; ++w) m = fmaxf(m, red_max[w * COLS + lane]);
+            // The first tile's maxima replace the zeros that stand for none; later ones only rise.  A row that
+            // sees nothing of its team's first tile keeps 0: such a tile begins with drafted keys, of which there are
+            // at most 64, so the row has no other tile.
+            const float up = m == -INFINITY ? 0.f : (j == first ? m : fmaxf(m, 0.f));
+            nmax[lane] -= up;
+            step[lane] = -up;
+            fac[lane] = ex2(-up);
+          }
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < NR; i += 4) {
-            const float4 f4 = *reinterpret_cast<const float4*>(fac + i);
-            l[i / 2] = f2_mul(l[i / 2], f2_pack(f4.x, f4.y));
-            l[i / 2 + 1] = f2_mul(l[i / 2 + 1], f2_pack(f4.z, f4.w));
+          for (int i = 0; i < COLS; i += 4) {
+            const float4 d4 = *reinterpret_cast<const float4*>(step + i);
+            f2_unpack(f2_add(f2_pack(y[i], y[i + 1]), f2_pack(d4.x, d4.y)), y[i], y[i + 1]);
+            f2_unpack(f2_add(f2_pack(y[i + 2], y[i + 3]), f2_pack(d4.z, d4.w)), y[i + 2], y[i + 3]);
           }
-          if (!bad && j > first && holds_o) {
-#pragma unroll 1
-            for (int i = 0; i < NR; i += 8) {
-              uint32_t o[8];
-              tmem_ld(o_at + i, o);
-              tmem_wait_ld();
+          if (j > first) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                reg_fence(o[k]);
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * fac[i + k] * vfac);
-              }
-              tmem_st8(o_at + i, o);
+            for (int i = 0; i < COLS; i += 4) {
+              const float4 f4 = *reinterpret_cast<const float4*>(fac + i);
+              l[i / 2] = f2_mul(l[i / 2], f2_pack(f4.x, f4.y));
+              l[i / 2 + 1] = f2_mul(l[i / 2 + 1], f2_pack(f4.z, f4.w));
             }
-            tmem_wait_st();
+            // O must hold PV of this O's last tile; PV of this one waits for the team's arrival below.  (In the state
+            // of its barrier nothing older can stand for that: PV two tiles before is complete.)
+            if (TURNS == 1 && !bad) {
+              if (!warp_wait(BAR_PV((at - 1) & 1), ((at - 1) >> 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+              else tc_fence_after();
+            }
+            if (!bad && holds_o) {
+#pragma unroll 1
+              for (int i = 0; i < COLS; i += 8) {
+                uint32_t o[8];
+                tmem_ld(o_at + i, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  reg_fence(o[k]);
+                  o[k] = __float_as_uint(__uint_as_float(o[k]) * fac[i + k] * vfac);
+                }
+                tmem_st8(o_at + i, o);
+              }
+              tmem_wait_st();
+            }
           }
-          if (NR == CH) logits(0, y, nmax);
         }
         // numerators
-        const float w = odd ? __int_as_float(0x7fffffff) : vsc * rv * TOP_E4M3;
-        const bool fix = FP8 && __any_sync(0xffffffffu, odd);    // hidden: 0 whatever the scale; seen and not finite: NaN
+        const uint32_t prow = sP + (at & 1) * C::NP * C::P_TERM + r * C::P_ROW;
+        if constexpr (!FP8) {
 #pragma unroll
-        for (int c = 0; c < NR; c += CH) {
-          if (NR > CH) logits(c, y, nmax);
-          if constexpr (!FP8) {
+          for (int i = 0; i < COLS; i += 8) {
+            uint32_t pk[4];
 #pragma unroll
-            for (int i = 0; i < CH; i += 8) {
-              uint32_t pk[4];
-#pragma unroll
-              for (int k = 0; k < 8; k += 2) {
-                const float a = ex2(y[i + k]), b = ex2(y[i + k + 1]);
-                l[(c + i + k) / 2] = f2_add(l[(c + i + k) / 2], f2_pack(a, b));
-                pk[k / 2] = pack_bf16x2(a, b);
-              }
-              st_shared_v4(prow + ((((c + i) >> 3) ^ swz) << 4), pk[0], pk[1], pk[2], pk[3]);
+            for (int k = 0; k < 8; k += 2) {
+              const float a = ex2(y[i + k]), b = ex2(y[i + k + 1]);
+              l[(i + k) / 2] = f2_add(l[(i + k) / 2], f2_pack(a, b));
+              pk[k / 2] = pack_bf16x2(a, b);
             }
-          } else {
+            st_shared_v4(prow + ((((cb + i) >> 3) ^ swz) << 4), pk[0], pk[1], pk[2], pk[3]);
+          }
+        } else {
+          const float w = odd ? __int_as_float(0x7fffffff) : vsc * rv * TOP_E4M3;
+          const bool fix = __any_sync(0xffffffffu, odd);       // hidden: 0 whatever the scale; seen and not finite: NaN
 #pragma unroll
-            for (int i = 0; i < CH; i += 16) {
-              uint32_t tt[4][3];
+          for (int i = 0; i < COLS; i += 16) {
+            uint32_t tt[4][3];
 #pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                float e[4], f[4];
+            for (int h = 0; h < 4; ++h) {
+              float e[4], f[4];
 #pragma unroll
-                for (int k = 0; k < 4; k += 2) {
-                  e[k] = ex2(y[i + 4 * h + k]);
-                  e[k + 1] = ex2(y[i + 4 * h + k + 1]);
-                  const uint64_t e2 = f2_pack(e[k], e[k + 1]);
-                  uint64_t& lc = l[(c + i + 4 * h + k) / 2];
-                  lc = f2_add(lc, e2);
-                  f2_unpack(f2_mul(e2, f2_pack(w, w)), f[k], f[k + 1]);
-                }
-                if (fix) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) f[k] = e[k] == 0.f ? 0.f : f[k];
-                }
-                e5m2_terms4(f[0], f[1], f[2], f[3], tt[h]);
+              for (int k = 0; k < 4; k += 2) {
+                e[k] = ex2(y[i + 4 * h + k]);
+                e[k + 1] = ex2(y[i + 4 * h + k + 1]);
+                const uint64_t e2 = f2_pack(e[k], e[k + 1]);
+                uint64_t& lc = l[(i + 4 * h + k) / 2];
+                lc = f2_add(lc, e2);
+                f2_unpack(f2_mul(e2, f2_pack(w, w)), f[k], f[k + 1]);
               }
-              const uint32_t dst = prow + ((((c + i) >> 4) ^ swz) << 4);
+              if (fix) {
 #pragma unroll
-              for (int k = 0; k < 3; ++k) st_shared_v4(dst + k * C::P_TERM, tt[0][k], tt[1][k], tt[2][k], tt[3][k]);
+                for (int k = 0; k < 4; ++k) f[k] = e[k] == 0.f ? 0.f : f[k];
+              }
+              e5m2_terms4(f[0], f[1], f[2], f[3], tt[h]);
             }
+            const uint32_t dst = prow + ((((cb + i) >> 4) ^ swz) << 4);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) st_shared_v4(dst + k * C::P_TERM, tt[0][k], tt[1][k], tt[2][k], tt[3][k]);
           }
         }
         if (tail) {
-          // thread = key row r of the value tile: what must not meet a zero numerator is taken out.  (PV of the tile
-          // two before is complete, so the slot's phase before this one is too.)
+          // thread = key row r of the value tile (in turns; else a team half the row): what must not meet a zero
+          // numerator is taken out.  (PV two tiles before is complete, so the slot's phase before this one is too.)
           if (!bad && !warp_wait(FULLV(at % C::NV), (at / C::NV) & 1, ctl, WHERE_PAGED_USE)) bad = true;
           if (!bad && key >= ctx) {
             uint8_t* row = base + C::V_OFF + (at % C::NV) * C::TILE_BYTES + r * C::PANEL_ROW;
             const bool clear = key >= L || odd;
             bool hits = false;
-            constexpr int PC = C::PANEL_ROW / 16;
+            constexpr int PC = C::PANEL_ROW / 16, NC = C::ROW_BYTES / 16;
             const int vswz = C::PANEL_ROW == 128 ? (r & 7) : ((r >> 1) & 3);
 #pragma unroll 1
-            for (int i = 0; i < C::ROW_BYTES / 16; ++i) {
+            for (int i = TURNS == 1 ? team * (NC / 2) : 0; i < (TURNS == 1 ? (team + 1) * (NC / 2) : NC); ++i) {
               uint4* v = reinterpret_cast<uint4*>(row + (i / PC) * C::PANEL_BYTES + (((i % PC) ^ vswz) << 4));
               if (clear) {
                 *v = make_uint4(0u, 0u, 0u, 0u);
@@ -674,31 +684,31 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(BAR_P(g));
+          mbar_arrive(BAR_P(at & 1));
           if (FP8) mbar_arrive(EMPTYS(sslot));
         }
-        ++done;
         if constexpr (FP8) {
-          sslot += 2;
+          sslot += TURNS;
           if (sslot >= C::NSC) {
             sslot -= C::NSC;
             spar ^= 1;
           }
         }
       }
-      // ---- end of the segment: the sums over the lanes and the groups, then the output; group g's warps take
-      // columns c0 .. c0 + NR / 2 of both groups' O ----
+      // ---- end of the segment: the sums over the lanes and the teams, then the output; a team's warps take
+      // columns c0 .. c0 + NR / 2 of O, or of both teams' O ----
 #pragma unroll
-      for (int c = 0; c < NR; c += CH) {
-        float part[CH];
+      for (int c = 0; c < COLS; c += 16) {
+        float part[16];
 #pragma unroll
-        for (int i = 0; i < CH; i += 2) f2_unpack(l[(c + i) / 2], part[i], part[i + 1]);
+        for (int i = 0; i < 16; i += 2) f2_unpack(l[(c + i) / 2], part[i], part[i + 1]);
         const float sum = column_reduce<false>(part);
-        if (lane < CH) red_sum[(4 * g + quarter) * NR + c + lane] = sum;
+        if (lane < 16) red_sum[warp * COLS + c + lane] = sum;
       }
-      if (FP8 && lane == 0 && quarter == 0) vmul_sh[g] = vref * (1.f / TOP_E4M3);
+      if (FP8 && lane == 0 && quarter == 0) vmul_sh[team] = vref * (1.f / TOP_E4M3);
       const int n = s.t1 - s.t0;
-      const bool has0 = n > 1 || (it & 1) == 0, has1 = n > 1 || (it & 1) == 1;        // groups with tiles in the segment
+      // teams with tiles in the segment; one without left nothing of it in its O
+      const bool has0 = TURNS == 1 || n > 1 || (it & 1) == 0, has1 = TURNS == 2 && (n > 1 || (it & 1) == 1);
       it += n;
       named_bar_sync(1, 256);
       const unsigned long long vodd = vodd_sh[seg & 3];
@@ -707,15 +717,22 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
       const bool whole = s.t0 == 0 && s.t1 == s.n;
       const long long ws_row = (2ll * group + (s.t0 > 0 ? 0 : 1)) * NR;
       constexpr int HALF = NR / 2;
-      const int c0 = HALF * g;
+      const int c0 = HALF * team;
       if (lane < HALF) {
         const int pr = c0 + lane, t = token_of(p, pr);
-        float sums[2] = {0.f, 0.f}, f[2];
+        float sums[2] = {0.f, 0.f}, m, f[2] = {1.f, 1.f};
+        if constexpr (TURNS == 2) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sums[k >> 2] += red_sum[k * NR + pr];
-        const float m0 = -nmax0[pr], m1 = -nmax0[4 * NR + pr], m = fmaxf(m0, m1);
-        f[0] = ex2(m0 - m);
-        f[1] = ex2(m1 - m);
+          for (int k = 0; k < 8; ++k) sums[k >> 2] += red_sum[k * COLS + pr];
+          const float m0 = sums[0] == 0.f ? -FLT_MAX : -nmax0[pr], m1 = sums[1] == 0.f ? -FLT_MAX : -nmax0[4 * COLS + pr];
+          m = fmaxf(m0, m1);
+          f[0] = ex2(m0 - m);
+          f[1] = ex2(m1 - m);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sums[0] += red_sum[(4 * team + k) * COLS + lane];
+          m = -nmax[lane];
+        }
         const float sum = sums[0] * f[0] + sums[1] * f[1], inv = sum == 0.f ? 0.f : 1.f / sum;
         fac[lane] = f[0] * inv;
         fac[HALF + lane] = f[1] * inv;
@@ -731,19 +748,19 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
       if (!bad && !warp_wait(BAR_O, seg & 1, ctl, WHERE_PAGED_USE)) bad = true;
       if (!bad && holds_o) {
         tc_fence_after();
-        const float v0 = FP8 ? vmul_sh[0] : 1.f, v1 = FP8 ? vmul_sh[1] : 1.f;
+        const float v0 = FP8 ? vmul_sh[TURNS == 2 ? 0 : team] : 1.f, v1 = FP8 ? vmul_sh[1] : 1.f;
 #pragma unroll 1
         for (int i = 0; i < HALF; i += 8) {
           uint32_t a[8], b[8];
           tmem_ld(tl + C::O_COL + c0 + i, a);
-          tmem_ld(tl + C::O_COL + NR + c0 + i, b);
+          if (TURNS == 2) tmem_ld(tl + C::O_COL + NR + c0 + i, b);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             reg_fence(a[k]);
-            reg_fence(b[k]);
-            // a group without tiles left nothing of this segment in its O
-            float f = (has0 ? __uint_as_float(a[k]) * fac[i + k] * v0 : 0.f) + (has1 ? __uint_as_float(b[k]) * fac[HALF + i + k] * v1 : 0.f);
+            if (TURNS == 2) reg_fence(b[k]);
+            float f = has0 ? __uint_as_float(a[k]) * fac[i + k] * v0 : 0.f;
+            if (TURNS == 2 && has1) f += __uint_as_float(b[k]) * fac[HALF + i + k] * v1;
             const long long to = row_at[i + k];
             if (to < 0) continue;
             if (!FP8 && vodd != 0) {
@@ -774,7 +791,7 @@ __global__ void __launch_bounds__(LANES_THREADS, 1)
   __syncthreads();
   if (warp == MMA_WARP) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::COLS);
+    tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 

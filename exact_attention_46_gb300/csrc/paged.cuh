@@ -172,18 +172,25 @@ __device__ __forceinline__ bool next_segment(const PagedParams& p, const int* pr
 
 __device__ __forceinline__ long long cta_start(long long i, long long W, long long N) { return quotient(i * W, N); }
 
-// What the merge has to do about the start of group i's tiles (i > 0): where that is the first cut inside a
-// unit, the unit and the number of its parts (groups i - 1 ..); otherwise no parts.  One thread.
+// Units of more parts than this are merged by the blocks of all their cuts, others by those of the first.
+constexpr int MANY_PARTS = 8;
+
+// What the merge has to do about the start of group i's tiles (i > 0), one thread: the unit cut there, if it is the
+// unit's first cut or one of many, as its parts (of groups i - 1 - k ..) + (k << 16), sequence, key/value head and
+// q_len; k counts the unit's cuts before this one.  Otherwise no parts.
 __device__ __forceinline__ void write_cut(const PagedParams& p, const int* pre, int i, long long W, long long N) {
   if (p.cuts == nullptr || i == 0) return;
   int4 c = make_int4(0, 0, 0, 0);
   if (i < N) {
     const long long x = cta_start(i, W, N);
     const Segment s = find_segment(p, pre, x, W);
-    // the group that holds list position y is the last c with c W / N <= y; x - t0 is tile 0's
-    const long long c0 = quotient((x - s.t0 + 1) * N - 1, W), c1 = quotient((x - s.t0 + s.n) * N - 1, W);
-    if (s.t0 > 0 && c0 == i - 1)
-      c = make_int4(static_cast<int>(c1 - c0) + 1, s.b, s.hkv, p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
+    if (s.t0 > 0) {
+      // the group that holds list position y is the last c with c W / N <= y; x - t0 is tile 0's
+      const int c0 = static_cast<int>(quotient((x - s.t0 + 1) * N - 1, W));
+      const int parts = static_cast<int>(quotient((x - s.t0 + s.n) * N - 1, W)) - c0 + 1;
+      if (c0 == i - 1 || parts > MANY_PARTS)
+        c = make_int4(parts + ((i - 1 - c0) << 16), s.b, s.hkv, p.q_lens != nullptr ? *(p.q_lens + s.b) : p.T);
+    }
   }
   p.cuts[i] = c;
 }
