@@ -91,25 +91,7 @@ struct LanesCfg {
 
 constexpr int LANES_THREADS = 512;
 constexpr int MMA_WARP = 8, K_WARP = 9, S_WARP = 11, Q_WARP = 12;
-// Lazy rescale threshold (log2).  Numerators reach 2^TAU; over E4M3 they are scaled by 2^(15 - TAU), the top of E5M2.
-constexpr float TAU_BF16 = 8.0f, TAU_E4M3 = 4.0f, TOP_E4M3 = 2048.0f;
-
-// Four numerators in [0, 2^15] as three E5M2 terms (packed bytes): fp16 first (2^-11), whose upper byte is
-// the first term, the remainder's upper byte the second, and what is left then rounded: each takes three bits
-// at least, so the sum is off by 2^-9 of the number, or 2^-17, half of E5M2's smallest step.
-__device__ __forceinline__ void e5m2_terms4(float a, float b, float c, float d, uint32_t (&t)[3]) {
-  asm("{\n\t.reg .b32 x, y, p, q, r, s;\n\t.reg .b16 u, v;\n\t"
-      "cvt.rn.f16x2.f32 x, %4, %3;\n\tcvt.rn.f16x2.f32 y, %6, %5;\n\t"
-      "prmt.b32 %0, x, y, 0x7531;\n\t"
-      "and.b32 p, x, 0xff00ff00;\n\tand.b32 q, y, 0xff00ff00;\n\t"
-      "sub.rn.f16x2 x, x, p;\n\tsub.rn.f16x2 y, y, q;\n\t"
-      "prmt.b32 %1, x, y, 0x7531;\n\t"
-      "and.b32 r, x, 0xff00ff00;\n\tand.b32 s, y, 0xff00ff00;\n\t"
-      "sub.rn.f16x2 x, x, r;\n\tsub.rn.f16x2 y, y, s;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 u, x;\n\tcvt.rn.satfinite.e5m2x2.f16x2 v, y;\n\t"
-      "mov.b32 %2, {u, v};\n\t}"
-      : "=r"(t[0]), "=r"(t[1]), "=r"(t[2]) : "f"(a), "f"(b), "f"(c), "f"(d));
-}
+constexpr float TAU_BF16 = 8.0f;        // lazy rescale threshold (log2): numerators reach 2^TAU
 
 // Registers of a warpgroup for 32 and 64 rows, out of the block's: 512 threads x 128 = 256 x 176 + 256 x 80 =
 // 256 x 184 + 256 x 72, what neither side spills in.
@@ -811,19 +793,19 @@ cudaError_t launch_lanes_d(const CUtensorMap& tk, const CUtensorMap& tv, const P
   return launch_overlapped(attn_lanes_kernel<D, FP8, NR>, dim3(p.n_cta), LANES_THREADS, C::SMEM_BYTES, st, tk, tv, p);
 }
 
-template <int D, bool FP8>
-cudaError_t launch_lanes_n(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, cudaStream_t st) {
+template <int D>
+cudaError_t launch_lanes_n(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, bool fp8, cudaStream_t st) {
   const int rb = paged_rows(p.G * p.T);
-  return rb == 16   ? launch_lanes_d<D, FP8, 16>(tk, tv, p, st)
-         : rb == 32 ? launch_lanes_d<D, FP8, 32>(tk, tv, p, st)
-                    : launch_lanes_d<D, FP8, 64>(tk, tv, p, st);
+  if (!fp8) return launch_lanes_d<D, false, 64>(tk, tv, p, st);
+  return rb == 16   ? launch_lanes_d<D, true, 16>(tk, tv, p, st)
+         : rb == 32 ? launch_lanes_d<D, true, 32>(tk, tv, p, st)
+                    : launch_lanes_d<D, true, 64>(tk, tv, p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_lanes(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8, cudaStream_t st) {
-  if (D == 64) return fp8 ? launch_lanes_n<64, true>(tk, tv, p, st) : launch_lanes_n<64, false>(tk, tv, p, st);
-  return fp8 ? launch_lanes_n<128, true>(tk, tv, p, st) : launch_lanes_n<128, false>(tk, tv, p, st);
+  return D == 64 ? launch_lanes_n<64>(tk, tv, p, fp8, st) : launch_lanes_n<128>(tk, tv, p, fp8, st);
 }
 
 }  // namespace ea46

@@ -19,8 +19,8 @@
 //   * E4M3: the products run on the codes themselves.  A query row, scaled by a power of two into
 //     E4M3's range, is the exact sum of two E4M3 terms (bf16 has eight significant bits, each term
 //     four; below 2^-10 of the row's largest element the second loses bits, 2^-18 of the largest at
-//     most), and a numerator times its value's scale is rounded to the sum of two: 2^-8 of it, as bf16
-//     would be, because one E4M3 term (2^-4) is too coarse and the tensor core takes no mixed types.
+//     most), and a numerator times its value's scale is rounded to the sum of three E5M2 terms: 2^-9 of it, as bf16
+//     would be.  (One E4M3 term would be off by 2^-4, two lose what lies 2^-17 under the largest.)
 //     Each term is one more MMA over the same tile;
 //   * hidden keys: logits replaced by -inf before the maximum.  In tiles with drafted keys or the end of
 //     the sequence the value rows past the end are zeroed in shared memory, and so is what is not
@@ -49,6 +49,7 @@ struct TreeCfg {
   static constexpr int PANEL_BYTES = 128 * PANEL_ROW;
   static constexpr int TILE_BYTES = 128 * ROW_BYTES;
   static constexpr int NQ = FP8 ? 2 : 1;                      // query tiles: terms of the queries
+  static constexpr int NP = FP8 ? 3 : 1;                      // terms of the numerators
   // K and V tiles in flight
   static constexpr int NK = TILE_BYTES == 32768 ? 3 : (TILE_BYTES == 16384 ? 5 : 8);
   static constexpr int NV = TILE_BYTES == 32768 ? 2 : (TILE_BYTES == 16384 ? 5 : 8);
@@ -61,9 +62,9 @@ struct TreeCfg {
   static constexpr int KSTEPS_PV = 128 / UMMA_K;
   static constexpr uint32_t FMT = FP8 ? 0u : 1u;
   static constexpr uint32_t IDESC_QK = instr_desc(FMT, 0, 128, 128);
-  static constexpr uint32_t IDESC_PV = instr_desc(FMT, 1, 128, D);
-  // Tensor Memory: S buffers at columns 0 and 128, O at 256, two P buffers of 64 columns after O (E4M3: 32
-  // for each term)
+  static constexpr uint32_t IDESC_PV = instr_desc(FMT, 1, 128, D) | (FP8 ? 1u << 7 : 0u);     // A: E5M2 (bf16: FMT)
+  // Tensor Memory: S buffers at columns 0 and 128, O at 256, after it two P buffers of 64 columns (E4M3: one, 32
+  // columns for each term)
   static constexpr uint32_t O_COL = 256, P_COL = 256 + D;
   static constexpr int K_OFF = NQ * TILE_BYTES, V_OFF = K_OFF + NK * TILE_BYTES;
   static constexpr int SC_OFF = V_OFF + NV * TILE_BYTES;
@@ -82,9 +83,7 @@ struct TreeCfg {
 
 constexpr int TREE_THREADS = 384;
 constexpr int MMA_WARP = 8, K_WARP = 9, S_WARP = 11;
-// Lazy rescale threshold (log2).  Numerators reach 2^TAU; E4M3's two terms then span [2^-10, 2^8] around
-// numerators scaled by 2^7.
-constexpr float TAU_BF16 = 8.0f, TAU_E4M3 = 1.0f;
+constexpr float TAU_BF16 = 8.0f;        // lazy rescale threshold (log2): numerators reach 2^TAU
 
 // Registers of a warpgroup, out of the block's: 384 threads x 168 = 2 x 128 x 200 + 128 x 104.  The E4M3
 // softmax spills 588 bytes in 168; bf16 fits.
@@ -216,9 +215,9 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             if (!(ok = wait_bounded(FULLV(vs), (it / C::NV) & 1, ctl, WHERE_PAGED_MMA))) break;
             tc_fence_after();
             const uint64_t bv = dv0 + ((vs * C::TILE_BYTES) >> 4);
-            const uint32_t pa = tmem + C::P_COL + 64u * (it & 1);
+            const uint32_t pa = tmem + C::P_COL + (FP8 ? 0u : 64u * (it & 1));
 #pragma unroll
-            for (int term = 0; term < C::NQ; ++term)
+            for (int term = 0; term < C::NP; ++term)
 #pragma unroll
               for (int kk = 0; kk < C::KSTEPS_PV; ++kk) {
                 const uint32_t off = (kk * C::UMMA_K * C::PANEL_ROW) >> 4;
@@ -289,7 +288,8 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         int ex = static_cast<int>(__float_as_uint(m) >> 23) - 127;
         ex = ex < -100 ? -100 : (ex > 100 ? 100 : ex);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
-        cmul = p.c_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
+        // (an infinite element, which E4M3 cannot hold, makes the row's logits NaN)
+        cmul = m == INFINITY ? __int_as_float(0x7fffffff) : p.c_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const int c = hf * (D / 32) + i;
@@ -422,10 +422,10 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
           rescale = true;
         }
         const float off = m_run == -INFINITY ? 0.f : m_run;
-        const uint32_t pb = tl + C::P_COL + 64u * (it & 1);
-        // E4M3: numerators times 2^7 / vref, a power of two that goes into the exponent (no scale seen: 1);
-        // what would leave fp32's range there (scales below 2^-53 or above 2^67) is multiplied on
-        const int want = FP8 && vref > 0.f ? 134 - static_cast<int>(__float_as_uint(vref) >> 23) : 0;
+        const uint32_t pb = tl + C::P_COL + (FP8 ? 0u : 64u * (it & 1));
+        // E4M3: numerators times 2^11 / vref, a power of two that goes into the exponent (no scale seen: 1);
+        // what would leave fp32's range there (scales below 2^-49 or above 2^71) is multiplied on
+        const int want = FP8 && vref > 0.f ? 138 - static_cast<int>(__float_as_uint(vref) >> 23) : 0;
         const int shift = want > 60 ? 60 : (want < -60 ? -60 : want);
         const float extra = __uint_as_float(static_cast<uint32_t>(127 + want - shift) << 23);
         const float off_v = off - (FP8 ? static_cast<float>(shift) : 0.f);
@@ -447,12 +447,17 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
             if (!bad) tmem_st16(pb + c0 / 2 + 16u * q, pk);
           }
         } else {
+          // one P buffer: PV of the tile before must be through with it
+          if (!bad && j > dn.t0) {
+            if (!warp_wait(BAR_PV, (it - 1) & 1, ctl, WHERE_PAGED_USE)) bad = true;
+            else tc_fence_after();
+          }
           // FIX: tiles where some numerator may meet a scale that is not finite, or needs `extra`
           auto numerators = [&](auto fix_c) {
             constexpr bool FIX = decltype(fix_c)::value;
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
-              uint32_t s[32], hi[8], lo[8];
+              uint32_t s[32], tt[3][8];
               load_s(c0 + 32 * q, s);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -474,11 +479,14 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
                   for (int h = 0; h < 4; ++h)
                     y[h] = e[h] == 0.f ? 0.f : (finite_f(v[h]) ? y[h] * extra : __int_as_float(0x7fffffff));
                 }
-                e4m3_terms4(y[0], y[1], y[2], y[3], hi[i], lo[i]);
+                uint32_t w[3];
+                e5m2_terms4(y[0], y[1], y[2], y[3], w);
+#pragma unroll
+                for (int h = 0; h < 3; ++h) tt[h][i] = w[h];
               }
               if (!bad) {
-                tmem_st8(pb + c0 / 4 + 8u * q, hi);
-                tmem_st8(pb + 32u + c0 / 4 + 8u * q, lo);
+#pragma unroll
+                for (int h = 0; h < 3; ++h) tmem_st8(pb + 32u * h + c0 / 4 + 8u * q, tt[h]);
               }
             }
           };
@@ -578,7 +586,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
         const bool whole = dn.t0 == 0 && dn.t1 == dn.n;
         const long long ws_slot = 2ll * (group * static_cast<long long>(p.row_tiles) + dn_rt) + (dn.t0 > 0 ? 0 : 1);
         float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-        if (FP8) inv *= vref * 0x1p-7f;
+        if (FP8) inv *= vref * (1.f / TOP_E4M3);
         const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
         const long long head = static_cast<long long>(dn.hkv) * p.G + pr - t * p.G;
         // a thread holds a row, whose columns lie side by side in memory: 16 columns of the warp's 32 rows at
@@ -660,7 +668,7 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
 }
 
 template <int D, bool FP8>
-cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, bool combine, cudaStream_t st) {
+cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, cudaStream_t st) {
   using C = TreeCfg<D, FP8>;
   static std::atomic<unsigned long long> configured{0};
   int dev = 0;
@@ -672,17 +680,15 @@ cudaError_t launch_tree_d(const CUtensorMap& tk, const CUtensorMap& tv, const Pa
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  e = launch_overlapped(attn_tree_kernel<D, FP8>, dim3(p.n_cta * p.group_ctas), TREE_THREADS, C::SMEM_BYTES, st, tk, tv, p);
-  if (e != cudaSuccess || !combine) return e;
-  return launch_tree_combine(p, D, st);
+  return launch_overlapped(attn_tree_kernel<D, FP8>, dim3(p.n_cta * p.group_ctas), TREE_THREADS, C::SMEM_BYTES, st, tk, tv, p);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_tree(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
-                             bool combine, cudaStream_t st) {
-  if (D == 64) return fp8 ? launch_tree_d<64, true>(tk, tv, p, combine, st) : launch_tree_d<64, false>(tk, tv, p, combine, st);
-  return fp8 ? launch_tree_d<128, true>(tk, tv, p, combine, st) : launch_tree_d<128, false>(tk, tv, p, combine, st);
+                             cudaStream_t st) {
+  if (D == 64) return fp8 ? launch_tree_d<64, true>(tk, tv, p, st) : launch_tree_d<64, false>(tk, tv, p, st);
+  return fp8 ? launch_tree_d<128, true>(tk, tv, p, st) : launch_tree_d<128, false>(tk, tv, p, st);
 }
 
 }  // namespace ea46

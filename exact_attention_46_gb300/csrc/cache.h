@@ -123,10 +123,9 @@ cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, cons
                               bool combine, cudaStream_t st);
 
 cudaError_t launch_attn_tree(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
-                             bool combine, cudaStream_t st);
+                             cudaStream_t st);
 cudaError_t launch_attn_lanes(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p, int D, bool fp8,
                               cudaStream_t st);
-cudaError_t launch_tree_combine(const PagedParams& p, int D, cudaStream_t st);
 
 // Launch a kernel that may become resident while the one before it on the stream ends; it waits for that
 // one's completion (griddepcontrol.wait) before it reads or writes anything.

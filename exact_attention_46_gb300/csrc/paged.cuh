@@ -224,6 +224,28 @@ __device__ __forceinline__ void e4m3_terms4(float a, float b, float c, float d, 
 
 __device__ __forceinline__ bool finite_f(float x) { return fabsf(x) < INFINITY; }
 
+// Numerators over an E4M3 cache in the kernels on tcgen05: lazily rescaled when they pass 2^TAU (log2), scaled by
+// 2^(15 - TAU), so that the sum of their terms spans E5M2's [2^-17, 2^15]: of a sequence of 2^17 keys that lie
+// 2^-20 under one other, none is lost.  (E4M3 terms span 2^19 and lose them.)
+constexpr float TAU_E4M3 = 4.0f, TOP_E4M3 = 2048.0f;
+
+// Four numerators in [0, 2^15] as three E5M2 terms (packed bytes): fp16 first (2^-11), whose upper byte is
+// the first term, the remainder's upper byte the second, and what is left then rounded: each takes three bits
+// at least, so the sum is off by 2^-9 of the number, or 2^-17, half of E5M2's smallest step.
+__device__ __forceinline__ void e5m2_terms4(float a, float b, float c, float d, uint32_t (&t)[3]) {
+  asm("{\n\t.reg .b32 x, y, p, q, r, s;\n\t.reg .b16 u, v;\n\t"
+      "cvt.rn.f16x2.f32 x, %4, %3;\n\tcvt.rn.f16x2.f32 y, %6, %5;\n\t"
+      "prmt.b32 %0, x, y, 0x7531;\n\t"
+      "and.b32 p, x, 0xff00ff00;\n\tand.b32 q, y, 0xff00ff00;\n\t"
+      "sub.rn.f16x2 x, x, p;\n\tsub.rn.f16x2 y, y, q;\n\t"
+      "prmt.b32 %1, x, y, 0x7531;\n\t"
+      "and.b32 r, x, 0xff00ff00;\n\tand.b32 s, y, 0xff00ff00;\n\t"
+      "sub.rn.f16x2 x, x, r;\n\tsub.rn.f16x2 y, y, s;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 u, x;\n\tcvt.rn.satfinite.e5m2x2.f16x2 v, y;\n\t"
+      "mov.b32 %2, {u, v};\n\t}"
+      : "=r"(t[0]), "=r"(t[1]), "=r"(t[2]) : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
 // ---- issue and loads of the kernels on tcgen05 ----
 
 // Whether the phase with this parity has completed.

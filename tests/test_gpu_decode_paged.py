@@ -16,10 +16,11 @@ Over an E4M3 cache with more than 8 rows (group x drafts) the products run on E4
   second holds exactly unless it lies below E4M3's smallest step 2^-9: that is off by at most half
   a step, 2^-10, so by 2^-17 of the row's largest element (and only in elements below 2^-9 of
   it).  A logit moves by at most 2^-17 scale max|q| sum_d |k_jd| more;
-* a numerator times its value's scale over 2^-7 vref (vref a power of two, at most twice the largest
-  scale) is rounded to fp16 (2^-11) and to two terms: 2^-4 * 2^-4 = 2^-8 of it, or half a step, 2^-10,
-  where that is more: 2^-17 vref of the value's code, per key, over a sum of at least 1.  So
-  r = 2^-8 + 2^-11 and the last term becomes 2^-16 max scale sum_j |code_jd|.
+* a numerator times its value's scale over 2^-11 vref (vref a power of two, at most twice the largest
+  scale) is rounded to fp16 (2^-11) and to the sum of three E5M2 terms: each of the first two cuts three
+  bits off the top and the third rounds to three, 2^-9 of the number in all, or half of E5M2's smallest
+  step, 2^-17, where that is more: 2^-27 of the largest scale times the value's code, per key, over a sum
+  of at least 1.  So r = 2^-9 + 2^-11, and the last term (2^-26 448 max scale a key) covers the rest.
 What no row may see -- free rows of used pages, free pages, entries behind the page table's end -- holds
 NaN.
 """
@@ -104,7 +105,7 @@ class Problem:
         scale = 1 / np.sqrt(self.D) if scale is None else scale
         o, lse = to64(o), to64(lse)
         terms = self.fp8 and self.T * self.Hq // self.Hkv > 8
-        r = 2.0 ** -8 + 2.0 ** -11 if terms else (2.0 ** -11 if self.fp8 else 2.0 ** -8)
+        r = 2.0 ** -9 + 2.0 ** -11 if terms else (2.0 ** -11 if self.fp8 else 2.0 ** -8)
         for b in range(self.B):
             n = self.ql[b]
             if n == 0:
@@ -124,9 +125,6 @@ class Problem:
                 j = np.arange(self.L[b])
                 s = self.scale[1].cpu().numpy().transpose(0, 2, 1)[self.table[b, j // self.page], j % self.page]
                 floor = self.L[b] * 2.0 ** -26 * 448 * float(s.max())
-                if terms:
-                    codes = np.abs(v / s.astype(np.float64)[..., None]).sum(0)              # [Hkv, D]
-                    floor = floor + 2.0 ** -16 * float(s.max()) * np.repeat(codes, self.Hq // self.Hkv, 0)[None]
             tol = 2.0 ** -8 * np.abs(ref) + (r + 2 * dx.T[..., None] + 2.0 ** -18) * A + floor
             err = np.abs(o[b, :n] - ref)
             assert np.all(err <= tol), (b, float((err - tol).max()))
@@ -185,6 +183,70 @@ def test_many_sequences_share_the_ctas(T, fp8):
 def test_one_long_sequence_is_cut_over_the_device(fp8):
     p = Problem([40000], 4, 4, 1, 128, 64, fp8, False, True)
     p.check(*run(p))
+
+
+ROWS = [
+    # 9 .. 64 rows (group x drafts), at and next to the tiles of 16, 32 and 64
+    ([5, 129, 700], 9, 1, 1, 64, 32, True, [9, 0, 4]),
+    ([300, 0, 1], 3, 8, 2, 128, 16, False, None),
+    ([1000], 16, 2, 2, 128, 64, True, None),
+    ([127, 640], 17, 2, 2, 64, 1024, False, [17, 1]),
+    ([2100, 90], 8, 8, 2, 128, 128, True, [8, 8]),
+    ([250, 0, 33], 33, 1, 1, 128, 16, True, [33, 2, 20]),
+    ([60, 1500], 12, 20, 4, 128, 64, True, None),
+    ([100, 0], 64, 2, 2, 64, 64, True, [64, 63]),
+    ([64, 128, 65, 191], 64, 1, 1, 128, 32, False, [64, 64, 1, 64]),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("token_major", [False, True])
+@pytest.mark.parametrize("shape", ROWS, ids=lambda s: "x".join(str(v) for v in (s[1:6])))
+def test_row_counts_between_the_tiles(shape, token_major, fp8):
+    ctx, T, Hq, Hkv, D, page, tree, ql = shape
+    p = Problem(ctx, T, Hq, Hkv, D, page, fp8, token_major, tree, ql, case=151)
+    p.check(*run(p))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 8, 16, 40])
+def test_units_of_many_parts(T, fp8):
+    # two sequences over all CTAs, and one with short ones beside it
+    for ctx in ([9000, 20000], [30, 25000, 7]):
+        p = Problem(ctx, T, 4, 1, 64, 128, fp8, False, True, case=152)
+        p.check(*run(p))
+
+
+@pytest.mark.parametrize("T,Hq", [(1, 4), (4, 4), (8, 4), (16, 4), (40, 4)])
+def test_one_key_far_above_many(T, Hq):
+    # 40000 keys of probability 2^-19.5 beside one of nearly 1: together they are worth a twentieth
+    p = Problem([40000], T, Hq, 1, 64, 1024, fp8=True)
+    one = np.float64(np.float32(1 / 448)) * 448
+    page, at = int(p.table[0, 0]), 777
+    p.q.zero_()
+    p.q[..., 0] = 8.0
+    for i, (code, sink) in enumerate([(0x00, 0x00), (0xFE, 0x7E)]):
+        p.cache[i].fill_(code)
+        p.cache[i][page, :, at] = sink
+        p.scale[i].fill_(1 / 448)
+        p.val[i][:] = 0.0 if i == 0 else -one
+    p.cache[0][page, :, at, 0] = 0x7E
+    p.scale[0][page, :, at] = 13.5 / 448
+    p.val[0][page, :, at, 0] = np.float64(np.float32(13.5 / 448)) * 448
+    p.val[1][page, :, at] = one
+    p.check(*run(p, scale=0.125), scale=0.125)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 6, 16, 40])
+def test_an_infinite_query_element_stays_in_its_row(T, fp8):
+    p = Problem([200, 70], T, 4, 1, 64, 32, fp8, tree=True)
+    clean = run(p)
+    p.q[1, T - 1, 2, 5] = float("inf")
+    o, lse = run(p)
+    assert torch.isnan(o[1, T - 1, 2]).all()
+    o[1, T - 1, 2], lse[1, 2, T - 1] = clean[0][1, T - 1, 2], clean[1][1, 2, T - 1]
+    assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
 
 
 def test_logits_far_apart_and_a_given_scale():
