@@ -492,3 +492,106 @@ def test_each_launch_sees_the_one_before(T, fp8):
         ops.check()
         for rep in range(3):
             assert torch.equal(got[6 * rep + i][0], want[0]) and torch.equal(got[6 * rep + i][1], want[1]), (rep, i)
+
+
+KINDS = [(1, 8, 2, False), (4, 8, 2, False), (8, 8, 2, False), (16, 8, 2, False), (40, 8, 2, False), (1, 8, 2, True), (3, 8, 2, True),
+         (8, 8, 2, True), (16, 8, 2, True), (40, 8, 2, True)]      # T, Hq, Hkv, fp8: each kernel and row tile
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,fp8", KINDS)
+def test_calls_on_two_streams_at_once(T, Hq, Hkv, fp8):
+    p = [Problem(c, T, Hq, Hkv, 128, 64, fp8, tree=True, case=155 + i) for i, c in enumerate([[2000, 90, 700], [30, 5000]])]
+    args = [x.args() for x in p]
+    want = [ops.attn_decode_paged(*a, **kw) for a, kw in args]
+    ops.check()
+    need = [ops.decode_paged_workspace_bytes(x.B, T, Hq, Hkv, 128, 64, x.max_pages) for x in p]
+    streams = [torch.cuda.Stream() for _ in p]
+    for i, x in enumerate(p):
+        streams[i].wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in need]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, (a, kw) in enumerate(args):
+            got[i].append(ops.attn_decode_paged(*a, workspace=ws[i], stream=streams[i], **kw))
+    torch.cuda.synchronize()
+    ops.check()
+    for w, outs in zip(want, got):
+        for o, lse in outs:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,fp8", KINDS)
+def test_the_workspace_is_not_left(T, Hq, Hkv, fp8):
+    p = Problem([9000, 40, 1300], T, Hq, Hkv, 64, 32, fp8, tree=True)
+    need = ops.decode_paged_workspace_bytes(p.B, T, Hq, Hkv, 64, 32, p.max_pages)
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    p.check(*run(p, workspace=ws[:need]))
+    assert torch.all(ws[need:] == 0xA5)
+    with pytest.raises(_lib.AttnError):
+        run(p, workspace=ws[:need - 16])
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,fp8", KINDS)
+def test_two_graphs_share_a_workspace(T, Hq, Hkv, fp8):
+    p = [Problem(c, T, Hq, Hkv, 128, 128, fp8, tree=True, case=157 + i) for i, c in enumerate([[4000, 90], [130, 2500]])]
+    args = [x.args() for x in p]
+    want = [ops.attn_decode_paged(*a, **kw) for a, kw in args]
+    ops.check()
+    ws = torch.empty(max(ops.decode_paged_workspace_bytes(x.B, T, Hq, Hkv, 128, 128, x.max_pages) for x in p),
+                     dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for a, kw in args:
+        o = torch.empty_like(want[len(outs)][0]), torch.empty_like(want[len(outs)][1])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ops.attn_decode_paged(*a, workspace=ws, out=o[0], lse=o[1], **kw)
+        graphs.append(g)
+        outs.append(o)
+    for _ in range(5):
+        for o in outs:
+            o[0].zero_()
+            o[1].zero_()
+        for g in graphs:
+            g.replay()
+        ops.check()
+        for o, w in zip(outs, want):
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,fp8", KINDS)
+def test_what_lies_outside_is_refused_by_every_kernel(T, Hq, Hkv, fp8):
+    # a page outside the cache is reported and not read; lengths out of range write nothing
+    p = Problem([700, 90], T, Hq, Hkv, 64, 64, fp8, tree=True)
+    clean = run(p)
+    good = p.table.copy()
+    p.table[0, 3] = p.n_pages
+    a, kw = p.args()
+    o = torch.full_like(clean[0], 5.0)
+    lse = torch.full_like(clean[1], 6.0)
+    ops.attn_decode_paged(*a, out=o, lse=lse, **kw)
+    with pytest.raises(_lib.AttnError, match="page"):
+        ops.check()
+    assert torch.equal(o[1], clean[0][1]) and torch.equal(lse[1], clean[1][1])
+    p.table[:] = good
+    p.ctx[0] = p.max_pages * p.page + 1
+    a, kw = p.args()
+    o.fill_(5.0)
+    lse.fill_(6.0)
+    ops.attn_decode_paged(*a, out=o, lse=lse, **kw)
+    with pytest.raises(_lib.AttnError):
+        ops.check()
+    assert torch.all(o == 5.0) and torch.all(lse == 6.0)
+    p.ctx[0] = 700
+    again = run(p)
+    assert torch.equal(again[0], clean[0]) and torch.equal(again[1], clean[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 5, 20, 33])
+def test_a_thousand_sequences(T, fp8):
+    rng = np.random.default_rng(159)
+    ctx = rng.integers(0, 200, 1024).tolist()
+    ql = rng.integers(0, T + 1, 1024).tolist()
+    p = Problem(ctx, T, 3, 1, 64, 128, fp8, False, True, ql, case=160)
+    p.check(*run(p))
