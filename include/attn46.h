@@ -463,7 +463,8 @@ int rope_apply(const void* x, void* out, const float* rope_cs, const int* positi
  *   Rows no slot names are left as they are.
  *
  * rope_kv_cache_append -- the same with rope_apply's rotation of q and k in front, in one launch:
- *   q_out [n_tokens, Hq, D] bf16 gets the rotated q of every token (padded ones too); the keys are rotated in fp32 and rounded once, into the cache; v is not rotated.
+ *   q_out [n_tokens, Hq, D] bf16 gets the rotated q of every token (padded ones too); the keys are
+ *   rotated in fp32 and rounded once, into the cache; v is not rotated.
  *   positions: int32 [n_tokens], required; a token whose position lies outside the table is
  *   reported and its q_out row and key are not written.
  */
@@ -503,7 +504,10 @@ int kv_cache_gather(const void* k_cache, const void* v_cache, const float* k_sca
  *   page_table: int32 [B, max_pages]; entries behind a sequence's last key are not read.
  *   Query head h reads key/value head h / (Hq / Hkv).  Rows t >= q_lens[b] of o and lse are left as
  *   they are; a row that sees no key gets o = 0 and lse = -inf.  What a row does not see never
- *   reaches it, whatever its bytes hold.
+ *   reaches it, whatever its bytes hold; of E4M3 rows that some rows of the sequence see, one that holds a
+ *   NaN code must have a scale that is not finite, as kv_cache_append writes it.
+ *   Numerators are rounded to bf16, or over an E4M3 cache to fp16 (up to 8 query rows per key/value head) or to 2^-9
+ *   of their size; sums and softmax statistics are fp32.  An infinite query element gives its row NaN.
  *   B <= 1024, T <= 64.  scale : as attn_fwd.
  *   workspace : attn_decode_paged_workspace_bytes(...) bytes of device scratch, 16-byte aligned,
  *               overwritten (NULL when that is 0); calls whose kernels may overlap need their own.
