@@ -47,7 +47,7 @@ struct AppendParams {
   long long q_stride, k_stride, v_stride;           // elements between tokens
   const long long* slots;                           // [n_tokens] page * page_size + offset, < 0: none
   int n_tokens, Hq;
-  unsigned q_blocks;    // blocks that rotate queries (set by the launch)
+  unsigned long long kv_step;                       // blocks for keys and values, of 2^32 (set by the launch)
   CacheView cache;
   RopeParams rope;
   int* err_word;

@@ -25,12 +25,11 @@ namespace ea46 {
 
 namespace {
 
-// Rows (heads of one token) a lane group works on at once, and blocks of 256 threads an SM is compiled for
-// (64 registers).  Measured, us: 2 rows instead of 4 takes the rotation of 16384 x 16 x 128 from 20.3 to
-// 22.7 and the E4M3 write of 16384 tokens (32 + 2 x 8 heads of 128) from 63.7 to 69.2; three blocks
-// instead of four give 21.7 and 65.8.
-constexpr int HEADS = 4, BLOCKS_PER_SM = 4;
-constexpr int THREADS = 256;
+// Rows (heads of one token) a lane group works on at once, threads of a block and blocks an SM is compiled for (64
+// registers).  Measured, us: 2 rows instead of 4 takes the rotation of 16384 x 16 x 128 from 20.3 to 22.7 and the
+// E4M3 write of 16384 tokens (32 + 2 x 8 heads of 128) from 63.7 to 69.2; three quarters of the threads give 21.7
+// and 65.8; blocks of 256 threads 20.1 and 63.4 against 19.8 and 62.2 of 128 (and of 64).
+constexpr int HEADS = 4, THREADS = 128, BLOCKS_PER_SM = 8;
 enum : int { WHERE_ROPE_POS = 41, WHERE_APPEND_SLOT = 42, WHERE_GATHER = 43 };
 
 __device__ __forceinline__ void note_bad(int* err_word, int* err_info, int where) {
@@ -177,13 +176,16 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_PER_SM) cache_append_kernel(co
   grid_dependency_wait();       // everything below reads what earlier kernels may have written
   constexpr int LPR = D / 16;
   const int l = threadIdx.x % LPR;
-  // the first q_blocks blocks take the queries, the rest keys and values: a block's groups do like work
-  const bool queries = blockIdx.x < p.q_blocks;
+  // A block's groups do like work, queries or keys and values, and the two kinds of blocks take turns: the
+  // quantiser's instructions run beside the queries' loads, and a token's kinds read its cos and sin
+  // soon after each other (62.2 us to 59.1; queries first, then the others).
+  const uint32_t kv_before = static_cast<uint32_t>((blockIdx.x * p.kv_step) >> 32);
+  const bool queries = kv_before == static_cast<uint32_t>(((blockIdx.x + 1ull) * p.kv_step) >> 32);
   const int nkv = (p.cache.Hkv + HEADS - 1) / HEADS;
   uint32_t t;
   int sub;
-  if (queries) item_of(blockIdx.x, LPR, (p.Hq + HEADS - 1) / HEADS, t, sub);
-  else item_of(blockIdx.x - p.q_blocks, LPR, 2 * nkv, t, sub);
+  if (queries) item_of(blockIdx.x - kv_before, LPR, (p.Hq + HEADS - 1) / HEADS, t, sub);
+  else item_of(kv_before, LPR, 2 * nkv, t, sub);
   if (t >= static_cast<uint32_t>(p.n_tokens)) return;
   const int which = queries ? 0 : (sub < nkv ? 1 : 2);                // q, k, v
   const int h0 = (which == 2 ? sub - nkv : sub) * HEADS;
@@ -366,8 +368,10 @@ cudaError_t rope_d(const RopeApplyParams& p, bool half, cudaStream_t st) {
 
 template <int D>
 cudaError_t append_d(AppendParams p, bool half, cudaStream_t st) {
-  p.q_blocks = p.q != nullptr ? blocks_for((p.Hq + HEADS - 1) / HEADS, p.n_tokens, D) : 0;
-  const unsigned grid = p.q_blocks + blocks_for(2 * ((p.cache.Hkv + HEADS - 1) / HEADS), p.n_tokens, D);
+  const unsigned q_blocks = p.q != nullptr ? blocks_for((p.Hq + HEADS - 1) / HEADS, p.n_tokens, D) : 0;
+  const unsigned kv_blocks = blocks_for(2 * ((p.cache.Hkv + HEADS - 1) / HEADS), p.n_tokens, D), grid = q_blocks + kv_blocks;
+  // rounded up: floor(grid * kv_step / 2^32) is kv_blocks
+  p.kv_step = ((static_cast<unsigned long long>(kv_blocks) << 32) + grid - 1) / grid;
   const bool fp8 = p.cache.k_scale != nullptr;
   void (*kernel)(AppendParams) = half ? (fp8 ? cache_append_kernel<D, true, true> : cache_append_kernel<D, true, false>)
                                       : (fp8 ? cache_append_kernel<D, false, true> : cache_append_kernel<D, false, false>);
