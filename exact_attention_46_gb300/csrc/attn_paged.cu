@@ -878,7 +878,9 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p)
 template <int D, int RB>
 cudaError_t launch_paged_combine(const PagedParams& p, cudaStream_t st) {
   if (p.n_cta < 2) return cudaSuccess;
-  return launch_overlapped(paged_combine_kernel<D, RB>, dim3(static_cast<unsigned>(p.n_cta - 1) * p.row_tiles, RB / COMBINE_ROWS<RB>),
+  const int rows = p.G * p.T < RB ? p.G * p.T : RB;
+  return launch_overlapped(paged_combine_kernel<D, RB>,
+                           dim3(static_cast<unsigned>(p.n_cta - 1) * p.row_tiles, (rows + COMBINE_ROWS<RB> - 1) / COMBINE_ROWS<RB>),
                            256, 0, st, p);
 }
 

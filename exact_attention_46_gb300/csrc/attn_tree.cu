@@ -253,22 +253,23 @@ __global__ void __launch_bounds__(TREE_THREADS, 1)
     // the last segment's S = Q K^T are complete.
     auto fetch = [&](int rt, long long& x) -> bool {
       if (!next_segment(p, pre, x, x1, sg)) return false;
-      ctx = *(p.ctx_lens + sg.b);
-      ql = p.q_lens != nullptr ? *(p.q_lens + sg.b) : p.T;
       const int pr = rt * PAGED_TREE_ROWS + r, t = token_of(p, pr);
       const bool there = t < p.T;
+      // this half of the row, all of it on its way before anything is waited for: behind the first K and V tiles in
+      // the memory's queues it takes 3 us longer
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(p.q) +
+          ((static_cast<long long>(sg.b) * p.T + t) * p.Hq + sg.hkv * p.G + pr - t * p.G) * D);
+      uint4 u[D / 16];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) u[i] = there ? src[hf * (D / 16) + i] : make_uint4(0u, 0u, 0u, 0u);
+      ctx = *(p.ctx_lens + sg.b);
+      ql = p.q_lens != nullptr ? *(p.q_lens + sg.b) : p.T;
       bits = 0;
       if (there)
         bits = p.tree_mask != nullptr ? *(p.tree_mask + static_cast<long long>(sg.b) * p.T + t)
                                       : (t >= 63 ? ~0ull : (2ull << t) - 1);
       if (ql < 64) bits &= (1ull << ql) - 1;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(p.q) +
-          ((static_cast<long long>(sg.b) * p.T + t) * p.Hq + sg.hkv * p.G + pr - t * p.G) * D);
-      // this half of the row, all of it on its way before the first use
-      uint4 u[D / 16];
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) u[i] = there ? src[hf * (D / 16) + i] : make_uint4(0u, 0u, 0u, 0u);
       if constexpr (!FP8) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
