@@ -90,7 +90,7 @@ class AttnError(RuntimeError):
 
 def call(name, *args):
     """Call an entry point that returns an attn_status; raise AttnError unless ATTN_OK."""
-    lib = load()
+    lib = load() if _lib is None else _lib
     rc = getattr(lib, name)(*args)
     if rc != 0:
         raise AttnError(rc, lib.attn_get_last_error().decode(errors="replace"))

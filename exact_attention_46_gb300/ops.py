@@ -519,13 +519,15 @@ def selftest_bounded_wait(cycles, stream=None):
 # their host time counts: a tensor that is as expected is found so by one look at its dtype, shape,
 # device and contiguity, and _arg says what is wrong with any other.
 
-# torch.cuda.current_stream() builds a Stream object (about 3 us); the raw handle does not
+# torch.cuda.current_stream() builds a Stream object (about 3 us), current_device() looks whether CUDA is up
+# (a tensor on it says so); the raw handle and number do not
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _run(index, stream, name, *args):
     """Call `name` with the stream appended, with device `index` current."""
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(index):
             return _run(index, stream, name, *args)
     if stream is not None:
@@ -537,26 +539,39 @@ def _run(index, stream, name, *args):
     return _lib.call(name, *args, raw)
 
 
-def _new(shape, dtype, dev, stream):
+def _new(shape, dtype, index, stream):
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=index)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=index)
 
 
-def _is(t, name, dtype, shape, dev):
-    """Check one tensor (exact dtype and shape, contiguous, device `dev`); its address."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev
-            or not t.is_contiguous()):
-        _arg(t, name, (dtype,), shape=shape, device=dev)
-    return t.data_ptr()
+def _is(t, name, dtype, shape, index):
+    """Check one tensor (exact dtype and shape, contiguous, on CUDA device `index`); its address."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _arg(t, name, (dtype,), shape=shape, device=torch.device("cuda", index)).data_ptr()
 
 
-def _is_opt(t, name, dtype, shape, dev):
-    return None if t is None else _is(t, name, dtype, shape, dev)
+def _is_opt(t, name, dtype, shape, index):
+    return None if t is None else _is(t, name, dtype, shape, index)
 
 
-def _rows(t, name, heads=None, D=None, device=None):
+def _is_dim(t, name, dtypes, dim, index=None):
+    """Check one tensor of `dim` dimensions, the first argument where no device index is given; its index."""
+    try:
+        at = t.get_device()
+        if t.dtype in dtypes and len(t.shape) == dim and at >= 0 and (index is None or at == index) and t.is_contiguous():
+            return at
+    except AttributeError:
+        pass
+    return _arg(t, name, dtypes, dim=dim, device=None if index is None else torch.device("cuda", index)).get_device()
+
+
+def _rows(t, name, heads=None, D=None, index=None):
     """Check rows of heads ([tokens, heads, D], or [B, S, heads, D]): bf16 on a CUDA device, heads and
     D contiguous, tokens evenly spaced (a view of a fused projection).  Returns (tokens, stride)."""
     if not isinstance(t, torch.Tensor):
@@ -567,45 +582,51 @@ def _rows(t, name, heads=None, D=None, device=None):
     n = len(sh)
     if n not in (3, 4):
         raise ValueError(f"{name}: expected 3 or 4 dimensions, got shape {tuple(sh)}")
-    if (heads is not None and sh[-2] != heads) or (D is not None and sh[-1] != D):
+    h, d = sh[-2], sh[-1]
+    if (heads is not None and h != heads) or (D is not None and d != D):
         raise ValueError(f"{name}: expected {heads} heads of {D}, got shape {tuple(sh)}")
-    if (st[-1] != 1 and sh[-1] > 1) or (st[-2] != sh[-1] and sh[-2] > 1):
+    if (st[-1] != 1 and d > 1) or (st[-2] != d and h > 1):
         raise ValueError(f"{name}: heads must be contiguous within a token")
     if n == 4 and sh[0] > 1 and sh[1] > 1 and st[0] != sh[1] * st[1]:
         raise ValueError(f"{name}: tokens must be evenly spaced")
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
-    tokens = sh[0] if n == 3 else sh[0] * sh[1]
-    if tokens <= 1:
-        return tokens, sh[-2] * sh[-1]
-    return tokens, (st[-3] if sh[-3] > 1 else st[0])
+    if index is not None and at != index:
+        raise ValueError(f"{name} is on {t.device}, the other arguments on {torch.device('cuda', index)}")
+    if n == 3:
+        return sh[0], (st[0] if sh[0] > 1 else h * d)
+    tokens = sh[0] * sh[1]
+    return tokens, (h * d if tokens <= 1 else (st[1] if sh[1] > 1 else st[0]))
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev):
+def _cache(k_cache, v_cache, k_scale, v_scale, token_major, index):
     """Check a paged cache; returns ((n_pages, page_size, Hkv, D, layout, dtype), (addresses))."""
-    _arg(k_cache, "k_cache", _BF16 + _CODES, dim=4, device=dev)
+    _is_dim(k_cache, "k_cache", _BF16 + _CODES, 4, index)
     shape, dtype = k_cache.shape, k_cache.dtype
-    pv = _is(v_cache, "v_cache", dtype, shape, dev)
-    n_pages, a, b, D = shape
-    page, Hkv = (a, b) if token_major else (b, a)
+    pv = _is(v_cache, "v_cache", dtype, shape, index)
+    if token_major:
+        n_pages, page, Hkv, D = shape
+        layout = 1
+    else:
+        n_pages, Hkv, page, D = shape
+        layout = 0
     if dtype is not torch.bfloat16:
         sh = (n_pages, Hkv, page)
-        return ((n_pages, page, Hkv, D, int(bool(token_major)), ATTN_FP8_E4M3),
-                (k_cache.data_ptr(), pv, _is(k_scale, "k_scale", torch.float32, sh, dev),
-                 _is(v_scale, "v_scale", torch.float32, sh, dev)))
+        return ((n_pages, page, Hkv, D, layout, ATTN_FP8_E4M3),
+                (k_cache.data_ptr(), pv, _is(k_scale, "k_scale", torch.float32, sh, index),
+                 _is(v_scale, "v_scale", torch.float32, sh, index)))
     if k_scale is not None or v_scale is not None:
         raise ValueError("k_scale and v_scale go with an E4M3 cache")
-    return (n_pages, page, Hkv, D, int(bool(token_major)), ATTN_BF16), (k_cache.data_ptr(), pv, None, None)
+    return (n_pages, page, Hkv, D, layout, ATTN_BF16), (k_cache.data_ptr(), pv, None, None)
 
 
-def _table_rot(rope_cs, dev):
+def _table_rot(rope_cs, index):
     sh = getattr(rope_cs, "shape", ())
     if len(sh) != 3 or sh[2] != 2:
-        _arg(rope_cs, "rope_cs", _F32, dim=3, device=dev)
+        _arg(rope_cs, "rope_cs", _F32, dim=3, device=torch.device("cuda", index))
         raise ValueError(f"rope_cs: expected shape (n_pos, rot_dim / 2, 2), got {tuple(sh)}")
-    return _is(rope_cs, "rope_cs", torch.float32, sh, dev), sh[0], 2 * sh[1]
+    return _is(rope_cs, "rope_cs", torch.float32, sh, index), sh[0], 2 * sh[1]
 
 
 def rope_scaled_table(n_pos, rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=0, device="cuda",
@@ -618,7 +639,7 @@ def rope_scaled_table(n_pos, rot_dim, base=10000.0, scaling="none", factor=1.0, 
     _opt(out, "out", _F32, shape=(n_pos, rot_dim // 2, 2))
     if out is None:
         out = _new((n_pos, rot_dim // 2, 2), torch.float32, torch.device(device), stream)
-    _run(out.device.index, stream, "rope_scaled_table", _ptr(out), int(n_pos), int(rot_dim), float(base),
+    _run(out.get_device(), stream, "rope_scaled_table", _ptr(out), int(n_pos), int(rot_dim), float(base),
          ROPE_SCALING[scaling], float(factor), float(original_length))
     return out
 
@@ -630,19 +651,19 @@ def rope_apply(x, rope_cs, positions=None, half=False, transpose=False, out=None
     (2i, 2i+1).  ``transpose``: the gradient with respect to x of an output gradient x.  ``out``: may
     be x itself."""
     tokens, stride = _rows(x, "x")
-    dev, shape = x.device, x.shape
-    H, D = shape[-2:]
-    pc, n_pos, rot = _table_rot(rope_cs, dev)
-    pp = _is_opt(positions, "positions", torch.int32, shape[:-2], dev)
+    index, shape = x.get_device(), x.shape
+    H, D = shape[-2], shape[-1]
+    pc, n_pos, rot = _table_rot(rope_cs, index)
+    pp = _is_opt(positions, "positions", torch.int32, shape[:-2], index)
     if out is None:
-        out = _new(shape, torch.bfloat16, dev, stream)
+        out = _new(shape, torch.bfloat16, index, stream)
         out_stride = H * D
     else:
-        _, out_stride = _rows(out, "out", device=dev)
+        _, out_stride = _rows(out, "out", index=index)
         if out.shape != shape:
             raise ValueError(f"out: expected shape {tuple(shape)}, got {tuple(out.shape)}")
-    _run(dev.index, stream, "rope_apply", x.data_ptr(), out.data_ptr(), pc, pp, tokens, shape[-3], H, D, stride,
-         out_stride, n_pos, rot, int(bool(half)), int(bool(transpose)))
+    _run(index, stream, "rope_apply", x.data_ptr(), out.data_ptr(), pc, pp, tokens, shape[-3], H, D, stride,
+         out_stride, n_pos, rot, 1 if half else 0, 1 if transpose else 0)
     return out
 
 
@@ -652,15 +673,15 @@ def kv_cache_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, t
     [n_pages, Hkv, page_size, D] (``token_major``: [n_pages, page_size, Hkv, D]), bf16 or E4M3 with one
     scale per row (fp32 [n_pages, Hkv, page_size])."""
     tokens, ks = _rows(k, "k")
-    dev = k.device
-    (n_pages, page, Hkv, D, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    index = k.get_device()
+    (n_pages, page, Hkv, D, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, index)
     if k.shape[-2:] != (Hkv, D):
         _rows(k, "k", Hkv, D)
-    tv, vs = _rows(v, "v", Hkv, D, dev)
+    tv, vs = _rows(v, "v", Hkv, D, index)
     if tv != tokens:
         raise ValueError(f"k holds {tokens} tokens, v {tv}")
-    sl = _is(slots, "slots", torch.int64, (tokens,), dev)
-    _run(dev.index, stream, "kv_cache_append", k.data_ptr(), v.data_ptr(), *cache, sl, tokens, Hkv, D, ks, vs, n_pages,
+    sl = _is(slots, "slots", torch.int64, (tokens,), index)
+    _run(index, stream, "kv_cache_append", k.data_ptr(), v.data_ptr(), *cache, sl, tokens, Hkv, D, ks, vs, n_pages,
          page, layout, dtype)
 
 
@@ -669,23 +690,23 @@ def rope_kv_cache_append(q, k, v, rope_cs, positions, k_cache, v_cache, slots, k
     """``rope_apply`` on q [tokens, Hq, D] and k, then ``kv_cache_append`` of k and v, in one launch.
     ``positions``: int32 [tokens].  Returns the rotated q."""
     tokens, qs = _rows(q, "q")
-    dev = q.device
-    (n_pages, page, Hkv, D, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    index = q.get_device()
+    (n_pages, page, Hkv, D, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, index)
     Hq = q.shape[-2]
     if q.shape[-1] != D:
         _rows(q, "q", Hq, D)
-    tk, ks = _rows(k, "k", Hkv, D, dev)
-    tv, vs = _rows(v, "v", Hkv, D, dev)
+    tk, ks = _rows(k, "k", Hkv, D, index)
+    tv, vs = _rows(v, "v", Hkv, D, index)
     if not tokens == tk == tv:
         raise ValueError(f"q, k and v hold {tokens}, {tk} and {tv} tokens")
-    pc, n_pos, rot = _table_rot(rope_cs, dev)
-    pp = _is(positions, "positions", torch.int32, (tokens,), dev)
-    sl = _is(slots, "slots", torch.int64, (tokens,), dev)
+    pc, n_pos, rot = _table_rot(rope_cs, index)
+    pp = _is(positions, "positions", torch.int32, (tokens,), index)
+    sl = _is(slots, "slots", torch.int64, (tokens,), index)
     if q_out is None:
-        q_out = _new(q.shape, torch.bfloat16, dev, stream)
-    po = _is(q_out, "q_out", torch.bfloat16, q.shape, dev)
-    _run(dev.index, stream, "rope_kv_cache_append", q.data_ptr(), k.data_ptr(), v.data_ptr(), po, pc, pp, *cache, sl,
-         tokens, Hq, Hkv, D, qs, ks, vs, n_pages, page, layout, dtype, n_pos, rot, int(bool(half)))
+        q_out = _new(q.shape, torch.bfloat16, index, stream)
+    po = _is(q_out, "q_out", torch.bfloat16, q.shape, index)
+    _run(index, stream, "rope_kv_cache_append", q.data_ptr(), k.data_ptr(), v.data_ptr(), po, pc, pp, *cache, sl,
+         tokens, Hq, Hkv, D, qs, ks, vs, n_pages, page, layout, dtype, n_pos, rot, 1 if half else 0)
     return q_out
 
 
@@ -693,17 +714,18 @@ def kv_cache_gather(k_cache, v_cache, page_table, cu_seqlens, total, k_scale=Non
                     k_out=None, v_out=None, stream=None):
     """Packed bf16 keys and values [total, Hkv, D] of sequences in a paged cache: ``page_table`` int32
     [n_seq, max_pages], ``cu_seqlens`` int32 [n_seq + 1] (0 .. total)."""
-    dev = _arg(k_cache, "k_cache", _BF16 + _CODES, dim=4).device
-    (n_pages, page, Hkv, D, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
-    pt = _arg(page_table, "page_table", _I32, dim=2, device=dev).data_ptr()
+    index = _is_dim(k_cache, "k_cache", _BF16 + _CODES, 4)
+    (n_pages, page, Hkv, D, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, index)
+    _is_dim(page_table, "page_table", _I32, 2, index)
+    pt = page_table.data_ptr()
     n_seq, max_pages = page_table.shape
-    cu = _is(cu_seqlens, "cu_seqlens", torch.int32, (n_seq + 1,), dev)
+    cu = _is(cu_seqlens, "cu_seqlens", torch.int32, (n_seq + 1,), index)
     total = int(total)
     shape = (total, Hkv, D)
-    k_out = _new(shape, torch.bfloat16, dev, stream) if k_out is None else k_out
-    v_out = _new(shape, torch.bfloat16, dev, stream) if v_out is None else v_out
-    pk, pv = _is(k_out, "k_out", torch.bfloat16, shape, dev), _is(v_out, "v_out", torch.bfloat16, shape, dev)
-    _run(dev.index, stream, "kv_cache_gather", *cache, pt, cu, pk, pv, n_seq, total, Hkv, D, n_pages, page, max_pages,
+    k_out = _new(shape, torch.bfloat16, index, stream) if k_out is None else k_out
+    v_out = _new(shape, torch.bfloat16, index, stream) if v_out is None else v_out
+    pk, pv = _is(k_out, "k_out", torch.bfloat16, shape, index), _is(v_out, "v_out", torch.bfloat16, shape, index)
+    _run(index, stream, "kv_cache_gather", *cache, pt, cu, pk, pv, n_seq, total, Hkv, D, n_pages, page, max_pages,
          layout, dtype)
     return k_out, v_out
 
@@ -722,32 +744,36 @@ def attn_decode_paged(q, k_cache, v_cache, page_table, ctx_lens, k_scale=None, v
     ``q_lens`` int32 [B]: drafted tokens of each sequence (None: T); ``tree_mask`` int64 [B, T]: bit i of
     entry (b, t) lets drafted token t see drafted token i (None: i <= t).  Returns (o [B, T, Hq, D]
     bf16, lse fp32 [B, Hq, T] or None); rows t >= q_lens[b] are not written."""
-    dev = _arg(q, "q", _BF16, dim=4).device
+    index = _is_dim(q, "q", _BF16, 4)
     B, T, Hq, D = q.shape
-    (n_pages, page, Hkv, Dc, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, dev)
+    (n_pages, page, Hkv, Dc, layout, dtype), cache = _cache(k_cache, v_cache, k_scale, v_scale, token_major, index)
     if Dc != D:
         raise ValueError(f"q has head dimension {D}, the cache {Dc}")
-    pt = _arg(page_table, "page_table", _I32, dim=2, device=dev).data_ptr()
+    _is_dim(page_table, "page_table", _I32, 2, index)
+    pt = page_table.data_ptr()
     rows, max_pages = page_table.shape
     if rows != B:
         raise ValueError(f"page_table: expected {B} rows, got shape {tuple(page_table.shape)}")
-    pc = _is(ctx_lens, "ctx_lens", torch.int32, (B,), dev)
-    pl = _is_opt(q_lens, "q_lens", torch.int32, (B,), dev)
-    pm = _is_opt(tree_mask, "tree_mask", torch.int64, (B, T), dev)
+    pc = _is(ctx_lens, "ctx_lens", torch.int32, (B,), index)
+    pl = _is_opt(q_lens, "q_lens", torch.int32, (B,), index)
+    pm = _is_opt(tree_mask, "tree_mask", torch.int64, (B, T), index)
     if workspace is None:
-        with torch.cuda.device(dev):
+        if index == _current_device():
             wsb = decode_paged_workspace_bytes(B, T, Hq, Hkv, D, page, max_pages)
-        workspace = _new((wsb,), torch.uint8, dev, stream) if wsb else None
+        else:
+            with torch.cuda.device(index):
+                wsb = decode_paged_workspace_bytes(B, T, Hq, Hkv, D, page, max_pages)
+        workspace = _new((wsb,), torch.uint8, index, stream) if wsb else None
     else:
-        if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        wsb = workspace.numel() * workspace.element_size()
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
+        wsb = workspace.nbytes
     if out is None:
-        out = _new(q.shape, torch.bfloat16, dev, stream)
+        out = _new(q.shape, torch.bfloat16, index, stream)
     if lse is None and want_lse:
-        lse = _new((B, Hq, T), torch.float32, dev, stream)
-    po = _is(out, "out", torch.bfloat16, q.shape, dev)
-    ps = _is_opt(lse, "lse", torch.float32, (B, Hq, T), dev)
-    _run(dev.index, stream, "attn_decode_paged", q.data_ptr(), *cache, po, ps, pt, pc, pl, pm,
+        lse = _new((B, Hq, T), torch.float32, index, stream)
+    po = _is(out, "out", torch.bfloat16, q.shape, index)
+    ps = _is_opt(lse, "lse", torch.float32, (B, Hq, T), index)
+    _run(index, stream, "attn_decode_paged", q.data_ptr(), *cache, po, ps, pt, pc, pl, pm,
          workspace.data_ptr() if wsb else None, wsb, B, T, Hq, Hkv, D, n_pages, page, max_pages, layout, dtype, float(scale))
     return out, lse
