@@ -400,7 +400,7 @@ int rope_hadamard_rotate_quant_fp8(const void* x, const float* rope_cs, int n_po
  *   per row -- a row is one token's one head, so a token can be written without its neighbours:
  *     ATTN_CACHE_HEAD_MAJOR   [n_pages, Hkv, page_size, D]
  *     ATTN_CACHE_TOKEN_MAJOR  [n_pages, page_size, Hkv, D]
- *     k_scale, v_scale        [n_pages, Hkv, page_size] fp32 (E4M3), NULL (bf16)
+ *     k_scale, v_scale        [n_pages, Hkv, page_size] fp32 (E4M3; not negative), NULL (bf16)
  *   16-byte aligned, contiguous.  Key j of a sequence lies in page page_table[seq][j / page_size]
  *   at offset j % page_size.  Page tables, lengths, slots and positions are device memory, so
  *   their contents are checked by the kernels: what lies outside the cache or the table is neither
