@@ -918,8 +918,9 @@ cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, cons
   if (rb == PAGED_TREE_ROWS) {
     e = launch_attn_tree(tk, tv, p, D, fp8, st);
   } else if (rb == 64 || (fp8 && rb > 8)) {
-    // Rows of 16 sequences of up to 8192 keys, and of 700, there and here: 16 of E4M3 46.0 and 46.5 us (15.6, 16.6),
-    // 32 50.0 and 72.5; 8 of E4M3 45.9 and 42.2; 16 of bf16 77.8 and 75.9 (18.9, 16.9), 32 79.3 and 77.0 (22.0, 18.6).
+    // 16 sequences of up to 8192 keys, and of 700, there and in this file's kernel: 4 rows of E4M3 43.8 and 42.2 us
+    // (14.9, 12.2), 16 45.5 and 46.5 (15.6, 16.6), 32 50.1 and 72.5; of bf16 16 rows 77.8 and 74.8 (18.9, 16.9), 32 79.3
+    // and 76.1 (22.0, 18.6).
     e = launch_attn_lanes(tk, tv, p, D, fp8, st);
   } else if (fp8) {
     e = D == 64 ? launch_paged_d<64, true, 1, false>(tk, tv, p, st) : launch_paged_d<128, true, 1, false>(tk, tv, p, st);
