@@ -23,7 +23,7 @@
 // Every mbarrier wait is bounded.
 //
 // Measured on 16 sequences of up to 8192 keys, 8 key/value heads, D = 128 (240 MB of E4M3, 35.5 us at the copy rate):
-// 16 rows 45.9 us, 32 50.1, 64 79; 64 rows of bf16 (465 MB, 69.3 us) 82.5.  Three sequences of up to 65536 keys, 32
+// 16 rows 45.5 us, 32 50.1, 64 79; 64 rows of bf16 (465 MB, 69.3 us) 81.2.  Three sequences of up to 65536 keys, 32
 // rows of E4M3 (345 MB, 50.8 us): 62.4.  Up to 32 rows a tile takes 1400 to 1600 cycles, HBM's share of an SM; with 64
 // the way of a tile through the softmax, 2600 cycles of which about half are waits, is longer.  The first logits
 // come 4 us after the launch may start and a unit's first tile takes 1 to 2 us more, its code being cold.

@@ -37,7 +37,7 @@
 // Every mbarrier wait is bounded.
 //
 // Measured: 16 sequences of up to 8192 keys, 32 query and 8 key/value heads, D = 128, T = 1: E4M3 42 us for
-// 240 MB (5.7 TB/s; 35.4 us at the copy rate), bf16 72.7 us for 465 MB (6.4 TB/s; 68.6 us).  HBM bounds the middle;
+// 240 MB (5.7 TB/s; 35.4 us at the copy rate), bf16 71.4 us for 465 MB (6.5 TB/s; 68.6 us).  HBM bounds the middle;
 // the first logits come 4 us after the launch may start (lengths, page numbers and the first tile are three
 // dependent reads), and the merge ends 3 us after the last tile.  One sequence of 1000 keys takes 7 us, all of it such steps.
 #include <atomic>
