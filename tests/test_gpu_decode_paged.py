@@ -595,3 +595,25 @@ def test_a_thousand_sequences(T, fp8):
     ql = rng.integers(0, T + 1, 1024).tolist()
     p = Problem(ctx, T, 3, 1, 64, 128, fp8, False, True, ql, case=160)
     p.check(*run(p))
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,fp8", KINDS)
+def test_no_drafts_at_all(T, Hq, Hkv, fp8):
+    # nothing is written, and the call after it is none the worse
+    p = Problem([700, 90, 0], T, Hq, Hkv, 64, 64, fp8, tree=True, q_lens=[0, 0, 0])
+    o, lse = run(p)
+    assert torch.all(o == 5.0) and torch.all(lse == 6.0)
+    p = Problem([700, 90, 0], T, Hq, Hkv, 64, 64, fp8, tree=True, q_lens=[0, T, 0])
+    p.check(*run(p))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 7, 30])
+def test_a_zero_value_scale_gives_zeros(T, fp8):
+    p = Problem([300, 20], T, 2, 1, 64, 32, fp8, tree=True)
+    if fp8:
+        p.scale[1].zero_()
+    else:
+        p.cache[1].zero_()
+    o, lse = run(p)
+    assert torch.all(o == 0) and torch.isfinite(lse).all()
